@@ -503,6 +503,127 @@ int echo_mla_decode(int B, int k, const uint16_t* q, const int32_t* sel_slot, co
                     float scale, float* out, float* lse, int32_t* status, echo_stream_t stream);
 
 /*
+ * Attention over a paged latent cache (multi-head latent attention in its
+ * absorbed form, as echo_mla_decode; the pages give no formula).  The cache is
+ * a pool of 576-dim bf16 rows in pages; a table names each page's place:
+ *   token t of request b is token row g = tok_off[b] + t; with
+ *   e = page_tab[g / page], its cache row is b * req_rows + e * page + g % page;
+ *   e < 0: the token has no row (it was evicted or never recalled) and nothing
+ *   attends to it.
+ * page_tab [ceil(n_tokens / page)] int32 device; kv [kv_rows, 576] bf16 device,
+ * 16-byte aligned, kv_rows > 0; page >= 1 (any number).  Two requests may share
+ * pages.  req_rows = 0: one pool for every request.  req_rows > 0: each request
+ * has its own kv rows [b * req_rows, (b+1) * req_rows), B * req_rows <= kv_rows:
+ * with page = 1, page_tab = echo_cache.tok2slot, kv = dev_kv and req_rows = C
+ * the cache of this library is such a pool.  A row outside its pool is
+ * treated as absent and sets ECHO_ST_BADDATA.
+ */
+typedef struct echo_pages {
+    const int32_t* page_tab;
+    const void* kv;
+    int64_t kv_rows;
+    int64_t req_rows;
+    int32_t page;
+    int32_t reserved;
+} echo_pages;
+
+#define ECHO_CHUNK_MAX_ROWS (1 << 20) /* rows per call */
+
+/*
+ * Attention of a chunk of new tokens.  Request b's new rows are
+ * [row_off[b], row_off[b+1]) of q (row_off [B+1] int64, device, non-decreasing,
+ * row_off[B] <= n_rows) and sit at the end of its context: with len_b =
+ * tok_end[b] - tok_off[b] tokens (tok_end NULL: the whole region) and n_b rows,
+ * row i is at position p = len_b - n_b + i.  One row per request is decode.
+ * Row i sees the tokens t that have a row and
+ *   sel NULL: t <= p, and, with window > 0, t > p - window or t < sinks (a
+ *     sliding window of `window` tokens, the row's own included, and the first
+ *     `sinks` tokens of the request kept visible; window = 0: every t <= p);
+ *   sel [n_rows, k] int32 (device): the tokens sel lists for the row, any order,
+ *     0 <= t < len_b, an entry listed twice counting twice; entries < 0 are
+ *     padding, entries >= len_b are left out and set ECHO_ST_BADDATA
+ *     (sel_idx of echo_prefill_block is such a list; window and sinks are 0
+ *     and k > 0 then, else k is ignored).
+ * For each row r and head h, over the tokens it sees,
+ *   s_t = scale * sum_{d<576} q[r,h,d] * kv[t,d],
+ *   out[r,h,:] = sum_t softmax(s)_t * kv[t, 0:512], lse[r,h] = log sum_t exp(s_t)
+ *   (out = 0 and lse = -inf for a row that sees nothing).
+ *   q [n_rows,heads,576] bf16 (as uint16 bits, 16-byte aligned), 1 <= heads <=
+ *   ECHO_MLA_HEADS; out [n_rows,heads,512] bf16 (16-byte aligned), lse
+ *   [n_rows,heads] f32; scale > 0 and finite.  Rows outside every request are left as
+ *   they were.  A request with more rows than tokens, or inconsistent token
+ *   bounds: its rows see nothing; inconsistent row bounds: its rows are left
+ *   as they were; both set ECHO_ST_BADDATA.
+ *   A cache row that some row of the call sees must be finite; rows that none
+ *   sees are not read.
+ * Scores and sums are fp32; the softmax weights enter the value sum rounded to
+ * bf16.  ws: echo_mla_chunk_workspace_size(n_rows, heads, B) bytes of device
+ * memory, 256-byte aligned, whose contents need not be kept between calls;
+ * calls that may run at the same time need their own.
+ * Errors: ECHO_EINVAL (sizes, NULL or misaligned pointers, a small workspace),
+ * ECHO_EUNSUPPORTED (B > ECHO_MAX_REQUESTS, heads > ECHO_MLA_HEADS, n_rows >
+ * ECHO_CHUNK_MAX_ROWS), ECHO_ECUDA.  n_rows = 0: nothing is enqueued.
+ */
+size_t echo_mla_chunk_workspace_size(int64_t n_rows, int heads, int B);
+int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q,
+                   const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_pages* pages,
+                   const int32_t* sel, int k, int64_t window, int64_t sinks, float scale, uint16_t* out, float* lse,
+                   void* ws, size_t ws_bytes, int32_t* status, echo_stream_t stream);
+
+/*
+ * The attention weight each cached token receives, accumulated: with the rows,
+ * pages, window and sinks of echo_mla_chunk (no selections) and its lse,
+ *   mass_out[g] = decay * mass[g] + sum over the rows r of the request that see
+ *     token g, and their heads h, of exp(s_{r,h,g} - lse[r,h])
+ * for every token row g of every request (tok_off[b] <= g < tok_end[b]; a token
+ * without a cache row, or that no row sees, only decays); other entries of
+ * mass_out are left as they were.  mass and mass_out [n_tokens] f32 may be the
+ * same array; decay is finite and >= 0, and with decay = 0 mass is not read.
+ * A row whose lse is -inf adds nothing.  Everything is fp32 and summed in a fixed
+ * order.  Limits and errors as echo_mla_chunk, with no workspace.
+ */
+int echo_mla_mass(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q, const float* lse,
+                  const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_pages* pages,
+                  int64_t window, int64_t sinks, float scale, const float* mass, float* mass_out, float decay,
+                  int32_t* status, echo_stream_t stream);
+
+/*
+ * Eviction by accumulated attention weight: the victims of each request's cache
+ * (slot2tok [B*C] as in echo_cache, any C >= 1) when it has to shrink to `keep`
+ * resident tokens.  A slot with slot2tok >= 0 holds a resident.  Of the
+ * residents outside the request's first `sinks` and last `recent` tokens, the
+ * max(0, residents - keep) with the lowest mass[tok_off[b] + token] are the
+ * victims (all of them when they are fewer); equal masses: the lower token.
+ *   evict_slot, evict_tok [B,C] int32: the victims' slots, ascending, and the
+ *   token of each, -1 behind them; evict_cnt [B] int32: how many.
+ * -0 counts as +0; a NaN mass sets ECHO_ST_NAN and counts as heavier than
+ * +inf.  A slot2tok entry at or past the request's
+ * end is no resident and sets ECHO_ST_BADDATA; inconsistent token bounds give no
+ * victims and ECHO_ST_BADDATA.  The call changes no table; echo_cache_release
+ * does.  mass [n_tokens] f32.  keep, sinks, recent >= 0.
+ * Errors: ECHO_EINVAL (sizes, NULL pointers), ECHO_EUNSUPPORTED
+ * (B > ECHO_MAX_REQUESTS, C > 524288), ECHO_ECUDA.
+ */
+int echo_evict_select(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens,
+                      const int32_t* slot2tok, int C, const float* mass, int64_t keep, int64_t sinks, int64_t recent,
+                      int32_t* evict_tok, int32_t* evict_slot, int32_t* evict_cnt, int32_t* status,
+                      echo_stream_t stream);
+
+/*
+ * Releases tokens from the cache: for each entry of tok [B,m] int32 (request-local,
+ * -1 padding; evict_tok with m = C is such a list) that is resident, its two
+ * table entries become -1, its slot's free bit is set and, with mass (may be
+ * NULL), mass[tok_off[b] + token] = 0.  Its bytes stay; nothing is written back
+ * (the host pool holds every row).  Entries that are not resident change
+ * nothing (a token listed twice is released once); entries at or past the request's end
+ * set ECHO_ST_BADDATA.  Enqueue between steps, on the step's stream, as
+ * echo_append_tokens, whose new token then finds a free slot.
+ * Errors: ECHO_EINVAL, ECHO_EUNSUPPORTED, cache errors as echo_cache_step.
+ */
+int echo_cache_release(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const int32_t* tok,
+                       int m, const echo_cache* cache, float* mass, int32_t* status, echo_stream_t stream);
+
+/*
  * Cross-layer early set [page "ECHO Guide: KV Offloading for Native Sparse Attention",
  * section "Intra-Query Prefetching: Layer-to-Layer Pipeline": layers l+1 and
  * l+2 select mostly what layer l selected; reading: layer l+1's early set is

@@ -27,9 +27,10 @@ TOPK_CACHED_MAX_SLOTS = 32768  # C limit of echo_topk_select_cached and of the c
 CAND_CAP = 16384             # candidate-list entries per request top-k keeps in shared memory
 EARLY_FETCH_BLOCKS = 24      # CTAs of the early-fetch and late-recall kernels
 
-EXPORTS = ("echo_above_words", "echo_append_tokens", "echo_cache_step", "echo_cache_step_resolved",
+EXPORTS = ("echo_above_words", "echo_append_tokens", "echo_cache_release", "echo_cache_step", "echo_cache_step_resolved",
            "echo_debug_stall_epilogue", "echo_device_sm_count",
-           "echo_early_fetch", "echo_host_device_alias", "echo_index_scores", "echo_index_scores_cands", "echo_mla_decode", "echo_pool_above", "echo_pool_select",
+           "echo_early_fetch", "echo_evict_select", "echo_host_device_alias", "echo_index_scores", "echo_index_scores_cands", "echo_mla_chunk",
+           "echo_mla_chunk_workspace_size", "echo_mla_decode", "echo_mla_mass", "echo_pool_above", "echo_pool_select",
            "echo_pool_slots", "echo_prefill_block",
            "echo_prefill_block_static", "echo_prefill_scores", "echo_prefill_workspace_size", "echo_quantize_q", "echo_seed_early",
            "echo_topk_select", "echo_topk_select_cached", "echo_topk_select_cands")
@@ -47,6 +48,11 @@ class EchoCacheStruct(ctypes.Structure):
 class EchoCandsStruct(ctypes.Structure):
     _fields_ = [("key", _vp), ("idx", _vp), ("cnt", _vp), ("cut", _vp), ("cap", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class EchoPagesStruct(ctypes.Structure):
+    _fields_ = [("page_tab", _vp), ("kv", _vp), ("kv_rows", ctypes.c_int64), ("req_rows", ctypes.c_int64),
+                ("page", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class EchoError(RuntimeError):
@@ -100,6 +106,19 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                                       _vp, _vp, _vp, _vp, i32]
         L.echo_mla_decode.restype = i32
         L.echo_mla_decode.argtypes = [i32, i32, _vp, _vp, _vp, i64, f32, _vp, _vp, _vp, _vp]
+        pages = ctypes.POINTER(EchoPagesStruct)
+        L.echo_mla_chunk_workspace_size.restype = ctypes.c_size_t
+        L.echo_mla_chunk_workspace_size.argtypes = [i64, i32, i32]
+        L.echo_mla_chunk.restype = i32
+        L.echo_mla_chunk.argtypes = [i32, _vp, i64, i32, _vp, _vp, _vp, i64, pages, _vp, i32, i64, i64, f32, _vp, _vp,
+                                     _vp, ctypes.c_size_t, _vp, _vp]
+        L.echo_mla_mass.restype = i32
+        L.echo_mla_mass.argtypes = [i32, _vp, i64, i32, _vp, _vp, _vp, _vp, i64, pages, i64, i64, f32, _vp, _vp, f32,
+                                    _vp, _vp]
+        L.echo_evict_select.restype = i32
+        L.echo_evict_select.argtypes = [i32, _vp, _vp, i64, _vp, i32, _vp, i64, i64, i64, _vp, _vp, _vp, _vp, _vp]
+        L.echo_cache_release.restype = i32
+        L.echo_cache_release.argtypes = [i32, _vp, _vp, i64, _vp, i32, ctypes.POINTER(EchoCacheStruct), _vp, _vp, _vp]
         L.echo_pool_above.restype = i32
         L.echo_pool_above.argtypes = [i32, _vp, _vp, i64, _vp, ctypes.POINTER(EchoCacheStruct), _vp, _vp, _vp]
         L.echo_pool_select.restype = i32
@@ -345,6 +364,123 @@ def mla_decode(q, sel_slot, dev_kv, C, scale, out, lse, status, stream=None):
     B, k = sel_slot.shape
     _check("echo_mla_decode", load().echo_mla_decode(
         int(B), int(k), _ptr(q), _ptr(sel_slot), _ptr(dev_kv), int(C), float(scale), _ptr(out), _ptr(lse),
+        _ptr(status), _stream(stream)))
+
+
+def _expect(call, name, t, dtype, shape):
+    # the layouts the C ABI takes: contiguous tensors of the given type, on the current device
+    if (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
+            or t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
+        raise ValueError(f"{call}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current "
+                         f"CUDA device, not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+class KVPages:
+    """A paged latent cache for mla_chunk / mla_mass (an echo_pages): token row g of the requests
+    (tok_off) is cache row page_tab[g // page] * page + g % page of kv [rows, 576] bf16 (< 0: no
+    row).  req_rows > 0: each request has that many kv rows of its own and its pages count from
+    there.  Keeps the tensors alive; the table may change between calls, in place."""
+
+    def __init__(self, page_tab: torch.Tensor, kv: torch.Tensor, page: int, req_rows: int = 0):
+        if page < 1 or req_rows < 0:
+            raise ValueError("KVPages: page >= 1 and req_rows >= 0")
+        _expect("KVPages", "page_tab", page_tab, torch.int32, (page_tab.numel(),))
+        _expect("KVPages", "kv", kv, torch.bfloat16, (kv.shape[0], MLA_DQK))
+        self.page_tab, self.kv, self.page, self.req_rows = page_tab, kv, int(page), int(req_rows)
+        s = EchoPagesStruct()
+        s.page_tab, s.kv, s.kv_rows = _ptr(page_tab), _ptr(kv), kv.shape[0]
+        s.req_rows, s.page, s.reserved = self.req_rows, self.page, 0
+        self.struct = s
+
+    @classmethod
+    def of_cache(cls, cache: "LayerCache") -> "KVPages":
+        """The slots of a LayerCache as pages of one row (a token that is not resident has no row)."""
+        return cls(cache.tok2slot, cache.dev_kv, 1, cache.C)
+
+    def check(self, call, n_tokens):
+        if self.page_tab.numel() * self.page < n_tokens:
+            raise ValueError(f"{call}: page_tab has {self.page_tab.numel()} pages of {self.page}, fewer than {n_tokens} "
+                             "token rows need")
+
+
+def mla_chunk_workspace_size(n_rows: int, heads: int, B: int) -> int:
+    return int(load().echo_mla_chunk_workspace_size(int(n_rows), int(heads), int(B)))
+
+
+def _check_chunk(call, row_off, q, tok_off, n_tokens, pages, lse, status, tok_end):
+    B = tok_off.shape[0] - 1
+    n, heads = q.shape[0], q.shape[1]
+    _expect(call, "row_off", row_off, torch.int64, (B + 1,))
+    _expect(call, "tok_off", tok_off, torch.int64, (B + 1,))
+    _expect(call, "q", q, torch.bfloat16, (n, heads, MLA_DQK))
+    _expect(call, "lse", lse, torch.float32, (n, heads))
+    _expect(call, "status", status, torch.int32, (1,))
+    if tok_end is not None:
+        _expect(call, "tok_end", tok_end, torch.int64, (B,))
+    pages.check(call, n_tokens)
+    return B, n, heads
+
+
+def mla_chunk(row_off, q, tok_off, n_tokens, pages, scale, out, lse, ws, status, tok_end=None, window=0, sinks=0,
+              sel=None, stream=None):
+    """echo_mla_chunk: attention of each request's new rows q [n,heads,576] bf16 (row_off [B+1], at
+    the end of its context) over the cache `pages` (a KVPages): causal; window > 0: the last
+    `window` tokens and the first `sinks`; sel [n,k] int32: the tokens listed for each row -> out
+    [n,heads,512] bf16, lse [n,heads] f32.  ws: uint8, mla_chunk_workspace_size(n, heads, B)."""
+    B, n, heads = _check_chunk("mla_chunk", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end)
+    _expect("mla_chunk", "out", out, torch.bfloat16, (n, heads, MLA_DV))
+    k = 0
+    if sel is not None:
+        k = sel.shape[-1]
+        _expect("mla_chunk", "sel", sel, torch.int32, (n, k))
+    _check("echo_mla_chunk", load().echo_mla_chunk(
+        B, _ptr(row_off), n, heads, _ptr(q), _ptr(tok_off), _ptr(tok_end), int(n_tokens),
+        ctypes.byref(pages.struct), _ptr(sel), k, int(window), int(sinks), float(scale), _ptr(out), _ptr(lse),
+        _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+
+
+def mla_mass(row_off, q, lse, tok_off, n_tokens, pages, scale, mass, mass_out, status, decay=1.0, tok_end=None,
+             window=0, sinks=0, stream=None):
+    """echo_mla_mass: mass_out [n_tokens] f32 = decay * mass + the attention weight each token
+    receives from the rows of an mla_chunk call (the same q, pages, window and sinks, and its lse),
+    summed over rows and heads.  mass_out may be mass."""
+    B, n, heads = _check_chunk("mla_mass", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end)
+    _expect("mla_mass", "mass", mass, torch.float32, (n_tokens,))
+    _expect("mla_mass", "mass_out", mass_out, torch.float32, (n_tokens,))
+    _check("echo_mla_mass", load().echo_mla_mass(
+        B, _ptr(row_off), n, heads, _ptr(q), _ptr(lse), _ptr(tok_off), _ptr(tok_end), int(n_tokens),
+        ctypes.byref(pages.struct), int(window), int(sinks), float(scale), _ptr(mass), _ptr(mass_out), float(decay),
+        _ptr(status), _stream(stream)))
+
+
+def evict_select(tok_off, n_tokens, slot2tok, mass, keep, evict_tok, evict_slot, evict_cnt, status, sinks=0, recent=0,
+                 tok_end=None, stream=None):
+    """echo_evict_select: the victims of each request's cache (slot2tok [B*C] or [B,C]) when it has to
+    shrink to `keep` residents: those of the lowest mass [n_tokens], the first `sinks` and last
+    `recent` tokens spared -> evict_tok / evict_slot [B,C] (ascending slots, -1 behind), evict_cnt [B]."""
+    B = tok_off.shape[0] - 1
+    C = slot2tok.numel() // B
+    _expect("evict_select", "tok_off", tok_off, torch.int64, (B + 1,))
+    _expect("evict_select", "slot2tok", slot2tok, torch.int32, (B * C,) if slot2tok.dim() == 1 else (B, C))
+    _expect("evict_select", "mass", mass, torch.float32, (n_tokens,))
+    _expect("evict_select", "evict_tok", evict_tok, torch.int32, (B, C))
+    _expect("evict_select", "evict_slot", evict_slot, torch.int32, (B, C))
+    _expect("evict_select", "evict_cnt", evict_cnt, torch.int32, (B,))
+    _check("echo_evict_select", load().echo_evict_select(
+        B, _ptr(tok_off), _ptr(tok_end), int(n_tokens), _ptr(slot2tok), C, _ptr(mass), int(keep), int(sinks),
+        int(recent), _ptr(evict_tok), _ptr(evict_slot), _ptr(evict_cnt), _ptr(status), _stream(stream)))
+
+
+def cache_release(tok_off, n_tokens, tok, cache, status, mass=None, tok_end=None, stream=None):
+    """echo_cache_release: frees the slots of the listed tokens (tok [B,m] int32, -1 padding) that are
+    resident in `cache`; with mass [n_tokens], their masses become 0."""
+    B = tok_off.shape[0] - 1
+    m = tok.shape[-1]
+    _expect("cache_release", "tok", tok, torch.int32, (B, m))
+    if mass is not None:
+        _expect("cache_release", "mass", mass, torch.float32, (n_tokens,))
+    _check("echo_cache_release", load().echo_cache_release(
+        B, _ptr(tok_off), _ptr(tok_end), int(n_tokens), _ptr(tok), m, ctypes.byref(cache.struct), _ptr(mass),
         _ptr(status), _stream(stream)))
 
 

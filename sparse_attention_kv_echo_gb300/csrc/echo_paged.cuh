@@ -1,0 +1,147 @@
+// echo_paged.cuh -- what the calls over a paged latent cache share: where a
+// token's cache row is, and which tokens a row sees.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "echo_common.cuh"
+#include "echo_internal.h"
+
+namespace echo {
+
+constexpr int kLatDqk = ECHO_MLA_DQK;            // 576
+constexpr int kLatDv = ECHO_MLA_DV;              // 512
+constexpr int64_t kLatRowBytes = kLatDqk * 2;    // 1152
+
+// The arguments of a chunk call that the kernels read (device pointers).
+struct ChunkArgs {
+    int B;
+    int heads;
+    int64_t n_rows;
+    const int64_t* row_off;
+    const int64_t* tok_off;
+    const int64_t* tok_end;
+    int64_t n_tokens;
+    const int32_t* page_tab;
+    const uint8_t* kv;
+    int64_t kv_rows;
+    int64_t req_rows;
+    uint32_t page;
+    const int32_t* sel;
+    int k;
+    int64_t window;
+    int64_t sinks;
+    const uint16_t* q;
+    float scale;
+    int32_t* status;
+};
+
+// Host checks of the arguments the chunk calls share.
+inline int check_chunk(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q,
+                       const int64_t* tok_off, int64_t n_tokens, const echo_pages* pg, int64_t window, int64_t sinks,
+                       float scale, const int32_t* status) {
+    if (B <= 0 || n_rows < 0 || heads <= 0 || n_tokens < 0 || window < 0 || sinks < 0) return ECHO_EINVAL;
+    if (B > ECHO_MAX_REQUESTS || heads > ECHO_MLA_HEADS || n_rows > ECHO_CHUNK_MAX_ROWS) return ECHO_EUNSUPPORTED;
+    if (!row_off || (n_rows > 0 && !q) || !tok_off || !pg || !status) return ECHO_EINVAL;
+    if ((n_tokens > 0 && !pg->page_tab) || !pg->kv || pg->page < 1 || pg->kv_rows <= 0 || pg->req_rows < 0) return ECHO_EINVAL;
+    if (pg->req_rows > pg->kv_rows / B) return ECHO_EINVAL;
+    if (!(scale > 0.f) || scale > 3.4028234e38f) return ECHO_EINVAL;
+    if (!is_aligned(q, 16) || !is_aligned(pg->kv, 16)) return ECHO_EINVAL;
+    return ECHO_OK;
+}
+
+inline ChunkArgs chunk_args(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q,
+                            const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_pages* pg,
+                            const int32_t* sel, int k, int64_t window, int64_t sinks, float scale, int32_t* status) {
+    ChunkArgs a;
+    a.B = B;
+    a.heads = heads;
+    a.n_rows = n_rows;
+    a.row_off = row_off;
+    a.tok_off = tok_off;
+    a.tok_end = tok_end;
+    a.n_tokens = n_tokens;
+    a.page_tab = pg->page_tab;
+    a.kv = static_cast<const uint8_t*>(pg->kv);
+    a.kv_rows = pg->kv_rows;
+    a.req_rows = pg->req_rows;
+    a.page = static_cast<uint32_t>(pg->page);
+    a.sel = sel;
+    a.k = sel ? k : 0;
+    a.window = window;
+    a.sinks = sinks;
+    a.q = q;
+    a.scale = scale;
+    a.status = status;
+    return a;
+}
+
+// Rows [r0, r0 + n) of request b, its token rows from off on and its length.
+// False: the row bounds are inconsistent (n = 0).  Inconsistent token bounds,
+// more rows than tokens or more tokens than an int32 index holds leave len = 0.
+__device__ __forceinline__ bool chunk_request(const ChunkArgs& a, int b, int64_t* r0, int64_t* n, int64_t* off,
+                                              int64_t* len) {
+    const int64_t lo = a.row_off[b], hi = a.row_off[b + 1];
+    int64_t t0, t1;
+    bool ok = seg_bounds(a.tok_off, a.tok_end, a.n_tokens, b, &t0, &t1);
+    *off = t0;
+    *len = t1 - t0;
+    *r0 = lo;
+    *n = hi - lo;
+    if (lo < 0 || hi < lo || hi > a.n_rows) {
+        *r0 = 0;
+        *n = 0;
+        set_status(a.status, ECHO_ST_BADDATA);
+        return false;
+    }
+    if (hi > lo && (!ok || *len < *n || *len > 0x7FFFFFFF)) {
+        set_status(a.status, ECHO_ST_BADDATA);
+        *len = 0;
+    }
+    return true;
+}
+
+// Where a request's tokens are: its pool's first row and the page position of its token 0.
+struct PageView {
+    const int32_t* tab;    // the table entry that holds token 0
+    uint32_t shift;        // token 0's offset in its page
+    int64_t base;          // first row of the request's pool
+    int64_t rows;          // rows of the pool
+};
+
+__device__ __forceinline__ PageView page_view(const ChunkArgs& a, int b, int64_t off) {
+    PageView v;
+    const int64_t e = off / a.page;
+    v.tab = a.page_tab + e;
+    v.shift = static_cast<uint32_t>(off - e * a.page);
+    v.base = a.req_rows ? b * a.req_rows : 0;
+    v.rows = a.req_rows ? a.req_rows : a.kv_rows;
+    return v;
+}
+
+// Cache row of token t (t < 2^31), -1 when it has none.  *bad: its table entry leaves the pool.
+__device__ __forceinline__ int64_t token_row(const ChunkArgs& a, const PageView& v, uint32_t t, bool* bad) {
+    uint32_t e = 0, r = 0;
+    if (a.page == 1) {
+        e = t;
+    } else {
+        const uint64_t x = static_cast<uint64_t>(v.shift) + t;  // page may be near 2^31
+        if (x < 0xFFFFFFFFull) {
+            e = static_cast<uint32_t>(x) / a.page;
+            r = static_cast<uint32_t>(x) - e * a.page;
+        } else {
+            e = static_cast<uint32_t>(x / a.page);
+            r = static_cast<uint32_t>(x - static_cast<uint64_t>(e) * a.page);
+        }
+    }
+    const int32_t p = v.tab[e];
+    if (p < 0) return -1;
+    const int64_t row = static_cast<int64_t>(p) * a.page + r;
+    if (row >= v.rows) {
+        *bad = true;
+        return -1;
+    }
+    return v.base + row;
+}
+
+}  // namespace echo

@@ -212,3 +212,68 @@ def test_pool_layer_refuses_append():
     lay.tok_end, lay.pool_slots = torch.zeros(1, dtype=torch.int64), 64
     with pytest.raises(ValueError):
         lay.append(torch.zeros((1, 128)), torch.zeros((1, 576)))
+
+
+def test_paged_calls_check_their_arguments(L):
+    """echo_mla_chunk, echo_mla_mass, echo_evict_select and echo_cache_release refuse before any CUDA call."""
+    from sparse_attention_kv_echo_gb300 import lib
+    v = ctypes.c_void_p
+    d = v(0x1000)
+
+    def pages(**kw):
+        p = lib.EchoPagesStruct()
+        p.page_tab, p.kv, p.kv_rows, p.req_rows, p.page = 0x1000, 0x1000, 64, 0, 16
+        for k, x in kw.items():
+            setattr(p, k, x)
+        return ctypes.byref(p)
+
+    def chunk(B=1, row_off=d, n_rows=2, heads=16, q=d, tok_off=d, n=10, pg=None, sel=None, k=0, window=0, sinks=0,
+              scale=0.1, out=d, lse=d, ws=d, short=0, status=d):
+        size = lib.mla_chunk_workspace_size(max(n_rows, 1), max(heads, 1), max(B, 1))
+        return L.echo_mla_chunk(B, row_off, n_rows, heads, q, tok_off, None, n, pages() if pg is None else pg, sel, k,
+                                window, sinks, scale, out, lse, ws, size - short, status, None)
+    inf, nan = float("inf"), float("nan")
+    for bad in (dict(B=0), dict(row_off=None), dict(n_rows=-1), dict(heads=0), dict(q=None), dict(tok_off=None),
+                dict(n=-1), dict(window=-1), dict(sinks=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=inf),
+                dict(scale=nan), dict(out=None), dict(lse=None), dict(ws=None), dict(short=1), dict(status=None),
+                dict(q=v(0x1008)), dict(out=v(0x1004)), dict(ws=v(0x1010)), dict(pg=pages(page=0)),
+                dict(pg=pages(page_tab=None)), dict(pg=pages(kv=None)), dict(pg=pages(kv=0x1008)),
+                dict(pg=pages(kv_rows=0)), dict(pg=pages(req_rows=-1)), dict(pg=pages(req_rows=65)),
+                dict(B=3, pg=pages(req_rows=22)), dict(sel=d, k=0), dict(sel=d, k=-4), dict(sel=d, k=4, window=3),
+                dict(sel=d, k=4, sinks=1)):
+        assert chunk(**bad) == lib.ECHO_EINVAL, bad
+    for big in (dict(B=lib.MAX_REQUESTS + 1), dict(heads=129), dict(n_rows=(1 << 20) + 1)):
+        assert chunk(**big) == lib.ECHO_EUNSUPPORTED, big
+    assert chunk(n_rows=0, q=None, out=None, lse=None) == lib.ECHO_OK
+    assert lib.mla_chunk_workspace_size(-1, 16, 1) == 0 and lib.mla_chunk_workspace_size(4, 0, 1) == 0
+
+    def mass(lse=d, m=d, out=d, decay=0.5, n=10, scale=0.1, n_rows=2):
+        return L.echo_mla_mass(1, d, n_rows, 16, d, lse, d, None, n, pages(), 0, 0, scale, m, out, decay, d, None)
+    for bad in (dict(lse=None), dict(m=None), dict(out=None), dict(decay=-0.1), dict(decay=nan), dict(decay=inf),
+                dict(n=-1), dict(scale=0.0), dict(n_rows=-1)):
+        assert mass(**bad) == lib.ECHO_EINVAL, bad
+    assert mass(n=0, m=None, out=None) == lib.ECHO_OK
+
+    def evict(B=1, off=d, n=10, s2t=d, C=64, m=d, keep=1, sinks=0, recent=0, et=d, es=d, ec=d, st=d):
+        return L.echo_evict_select(B, off, None, n, s2t, C, m, keep, sinks, recent, et, es, ec, st, None)
+    for bad in (dict(B=0), dict(off=None), dict(n=-1), dict(s2t=None), dict(C=0), dict(m=None), dict(keep=-1),
+                dict(sinks=-1), dict(recent=-1), dict(et=None), dict(es=None), dict(ec=None), dict(st=None)):
+        assert evict(**bad) == lib.ECHO_EINVAL, bad
+    assert evict(B=lib.MAX_REQUESTS + 1) == lib.ECHO_EUNSUPPORTED
+    assert evict(C=(1 << 19) + 1) == lib.ECHO_EUNSUPPORTED
+
+    c = lib.EchoCacheStruct()
+    for f, _ in lib.EchoCacheStruct._fields_:
+        if f not in ("row_bytes", "C", "reserved"):
+            setattr(c, f, 0x1000)
+    c.row_bytes, c.C = 1152, 64
+    cache = ctypes.byref(c)
+
+    def release(B=1, off=d, n=10, tok=d, m=4, cache=cache, st=d):
+        return L.echo_cache_release(B, off, None, n, tok, m, cache, None, st, None)
+    for bad in (dict(B=0), dict(off=None), dict(n=-1), dict(tok=None), dict(m=-1), dict(cache=None), dict(st=None)):
+        assert release(**bad) == lib.ECHO_EINVAL, bad
+    assert release(B=lib.MAX_REQUESTS + 1) == lib.ECHO_EUNSUPPORTED
+    assert release(m=0, tok=None) == lib.ECHO_OK
+    c.C = 48
+    assert release() == lib.ECHO_ECAPACITY
