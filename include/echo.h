@@ -580,12 +580,16 @@ int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int heads, con
  * mass_out are left as they were.  mass and mass_out [n_tokens] f32 may be the
  * same array; decay is finite and >= 0, and with decay = 0 mass is not read.
  * A row whose lse is -inf adds nothing.  Everything is fp32 and summed in a fixed
- * order.  Limits and errors as echo_mla_chunk, with no workspace.
+ * order.  ws: echo_mla_mass_workspace_size(n_tokens, B) bytes, as
+ * echo_mla_chunk's.  Limits and errors as echo_mla_chunk; n_tokens >
+ * ECHO_MASS_MAX_TOKENS: ECHO_EUNSUPPORTED.
  */
+#define ECHO_MASS_MAX_TOKENS (1ll << 36)
+size_t echo_mla_mass_workspace_size(int64_t n_tokens, int B);
 int echo_mla_mass(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q, const float* lse,
                   const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_pages* pages,
                   int64_t window, int64_t sinks, float scale, const float* mass, float* mass_out, float decay,
-                  int32_t* status, echo_stream_t stream);
+                  void* ws, size_t ws_bytes, int32_t* status, echo_stream_t stream);
 
 /*
  * Eviction by accumulated attention weight: the victims of each request's cache

@@ -30,7 +30,8 @@ EARLY_FETCH_BLOCKS = 24      # CTAs of the early-fetch and late-recall kernels
 EXPORTS = ("echo_above_words", "echo_append_tokens", "echo_cache_release", "echo_cache_step", "echo_cache_step_resolved",
            "echo_debug_stall_epilogue", "echo_device_sm_count",
            "echo_early_fetch", "echo_evict_select", "echo_host_device_alias", "echo_index_scores", "echo_index_scores_cands", "echo_mla_chunk",
-           "echo_mla_chunk_workspace_size", "echo_mla_decode", "echo_mla_mass", "echo_pool_above", "echo_pool_select",
+           "echo_mla_chunk_workspace_size", "echo_mla_decode", "echo_mla_mass",
+           "echo_mla_mass_workspace_size", "echo_pool_above", "echo_pool_select",
            "echo_pool_slots", "echo_prefill_block",
            "echo_prefill_block_static", "echo_prefill_scores", "echo_prefill_workspace_size", "echo_quantize_q", "echo_seed_early",
            "echo_topk_select", "echo_topk_select_cached", "echo_topk_select_cands")
@@ -114,7 +115,9 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                                      _vp, ctypes.c_size_t, _vp, _vp]
         L.echo_mla_mass.restype = i32
         L.echo_mla_mass.argtypes = [i32, _vp, i64, i32, _vp, _vp, _vp, _vp, i64, pages, i64, i64, f32, _vp, _vp, f32,
-                                    _vp, _vp]
+                                    _vp, ctypes.c_size_t, _vp, _vp]
+        L.echo_mla_mass_workspace_size.restype = ctypes.c_size_t
+        L.echo_mla_mass_workspace_size.argtypes = [i64, i32]
         L.echo_evict_select.restype = i32
         L.echo_evict_select.argtypes = [i32, _vp, _vp, i64, _vp, i32, _vp, i64, i64, i64, _vp, _vp, _vp, _vp, _vp]
         L.echo_cache_release.restype = i32
@@ -439,18 +442,29 @@ def mla_chunk(row_off, q, tok_off, n_tokens, pages, scale, out, lse, ws, status,
         _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
 
 
+def mla_mass_workspace_size(n_tokens: int, B: int) -> int:
+    return int(load().echo_mla_mass_workspace_size(int(n_tokens), int(B)))
+
+
 def mla_mass(row_off, q, lse, tok_off, n_tokens, pages, scale, mass, mass_out, status, decay=1.0, tok_end=None,
-             window=0, sinks=0, stream=None):
+             window=0, sinks=0, ws=None, stream=None):
     """echo_mla_mass: mass_out [n_tokens] f32 = decay * mass + the attention weight each token
     receives from the rows of an mla_chunk call (the same q, pages, window and sinks, and its lse),
-    summed over rows and heads.  mass_out may be mass."""
+    summed over rows and heads.  mass_out may be mass.  ws: uint8, mla_mass_workspace_size(n_tokens,
+    B) (None: one is taken from torch's allocator for the call)."""
     B, n, heads = _check_chunk("mla_mass", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end)
     _expect("mla_mass", "mass", mass, torch.float32, (n_tokens,))
     _expect("mla_mass", "mass_out", mass_out, torch.float32, (n_tokens,))
+    if ws is None:
+        ws = torch.empty(mla_mass_workspace_size(n_tokens, B), dtype=torch.uint8, device=q.device)
+        if isinstance(stream, torch.cuda.Stream):
+            ws.record_stream(stream)
+        elif stream is not None:
+            raise ValueError("mla_mass: a stream given by its handle needs ws")
     _check("echo_mla_mass", load().echo_mla_mass(
         B, _ptr(row_off), n, heads, _ptr(q), _ptr(lse), _ptr(tok_off), _ptr(tok_end), int(n_tokens),
         ctypes.byref(pages.struct), int(window), int(sinks), float(scale), _ptr(mass), _ptr(mass_out), float(decay),
-        _ptr(status), _stream(stream)))
+        _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
 
 
 def evict_select(tok_off, n_tokens, slot2tok, mass, keep, evict_tok, evict_slot, evict_cnt, status, sinks=0, recent=0,

@@ -114,26 +114,6 @@ __device__ __forceinline__ int tiles_of(int nv) { return (nv + kTok - 1) / kTok;
 // ---------------------------------------------------------------- plan
 constexpr int kPT = 1024;
 
-__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* scratch, int64_t* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) scratch[warp] = x;
-    __syncthreads();
-    int64_t before = 0, sum = 0;
-    for (int w = 0; w < kPT / 32; ++w) {
-        if (w < warp) before += scratch[w];
-        sum += scratch[w];
-    }
-    __syncthreads();
-    *total = sum;
-    return before + x - v;
-}
-
 // One block: the groups of every request in order, with their costs summed.
 __global__ void __launch_bounds__(kPT) chunk_plan_kernel(ChunkArgs a, Plan plan) {
     __shared__ uint32_t goff[ECHO_MAX_REQUESTS + 1];
@@ -197,7 +177,7 @@ __global__ void __launch_bounds__(kPT) chunk_plan_kernel(ChunkArgs a, Plan plan)
             cost = kOver + tiles_of(r.nv);
         }
         int64_t total;
-        const int64_t at = sum + block_scan64(cost, scratch64, &total);
+        const int64_t at = sum + block_scan64<kPT>(cost, scratch64, &total);
         if (g < groups) plan.cum[g] = at;
         sum += total;
     }
@@ -210,32 +190,6 @@ __global__ void __launch_bounds__(kPT) chunk_plan_kernel(ChunkArgs a, Plan plan)
             max(static_cast<int64_t>(1), min(static_cast<int64_t>(plan.clusters), sum / kMinUnits)));
         *plan.head = h;
     }
-}
-
-// ---------------------------------------------------------------- the shares
-__device__ __forceinline__ int64_t share_start(const PlanHead& h, int i) { return h.total * i / h.parts; }
-// The cluster whose share holds unit u.
-__device__ __forceinline__ int share_of(const PlanHead& h, int64_t u) {
-    int i = static_cast<int>(min(static_cast<int64_t>(h.parts) - 1, u * h.parts / h.total));
-    while (i + 1 < h.parts && share_start(h, i + 1) <= u) ++i;
-    while (share_start(h, i) > u) --i;
-    return i;
-}
-
-// The last group whose units start at or before u (a warp together).
-__device__ __forceinline__ int find_group(const int64_t* cum, int groups, int64_t u) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, n = groups;  // cum[lo] <= u; the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const int at = lo + lane * step;
-        const bool le = lane * step < n && cum[at] <= u;
-        const int k = __popc(__ballot_sync(0xffffffffu, le));  // le is true for a prefix of the lanes
-        const int end = lo + n;
-        lo += (k - 1) * step;
-        n = min(step, end - lo);
-    }
-    return lo;
 }
 
 // The part of a group that a share holds: tiles [lo, hi) of `tiles`.
@@ -339,8 +293,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     walk.u0 = walk.u1 = 0;
     walk.g = 0;
     if (ci < head.parts) {
-        walk.u0 = share_start(head, ci);
-        walk.u1 = share_start(head, ci + 1);
+        walk.u0 = share_start(head.total, head.parts, ci);
+        walk.u1 = share_start(head.total, head.parts, ci + 1);
     }
     if (warp == 1 && walk.u0 < walk.u1) {
         const int g = find_group(plan.cum, head.groups, walk.u0);
@@ -718,7 +672,7 @@ __global__ void __launch_bounds__(kJT) chunk_join_kernel(ChunkArgs a, Plan plan,
     const int tid = threadIdx.x, i = blockIdx.x + 1;
     const PlanHead head = *plan.head;
     if (i >= head.parts) return;
-    const int64_t u = share_start(head, i);
+    const int64_t u = share_start(head.total, head.parts, i);
     if (tid < 32) {
         const int g = find_group(plan.cum, head.groups, u);
         if (tid == 0) s_group = g;
@@ -727,8 +681,8 @@ __global__ void __launch_bounds__(kJT) chunk_join_kernel(ChunkArgs a, Plan plan,
     const Group g = plan.group[s_group];
     const int64_t c = plan.cum[s_group];
     const int tiles = tiles_of(g.nv);
-    if (u <= c + kOver || share_start(head, i - 1) > c + kOver) return;  // no cut here, or not the group's first
-    const int i0 = i - 1, i1 = share_of(head, c + kOver + tiles - 1);
+    if (u <= c + kOver || share_start(head.total, head.parts, i - 1) > c + kOver) return;  // no cut here, or not the group's first
+    const int i0 = i - 1, i1 = share_of(head.total, head.parts, c + kOver + tiles - 1);
     const int n = i1 - i0 + 1, live = g.rows * a.heads;
     const int m0 = blockIdx.y * kJRows;
     if (m0 >= live) return;
@@ -774,47 +728,6 @@ __global__ void __launch_bounds__(kJT) chunk_join_kernel(ChunkArgs a, Plan plan,
     }
 }
 
-// Pairs of SMs that hold a cluster at once (queried once per device).
-int active_clusters() {
-    static int cache[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    if (cache[dev] == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, chunk_kernel, &cfg) != cudaSuccess || n < 1) {
-            (void)cudaGetLastError();
-            n = sm_count() / 2;
-        }
-        cache[dev] = n < 1 ? 1 : n > kMaxClusters ? kMaxClusters : n;
-    }
-    return cache[dev];
-}
-
-template <class... Args>
-cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace
 }  // namespace echo
 
@@ -841,7 +754,6 @@ extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int
     const ChunkArgs a = chunk_args(B, row_off, n_rows, heads, q, tok_off, tok_end, n_tokens, pages, sel, k, window,
                                    sinks, scale, status);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    ECHO_CUDA_OK(cudaFuncSetAttribute(chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
     const int64_t cap = plan_cap(n_rows, heads, B, sel != nullptr);
     const Layout l = plan_layout(cap);
     uint8_t* const w = static_cast<uint8_t*>(ws);
@@ -851,7 +763,9 @@ extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int
     plan.cum = reinterpret_cast<int64_t*>(w + l.cum);
     plan.part = w + l.part;
     plan.cap = static_cast<int>(cap);
-    plan.clusters = active_clusters();
+    static int cached[64];
+    plan.clusters = cluster2_count(chunk_kernel, kThreads, kSmem, kMaxClusters, cached);
+    if (plan.clusters < 1) return ECHO_ECUDA;
     ECHO_CUDA_OK(prefer_max_shared(chunk_plan_kernel));
     ECHO_CUDA_OK(prefer_max_shared(chunk_join_kernel));
     chunk_plan_kernel<<<1, kPT, 0, s>>>(a, plan);

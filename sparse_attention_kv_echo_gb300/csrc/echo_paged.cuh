@@ -144,4 +144,99 @@ __device__ __forceinline__ int64_t token_row(const ChunkArgs& a, const PageView&
     return v.base + row;
 }
 
+// ---------------------------------------------------------------- shares of a row of units
+// `parts` shares of `total` units (total >= parts): share i is units
+// [share_start(i), share_start(i + 1)).
+__device__ __forceinline__ int64_t share_start(int64_t total, int parts, int i) { return total * i / parts; }
+
+// The share that holds unit u.
+__device__ __forceinline__ int share_of(int64_t total, int parts, int64_t u) {
+    int i = static_cast<int>(min(static_cast<int64_t>(parts) - 1, u * parts / total));
+    while (i + 1 < parts && share_start(total, parts, i + 1) <= u) ++i;
+    while (share_start(total, parts, i) > u) --i;
+    return i;
+}
+
+// The last of n things whose units start at or before u (cum ascending, cum[0] <= u; a warp together).
+__device__ __forceinline__ int find_group(const int64_t* cum, int n, int64_t u) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const bool le = lane * step < n && cum[lo + lane * step] <= u;
+        const int k = __popc(__ballot_sync(0xffffffffu, le));  // le is true for a prefix of the lanes
+        const int end = lo + n;
+        lo += (k - 1) * step;
+        n = min(step, end - lo);
+    }
+    return lo;
+}
+
+// Exclusive prefix sum of a block of NT threads, and its total, in 64 bits.  scratch: [NT / 32].
+template <int NT>
+__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* scratch, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    int64_t before = 0, sum = 0;
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += scratch[w];
+        sum += scratch[w];
+    }
+    __syncthreads();
+    *total = sum;
+    return before + x - v;
+}
+
+// Sets a two-CTA cluster kernel up for `smem` bytes; how many of its clusters the device holds at
+// once, at most `most` (queried once per device: `cached`, zeros at first), 0 on an error.
+template <class Kernel>
+int cluster2_count(Kernel kernel, int threads, uint32_t smem, int most, int (&cached)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return 0;
+    if (cached[dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            n = sm_count() / 2;
+        }
+        cached[dev] = n < 1 ? 1 : n > most ? most : n;
+    }
+    return cached[dev];
+}
+
+// Launch as a programmatic dependent of the kernel before it on the stream.
+template <class... Args>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace echo

@@ -247,9 +247,10 @@ def test_paged_calls_check_their_arguments(L):
     assert chunk(n_rows=0, q=None, out=None, lse=None) == lib.ECHO_OK
     assert lib.mla_chunk_workspace_size(-1, 16, 1) == 0 and lib.mla_chunk_workspace_size(4, 0, 1) == 0
 
-    def mass(lse=d, m=d, out=d, decay=0.5, n=10, scale=0.1, n_rows=2):
-        return L.echo_mla_mass(1, d, n_rows, 16, d, lse, d, None, n, pages(), 0, 0, scale, m, out, decay, d, None)
-    for bad in (dict(lse=None), dict(m=None), dict(out=None), dict(decay=-0.1), dict(decay=nan), dict(decay=inf),
+    def mass(lse=d, m=d, out=d, decay=0.5, n=10, scale=0.1, n_rows=2, ws=d, short=0):
+        return L.echo_mla_mass(1, d, n_rows, 16, d, lse, d, None, n, pages(), 0, 0, scale, m, out, decay, ws,
+                               lib.mla_mass_workspace_size(max(n, 0), 1) - short, d, None)
+    for bad in (dict(ws=None), dict(ws=v(0x1080)), dict(short=1), dict(lse=None), dict(m=None), dict(out=None), dict(decay=-0.1), dict(decay=nan), dict(decay=inf),
                 dict(n=-1), dict(scale=0.0), dict(n_rows=-1)):
         assert mass(**bad) == lib.ECHO_EINVAL, bad
     assert mass(n=0, m=None, out=None) == lib.ECHO_OK
