@@ -527,7 +527,8 @@ typedef struct echo_pages {
     int32_t reserved;
 } echo_pages;
 
-#define ECHO_CHUNK_MAX_ROWS (1 << 20) /* rows per call */
+#define ECHO_CHUNK_MAX_ROWS (1 << 20)        /* rows per call */
+#define ECHO_CHUNK_MAX_TOKENS 0x7FFFFF00     /* tokens of a request that has rows, entries of a row's selection */
 
 /*
  * Attention of a chunk of new tokens.  Request b's new rows are
@@ -551,8 +552,8 @@ typedef struct echo_pages {
  *   q [n_rows,heads,576] bf16 (as uint16 bits, 16-byte aligned), 1 <= heads <=
  *   ECHO_MLA_HEADS; out [n_rows,heads,512] bf16 (16-byte aligned), lse
  *   [n_rows,heads] f32; scale > 0 and finite.  Rows outside every request are left as
- *   they were.  A request with more rows than tokens, or inconsistent token
- *   bounds: its rows see nothing; inconsistent row bounds: its rows are left
+ *   they were.  A request with more rows than tokens, more than
+ *   ECHO_CHUNK_MAX_TOKENS tokens or inconsistent token bounds: its rows see nothing; inconsistent row bounds: its rows are left
  *   as they were; both set ECHO_ST_BADDATA.
  *   A cache row that some row of the call sees must be finite; rows that none
  *   sees are not read.
@@ -562,7 +563,8 @@ typedef struct echo_pages {
  * calls that may run at the same time need their own.
  * Errors: ECHO_EINVAL (sizes, NULL or misaligned pointers, a small workspace),
  * ECHO_EUNSUPPORTED (B > ECHO_MAX_REQUESTS, heads > ECHO_MLA_HEADS, n_rows >
- * ECHO_CHUNK_MAX_ROWS), ECHO_ECUDA.  n_rows = 0: nothing is enqueued.
+ * ECHO_CHUNK_MAX_ROWS, k > ECHO_CHUNK_MAX_TOKENS), ECHO_ECUDA.  n_rows = 0:
+ * nothing is enqueued.
  */
 size_t echo_mla_chunk_workspace_size(int64_t n_rows, int heads, int B);
 int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q,

@@ -19,13 +19,15 @@
 //               MN-major operand.
 // Neither product is done twice, and the softmax needs nothing from the other
 // CTA.  Warps of a CTA: 0-3 softmax (thread = TMEM lane; the two threads of a
-// row exchange their tile maxima in shared memory), 4-7 gather the K and V
-// parts of the tiles (16-byte cp.async, any row for any token, two stages
-// each), 8 issues the MMAs (CTA 0) or reports its CTA's K tiles to CTA 0 (CTA 1), 9
-// reports the V tiles.  QK of tile t + 1 is issued before PV of tile t, so the
-// softmax runs under the tensor cores.  The softmax reference moves only when a
-// score exceeds it by more than 2^8 (P <= 256 in bf16, exact after the final
-// division); O in TMEM is rescaled then.
+// row exchange their tile maxima in shared memory), 4-7 gather K, 8-11 gather V
+// and Q (16-byte cp.async: any row for any token; two stages of each, K in
+// thirds that are refilled as their MMAs end), 12 of CTA 0 issues the MMAs, 13
+// and 14 report what has landed in their CTA to it (one barrier for both CTAs: each
+// wait costs the issuing warp a hundred cycles).  QK of tile t + 1 is
+// issued before PV of tile t and P has two buffers, so the softmax runs under the
+// tensor cores.  The softmax reference moves only when a score exceeds it by
+// more than 2^8 (P <= 256 in bf16, exact after the final division); O in TMEM is
+// rescaled then.
 //
 // Work: every tile costs the same and a group costs kOver tiles more (its Q, its
 // result).  chunk_plan_kernel lays the groups' costs in a row; cluster i takes the
@@ -41,13 +43,14 @@ namespace {
 
 constexpr int kTok = 64;                 // tokens per tile
 constexpr int kM = 128;                  // (row, head) pairs per group
-constexpr int kThreads = 320;
+constexpr int kThreads = 512;
 constexpr int kSoftmax = 128, kLoad = 128;
 constexpr int kAtoms = kLatDqk / 64;     // 9 swizzle atoms of 64 dims
 constexpr uint32_t kQAtom = 64 * 128;    // 64 rows x 128 B
 constexpr uint32_t kKAtom = 32 * 128;    // this CTA's 32 tokens
 constexpr uint32_t kVAtom = kTok * 128;  // 64 tokens x 64 dims
 constexpr uint32_t kQBytes = kAtoms * kQAtom;
+constexpr int kChunks = 1;               // parts in which K of a tile comes and goes
 constexpr uint32_t kKBytes = kAtoms * kKAtom;
 constexpr uint32_t kVBytes = 4 * kVAtom;
 constexpr uint32_t kPBytes = 64 * 128;
@@ -55,7 +58,7 @@ constexpr uint32_t kTmemCols = 512;      // O [0, 256) | S0 [256, 288) | S1 [288
 constexpr uint32_t kSCol = 256;
 constexpr float kLazy = 8.f;
 constexpr int kOver = 3;                 // a group's fixed cost in tiles
-constexpr int kMinUnits = 6;             // least units per cluster
+constexpr int kMinUnits = 4;             // least units per cluster
 constexpr int kMaxClusters = 96;         // bounds the workspace (the device has 76 pairs of SMs)
 constexpr uint32_t kIdescS = idesc_bf16_f32(kM, kTok);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kM, 256) | (1u << 16);  // B (V) MN-major
@@ -81,8 +84,14 @@ struct __align__(16) PlanHead {
     int32_t parts;  // clusters that take a share
 };
 
+// A group that more than one share holds a part of: shares i0 .. i0 + n - 1.
+struct __align__(16) Cut {
+    int32_t n, i0, row0, live;  // live: its (row, head) pairs
+};
+
 struct Plan {
     PlanHead* head;
+    Cut* cut;       // [kMaxClusters] by the second of its shares; n = 0: none
     Group* group;   // [cap]
     int64_t* cum;   // [cap + 1] units before each group
     uint8_t* part;  // [2 * kMaxClusters] partial results
@@ -97,7 +106,7 @@ struct Layout {
 };
 inline Layout plan_layout(int64_t cap) {
     Layout l;
-    l.group = 256;
+    l.group = 256 + round_up(kMaxClusters * sizeof(Cut), 256);
     l.cum = round_up(l.group + static_cast<size_t>(cap) * sizeof(Group), 256);
     l.part = round_up(l.cum + static_cast<size_t>(cap + 1) * 8, 256);
     l.total = l.part + 2 * kMaxClusters * kPartBytes;
@@ -221,23 +230,75 @@ struct Walk {
     }
 };
 
+// One token of every tile of a piece, looked up ahead of its copy: the list entry
+// (selections) of two tiles ahead and the table entry of the next tile are in flight
+// while this tile's rows are copied.
+struct Gather {
+    const int32_t* sel;  // the row's list, null: causal or window
+    PageView pv;
+    int lo_tok;
+    int v;               // index of the token whose table entry is in flight
+    int tok;             // token of the tile after it, -1: none
+    int32_t entry;       // table entry in flight, < 0: none
+    uint32_t at;         // offset in that page
+    bool bad;
+    __device__ __forceinline__ int token(const Piece& p, int x) const {
+        if (x >= p.g.nv) return -1;
+        if (sel) return sel[x];
+        return x < p.g.kept ? x : x - p.g.kept + lo_tok;
+    }
+    __device__ __forceinline__ void look(const ChunkArgs& a, const Piece& p, int t) {
+        entry = -1;
+        if (sel && t >= p.g.kept) {  // past the request's end
+            bad = true;
+            t = -1;
+        }
+        if (t >= 0) entry = pv.tab[page_of(a, pv, static_cast<uint32_t>(t), &at)];
+    }
+    __device__ __forceinline__ void start(const ChunkArgs& a, const Piece& p, int r) {
+        sel = a.sel ? a.sel + static_cast<int64_t>(p.g.row0) * a.k : nullptr;
+        pv = page_view(a, p.g.req, p.g.off);
+        lo_tok = p.g.pos0 + p.g.rows + p.g.kept - p.g.nv;
+        v = p.lo * kTok + r;
+        bad = false;
+        at = 0;
+        const int t0 = token(p, v);
+        tok = p.lo + 1 < p.hi ? token(p, v + kTok) : -1;
+        look(a, p, t0);
+    }
+    // The cache row of the current tile's token, -1 when it has none.
+    __device__ __forceinline__ int64_t row(const ChunkArgs& a) {
+        int64_t r = entry < 0 ? -1 : page_row(a, pv, entry, at, &bad);
+        if (bad) set_status(a.status, ECHO_ST_BADDATA);
+        bad = false;
+        return r;
+    }
+    __device__ __forceinline__ void next(const ChunkArgs& a, const Piece& p) {
+        v += kTok;
+        const int t = tok;
+        tok = v + kTok < p.hi * kTok ? token(p, v + kTok) : -1;
+        look(a, p, t);
+    }
+};
+
 // ---------------------------------------------------------------- attention
 struct Ctl {
-    uint64_t q_full, pq_full;         // Q of a group landed here / in CTA 1
-    uint64_t k_full[2], pk_full[2];   // K part of a stage landed here / in CTA 1
-    uint64_t v_full[2], pv_full[2];   // V part
-    uint64_t qk_done[2];              // S of a tile done: K stage free, S ready
-    uint64_t pv_done[2];              // P V of a tile done: V stage and P free, O ready
-    uint64_t p_full;                  // P of a tile written in both CTAs
-    uint64_t drain;
+    // here: landed in this CTA; the *_ready barriers of CTA 0: landed in both
+    uint64_t q_full, q_ready;                            // Q of a group
+    uint64_t k_full[2][kChunks], k_ready[2][kChunks];    // a third of a stage's K
+    uint64_t k_free[2][kChunks];                         // its MMAs are done; the last third: S of the tile is ready
+    uint64_t v_full[2];                                  // V of a stage
+    uint64_t pv_ready[2];                                // V, and P of the tile, in both CTAs
+    uint64_t pv_done[2];                                 // P V of a tile done: V stage and P buffer free, O ready
+    uint64_t drain[2];
     uint32_t tmem;
     int abort;
-    int first;                        // the share's first group
-    float mx[2][2][64];               // tile maxima by (tile parity, token half, row)
-    float l[2][2][64];                // sums by (piece parity, token half, row)
-    alignas(16) uint8_t valid[4][kTok];           // tokens of a tile that have a row
+    int first;                                           // the share's first group
+    float mx[2][2][64];                                  // tile maxima by (tile parity, token half, row)
+    float l[2][2][64];                                   // sums by (piece parity, token half, row)
+    alignas(16) uint8_t valid[4][kTok];                  // tokens of a tile that have a row
 };
-constexpr uint32_t kSmem = kQBytes + 2 * kKBytes + 2 * kVBytes + kPBytes + ((sizeof(Ctl) + 15u) & ~15u) + 1024;
+constexpr uint32_t kSmem = kQBytes + 2 * kKBytes + 2 * kVBytes + 2 * kPBytes + ((sizeof(Ctl) + 15u) & ~15u);
 static_assert(kSmem <= 227u * 1024u, "chunk shared memory");
 
 // Barrier over the softmax warps; true when any thread votes so.
@@ -254,15 +315,40 @@ __device__ __forceinline__ bool softmax_sync_or(bool v) {
     return r != 0;
 }
 
+// The MMAs of stage ST.  The stage is a constant so that every descriptor is one too: with
+// descriptors computed from a variable stage an MMA took 100 cycles to issue, four times what it runs.
+template <int ST>
+__device__ __forceinline__ void issue_qk(uint32_t tmem, uint32_t sQ, uint32_t sK, int ch) {
+    const uint64_t ad = sw128_kmajor_desc(sQ), bd = sw128_kmajor_desc(sK + ST * kKBytes);
+#pragma unroll
+    for (int kk = 0; kk < 4 * kAtoms; ++kk)
+        if (kk / (4 * kAtoms / kChunks) == ch)
+            mma2_bf16(tmem + kSCol + ST * 32u, ad + (((kk >> 2) * kQAtom + (kk & 3) * 32u) >> 4),
+                      bd + (((kk >> 2) * kKAtom + (kk & 3) * 32u) >> 4), kIdescS, kk > 0 ? 1u : 0u);
+}
+template <int ST>
+__device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t sP, uint32_t sV, bool add) {
+    const uint64_t ad = sw128_kmajor_desc(sP + ST * kPBytes), bd = sw128_mnmajor_desc(sV + ST * kVBytes, kVAtom);
+#pragma unroll
+    for (int kk = 0; kk < kTok / 16; ++kk)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            mma2_bf16(tmem + 128u * j, ad + ((kk * 32u) >> 4), bd + ((2u * j * kVAtom + kk * 2048u) >> 4), kIdescO,
+                      (add || kk > 0) ? 1u : 0u);
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_kernel(ChunkArgs a, Plan plan, float scale_log2, uint16_t* __restrict__ out, float* __restrict__ lse) {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t* const gbase = smem_raw + (base - raw);
+    extern __shared__ __align__(1024) uint8_t chunk_smem[];  // the swizzled tiles need 1024 bytes
+    uint8_t* const gbase = chunk_smem;
+    const uint32_t base = smem_addr(gbase);
+    if (base & 1023u) {  // the same in every CTA
+        set_status(a.status, ECHO_ST_TIMEOUT);
+        return;
+    }
     const uint32_t sQ = base, sK = sQ + kQBytes, sV = sK + 2 * kKBytes, sP = sV + 2 * kVBytes;
     uint8_t* const gP = gbase + (sP - base);
-    Ctl* const ctl = reinterpret_cast<Ctl*>(gP + kPBytes);
+    Ctl* const ctl = reinterpret_cast<Ctl*>(gP + 2 * kPBytes);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t c = cluster_rank();
     const int ci = blockIdx.x >> 1;
@@ -270,17 +356,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         mbar_init(smem_addr(&ctl->q_full), kLoad);
-        mbar_init(smem_addr(&ctl->pq_full), 1);
+        mbar_init(smem_addr(&ctl->q_ready), 2);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&ctl->k_full[i]), 2 * kLoad);  // the copies, and the valid flags
-            mbar_init(smem_addr(&ctl->pk_full[i]), 1);
+            for (int j = 0; j < kChunks; ++j) {
+                mbar_init(smem_addr(&ctl->k_full[i][j]), j == 0 ? 2 * kLoad : kLoad);  // the copies; first: the valid flags too
+                mbar_init(smem_addr(&ctl->k_ready[i][j]), 2);
+                mbar_init(smem_addr(&ctl->k_free[i][j]), 1);
+            }
             mbar_init(smem_addr(&ctl->v_full[i]), kLoad);
-            mbar_init(smem_addr(&ctl->pv_full[i]), 1);
-            mbar_init(smem_addr(&ctl->qk_done[i]), 1);
+            mbar_init(smem_addr(&ctl->pv_ready[i]), 2 * kSoftmax / 32 + 2);
             mbar_init(smem_addr(&ctl->pv_done[i]), 1);
         }
-        mbar_init(smem_addr(&ctl->p_full), 2 * kSoftmax / 32);
-        mbar_init(smem_addr(&ctl->drain), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&ctl->drain[i]), 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -298,7 +385,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (warp == 1 && walk.u0 < walk.u1) {
         const int g = find_group(plan.cum, head.groups, walk.u0);
-        if (lane == 0) ctl->first = g;
+        if (lane == 0) {
+            ctl->first = g;
+            if (c == 0 && ci > 0) {  // for the join: whether this share starts the second part of a group
+                const Group gr = plan.group[g];
+                const int64_t at = plan.cum[g];
+                Cut cut = {0, ci - 1, gr.row0, gr.rows * a.heads};
+                if (walk.u0 > at + kOver && share_start(head.total, head.parts, ci - 1) <= at + kOver)
+                    cut.n = share_of(head.total, head.parts, at + kOver + tiles_of(gr.nv) - 1) - cut.i0 + 1;
+                plan.cut[ci] = cut;
+            }
+        }
+    } else if (warp == 1 && lane == 0 && c == 0 && ci > 0) {
+        plan.cut[ci] = Cut{0, 0, 0, 0};
     }
     tc_fence_before();
     __syncthreads();
@@ -314,7 +413,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int half = tid >> 6, row = tid & 63, mi = static_cast<int>(c) * 64 + row;
         const int rig = mi / a.heads;  // row within the group
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-        const uint32_t pfull = smem_addr(&ctl->p_full);
         bool ok = true;
         for (uint32_t piece = 0; ok && walk.next(&p); ++piece) {
             const bool lives = rig < p.g.rows;
@@ -336,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.f;
             for (int it = p.lo; it < p.hi; ++it, ++t) {
                 const uint32_t st = t & 1u;
-                ok = ok && mbar_wait(smem_addr(&ctl->qk_done[st]), (t >> 1) & 1u, abort);
+                ok = ok && mbar_wait(smem_addr(&ctl->k_free[st][kChunks - 1]), (t >> 1) & 1u, abort);
                 tc_fence_after();
                 __syncwarp();
                 float s[32];
@@ -385,16 +483,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     packed[j >> 1] = *reinterpret_cast<const uint32_t*>(&pb);
                 }
                 l = l * corr + ((part[0] + part[1]) + (part[2] + part[3]));
-                // P and O are free once PV of the tile before is done
-                if (it > p.lo) ok = mbar_wait(smem_addr(&ctl->pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, abort);
-                tc_fence_after();
-                __syncwarp();
-                uint8_t* const prow = gP + row * 128;
+                // this P buffer is free once PV of two tiles before is done
+                if (t >= 2) ok = mbar_wait(smem_addr(&ctl->pv_done[st]), ((t >> 1) & 1u) ^ 1u, abort);
+                uint8_t* const prow = gP + st * kPBytes + row * 128;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     *reinterpret_cast<uint4*>(prow + (((4 * half + j) ^ (row & 7)) << 4)) =
                         make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-                if (it > p.lo && moves) {
+                if (it > p.lo && moves) {  // O holds earlier tiles: bring it to the new reference
+                    ok = ok && mbar_wait(smem_addr(&ctl->pv_done[st ^ 1u]), ((t - 1) >> 1) & 1u, abort);
+                    tc_fence_after();
+                    __syncwarp();
 #pragma unroll 1
                     for (uint32_t x = 0; x < 256u; x += 32u) {
                         float o[32];
@@ -407,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(pfull, 0);
+                if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->pv_ready[st]), 0);
             }
             if (!ok) break;
             // ---- the group's result, or this piece's part of it
@@ -468,183 +567,171 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!ok) *abort = 1;
     } else if (warp < 8) {
-        // ---- gather
-        const int lt = tid - kSoftmax;
-        const int kr = lt >> 2, vr = lt >> 1;  // K row (of this CTA's 32 tokens), V row (of the tile's 64)
-        const uint32_t kdst = static_cast<uint32_t>(kr) * 128u, vdst = static_cast<uint32_t>(vr) * 128u;
-        uint32_t groups = 0;
+        // ---- K of this CTA's 32 tokens, a third of the dims at a time.  A warp has 8 tokens and copies
+        // four 128-byte row pieces per instruction (8 lanes each): with 64-byte pieces of 8 rows the
+        // copies took twice the shared-memory cycles.  Lanes 0-7 look up the warp's tokens, lanes 8-15
+        // those of the other CTA, for the valid flags.
+        const int w = warp - 4, x = lane & 7, r4 = lane >> 3;
         bool ok = true;
         while (ok && walk.next(&p)) {
             if (p.hi == p.lo) continue;
-            const PageView pv = page_view(a, p.g.req, p.g.off);
-            const int lo_tok = p.g.pos0 + p.g.rows + p.g.kept - p.g.nv;
-            const int32_t* const sel = a.sel ? a.sel + static_cast<int64_t>(p.g.row0) * a.k : nullptr;
-            const auto cache_row = [&](int v) -> int64_t {
-                if (v >= p.g.nv) return -1;
-                bool bad = false;
-                int64_t r = -1;
-                int tk;
-                if (sel) {
-                    tk = sel[v];
-                    if (tk >= p.g.kept) {
-                        bad = true;
-                        tk = -1;
-                    }
-                } else {
-                    tk = v < p.g.kept ? v : v - p.g.kept + lo_tok;
-                }
-                if (tk >= 0) r = token_row(a, pv, static_cast<uint32_t>(tk), &bad);
-                if (bad) set_status(a.status, ECHO_ST_BADDATA);
-                return r;
-            };
-            int64_t rk = cache_row(p.lo * kTok + static_cast<int>(c) * 32 + kr), rv = cache_row(p.lo * kTok + vr);
+            const int mine = static_cast<int>(lane < 8 ? c : c ^ 1u) * 32 + 8 * w + (lane & 7);
+            Gather own;
+            own.start(a, p, mine);
             for (int it = p.lo; it < p.hi; ++it, ++t) {
                 const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
-                int64_t nk = -1, nv = -1;
-                if (it + 1 < p.hi) {  // the next tile's rows, looked up while this one waits
-                    nk = cache_row((it + 1) * kTok + static_cast<int>(c) * 32 + kr);
-                    nv = cache_row((it + 1) * kTok + vr);
-                }
-                if (t >= 2 && !mbar_wait(smem_addr(&ctl->qk_done[st]), ph ^ 1u, abort)) {
-                    ok = false;
-                    break;
-                }
-                {
-                    const uint8_t* src = a.kv + (rk < 0 ? 0 : rk * kLatRowBytes);
-                    const uint32_t n = rk < 0 ? 0u : 16u, dst = sK + st * kKBytes + kdst;
+                const int64_t row = own.row(a);
+                own.next(a, p);
+                const uint8_t* src[2];
+                uint32_t n[2], dst[2];
 #pragma unroll
-                    for (int j = 0; j < 18; ++j) {
-                        const int x = (lt & 3) + 4 * j;
-                        cp_async_16(dst + static_cast<uint32_t>(x >> 3) * kKAtom + (static_cast<uint32_t>((x ^ kr) & 7) << 4),
-                                    src + 16 * x, n);
-                    }
-                    if ((lt & 1) == 0) ctl->valid[t & 3u][vr] = rv < 0 ? 0 : 1;
-                    cp_async_arrive_noinc(smem_addr(&ctl->k_full[st]));
-                    mbar_arrive(smem_addr(&ctl->k_full[st]));
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 4 * i + r4;  // of the warp's 8
+                    const int64_t rk = __shfl_sync(0xffffffffu, row, r);
+                    src[i] = a.kv + (rk < 0 ? 0 : rk * kLatRowBytes) + 16 * x;
+                    n[i] = rk < 0 ? 0u : 16u;
+                    dst[i] = sK + st * kKBytes + static_cast<uint32_t>(8 * w + r) * 128u + (static_cast<uint32_t>(x ^ r) << 4);
                 }
-                if (it == p.lo) {  // Q of the group, once the group before has no QK left
-                    if (t >= 1 && !mbar_wait(smem_addr(&ctl->qk_done[st ^ 1u]), ((t - 1) >> 1) & 1u, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const int live = p.g.rows * a.heads - static_cast<int>(c) * 64;
-                    const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q) +
-                                       (static_cast<int64_t>(p.g.row0) * a.heads + static_cast<int64_t>(c) * 64) * kLatRowBytes;
-#pragma unroll 4
-                    for (int i = lt; i < 64 * 72; i += kLoad) {
-                        const int r = i / 72, x = i - r * 72;
-                        const bool in = r < live;
-                        cp_async_16(sQ + sw_offset(r, x, kQAtom), in ? q + static_cast<int64_t>(r) * kLatRowBytes + 16 * x : a.kv,
-                                    in ? 16u : 0u);
-                    }
-                    cp_async_arrive_noinc(smem_addr(&ctl->q_full));
-                    ++groups;
-                }
-                if (t >= 2 && !mbar_wait(smem_addr(&ctl->pv_done[st]), ph ^ 1u, abort)) {
-                    ok = false;
-                    break;
-                }
-                {
-                    const uint8_t* src = a.kv + (rv < 0 ? 0 : rv * kLatRowBytes) + c * 512u;
-                    const uint32_t n = rv < 0 ? 0u : 16u, dst = sV + st * kVBytes + vdst;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int x = (lt & 1) + 2 * j;
-                        cp_async_16(dst + static_cast<uint32_t>(x >> 3) * kVAtom + (static_cast<uint32_t>((x ^ vr) & 7) << 4),
-                                    src + 16 * x, n);
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    if (t >= 2 && ok) ok = mbar_wait(smem_addr(&ctl->k_free[st][ch]), ph ^ 1u, abort);
+                    if (!ok) break;
+#pragma unroll
+                    for (int j = kAtoms / kChunks * ch; j < kAtoms / kChunks * (ch + 1); ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) cp_async_16(dst[i] + j * kKAtom, src[i] + 128 * j, n[i]);
+                    cp_async_arrive_noinc(smem_addr(&ctl->k_full[st][ch]));
+                    if (ch == 0) {
+                        if (lane < 16) ctl->valid[t & 3u][mine] = row < 0 ? 0 : 1;
+                        mbar_arrive(smem_addr(&ctl->k_full[st][0]));
                     }
-                    cp_async_arrive_noinc(smem_addr(&ctl->v_full[st]));
                 }
-                rk = nk;
-                rv = nv;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
             }
         }
         if (!ok) *abort = 1;
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 8 && c == 0) {
-        // ---- the MMAs of both CTAs
+    } else if (warp < 12) {
+        // ---- Q of a group, and V: this CTA's 256 dims of the tile's 64 tokens, 16 to a warp, copied like K
+        const int lt = tid - kSoftmax - kLoad, w = warp - 8, x = lane & 7, r4 = lane >> 3;
+        bool ok = true;
+        while (ok && walk.next(&p)) {
+            if (p.hi == p.lo) continue;
+            Gather own;
+            own.start(a, p, 16 * w + (lane & 15));
+            // Q once the group before has no QK left
+            if (t >= 1) ok = mbar_wait(smem_addr(&ctl->k_free[(t - 1) & 1u][kChunks - 1]), ((t - 1) >> 1) & 1u, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            {
+                const int live = p.g.rows * a.heads - static_cast<int>(c) * 64;
+                const uint8_t* const q = reinterpret_cast<const uint8_t*>(a.q) +
+                                         (static_cast<int64_t>(p.g.row0) * a.heads + static_cast<int64_t>(c) * 64) * kLatRowBytes;
+#pragma unroll 4
+                for (int i = lt; i < 64 * 72; i += kLoad) {
+                    const int r = i / 72, y = i - r * 72;
+                    const bool in = r < live;
+                    cp_async_16(sQ + sw_offset(r, y, kQAtom), in ? q + static_cast<int64_t>(r) * kLatRowBytes + 16 * y : a.kv,
+                                in ? 16u : 0u);
+                }
+                cp_async_arrive_noinc(smem_addr(&ctl->q_full));
+            }
+            for (int it = p.lo; it < p.hi; ++it, ++t) {
+                const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
+                const int64_t row = own.row(a);
+                own.next(a, p);
+                const uint8_t* src[4];
+                uint32_t n[4], dst[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 4 * i + r4;  // of the warp's 16
+                    const int64_t rv = __shfl_sync(0xffffffffu, row, r);
+                    src[i] = a.kv + (rv < 0 ? 0 : rv * kLatRowBytes) + c * 512u + 16 * x;
+                    n[i] = rv < 0 ? 0u : 16u;
+                    dst[i] = sV + st * kVBytes + static_cast<uint32_t>(16 * w + r) * 128u +
+                             (static_cast<uint32_t>(x ^ (r & 7)) << 4);
+                }
+                if (t >= 2) ok = mbar_wait(smem_addr(&ctl->pv_done[st]), ph ^ 1u, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cp_async_16(dst[i] + j * kVAtom, src[i] + 128 * j, n[i]);
+                cp_async_arrive_noinc(smem_addr(&ctl->v_full[st]));
+            }
+        }
+        if (!ok) *abort = 1;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 12 || warp == 13) {
+        // ---- the MMAs of both CTAs: Q K by one thread of CTA 0, P V by another.  A look at a barrier and a
+        // commit cost their thread about 300 cycles a pair; one thread for both products was the limit.
+        const bool qk = warp == 12;
+        if (c == 0 && elect_one()) {
+            uint32_t groups = 0;
+            bool ok = true;
+            while (ok && walk.next(&p)) {
+                if (p.hi == p.lo) continue;
+                if (qk) ok = mbar_wait_cluster(smem_addr(&ctl->q_ready), groups & 1u, abort);
+                ++groups;
+                for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
+                    const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
+                    if (qk) {
+                        // S(t - 2) has been read once its P is written
+                        if (t >= 2) ok = mbar_wait_cluster(smem_addr(&ctl->pv_ready[st]), ph ^ 1u, abort);
+#pragma unroll
+                        for (int ch = 0; ch < kChunks; ++ch) {
+                            ok = ok && mbar_wait_cluster(smem_addr(&ctl->k_ready[st][ch]), ph, abort);
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (st == 0) issue_qk<0>(tmem, sQ, sK, ch);
+                            else issue_qk<1>(tmem, sQ, sK, ch);
+                            mma2_commit_both(smem_addr(&ctl->k_free[st][ch]));
+                        }
+                    } else {  // O += P V
+                        ok = mbar_wait_cluster(smem_addr(&ctl->pv_ready[st]), ph, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (st == 0) issue_pv<0>(tmem, sP, sV, it > p.lo);
+                        else issue_pv<1>(tmem, sP, sV, it > p.lo);
+                        mma2_commit_both(smem_addr(&ctl->pv_done[st]));
+                    }
+                }
+            }
+            if (!ok) {  // the MMAs in flight end before the CTAs' memory goes
+                *abort = 1;
+                mma2_commit_both(smem_addr(&ctl->drain[qk ? 0 : 1]));
+                (void)mbar_wait(smem_addr(&ctl->drain[qk ? 0 : 1]), 0, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 14) {
+        // ---- Q and K have landed here: made visible to the tensor cores and reported to CTA 0
         uint32_t groups = 0;
         bool ok = true;
         while (ok && walk.next(&p)) {
             if (p.hi == p.lo) continue;
-            ok = mbar_wait(smem_addr(&ctl->q_full), groups & 1u, abort) &&
-                 mbar_wait_cluster(smem_addr(&ctl->pq_full), groups & 1u, abort);
+            ok = mbar_wait(smem_addr(&ctl->q_full), groups & 1u, abort);
             ++groups;
-            const int n = p.hi - p.lo;
-            for (int i = 0; ok && i <= n; ++i) {
-                if (i < n) {  // S of tile t
-                    const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
-                    ok = mbar_wait(smem_addr(&ctl->k_full[st]), ph, abort) &&
-                         mbar_wait_cluster(smem_addr(&ctl->pk_full[st]), ph, abort);
-                    if (!ok) break;
+            fence_proxy_async_smem();
+            if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->q_ready), 0);
+            for (int it = p.lo; ok && it < p.hi; ++it, ++t)
+                for (int ch = 0; ok && ch < kChunks; ++ch) {
+                    ok = mbar_wait(smem_addr(&ctl->k_full[t & 1u][ch]), (t >> 1) & 1u, abort);
                     fence_proxy_async_smem();
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t ad = sw128_kmajor_desc(sQ), bd = sw128_kmajor_desc(sK + st * kKBytes);
-                        const uint32_t d = tmem + kSCol + st * 32u;
-#pragma unroll
-                        for (int kk = 0; kk < 4 * kAtoms; ++kk)
-                            mma2_bf16(d, ad + (((kk >> 2) * kQAtom + (kk & 3) * 32u) >> 4),
-                                      bd + (((kk >> 2) * kKAtom + (kk & 3) * 32u) >> 4), kIdescS, kk > 0 ? 1u : 0u);
-                        mma2_commit_both(smem_addr(&ctl->qk_done[st]));
-                    }
-                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->k_ready[t & 1u][ch]), 0);
                 }
-                if (i > 0) {  // O += P V of the tile before
-                    const uint32_t u = t - 1, st = u & 1u, ph = (u >> 1) & 1u;
-                    ok = mbar_wait_cluster(smem_addr(&ctl->p_full), u & 1u, abort) &&
-                         mbar_wait(smem_addr(&ctl->v_full[st]), ph, abort) &&
-                         mbar_wait_cluster(smem_addr(&ctl->pv_full[st]), ph, abort);
-                    if (!ok) break;
-                    fence_proxy_async_smem();
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t ad = sw128_kmajor_desc(sP), bd = sw128_mnmajor_desc(sV + st * kVBytes, kVAtom);
-#pragma unroll
-                        for (int kk = 0; kk < kTok / 16; ++kk)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                mma2_bf16(tmem + 128u * j, ad + ((kk * 32u) >> 4),
-                                          bd + ((2u * j * kVAtom + kk * 2048u) >> 4), kIdescO, (i > 1 || kk > 0) ? 1u : 0u);
-                        mma2_commit_both(smem_addr(&ctl->pv_done[st]));
-                    }
-                    __syncwarp();
-                }
-                if (i < n) ++t;
-            }
-        }
-        if (!ok) {  // the MMAs in flight end before the CTAs' memory goes
-            if (lane == 0) *abort = 1;
-            if (elect_one()) mma2_commit_both(smem_addr(&ctl->drain));
-            __syncwarp();
-            (void)mbar_wait(smem_addr(&ctl->drain), 0, nullptr);
-        }
-    } else if (warp == 8) {
-        // ---- CTA 1: Q and K have landed here
-        uint32_t groups = 0;
-        bool ok = true;
-        while (ok && walk.next(&p)) {
-            for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
-                ok = mbar_wait(smem_addr(&ctl->k_full[t & 1u]), (t >> 1) & 1u, abort);
-                fence_proxy_async_smem();
-                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->pk_full[t & 1u]), 0);
-                if (ok && it == p.lo) {
-                    ok = mbar_wait(smem_addr(&ctl->q_full), groups & 1u, abort);
-                    fence_proxy_async_smem();
-                    if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->pq_full), 0);
-                    ++groups;
-                }
-            }
         }
         if (!ok && lane == 0) *abort = 1;
-    } else if (c == 1) {
-        // ---- CTA 1, warp 9: V has landed here
+    } else {
+        // ---- V has landed here
         bool ok = true;
         while (ok && walk.next(&p)) {
             for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
                 ok = mbar_wait(smem_addr(&ctl->v_full[t & 1u]), (t >> 1) & 1u, abort);
                 fence_proxy_async_smem();
-                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->pv_full[t & 1u]), 0);
+                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->pv_ready[t & 1u]), 0);
             }
         }
         if (!ok && lane == 0) *abort = 1;
@@ -660,71 +747,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- join
-// Block (i, y): share boundary i + 1, when it is the first inside a group's tiles; 4 (row, head) pairs.
-constexpr int kJT = 256, kJRows = 4;
+// A block takes (cut group, (row, head)) tasks in turn: thread = 4 dims, and every warp
+// works out the pieces' weights for itself (lane = piece).
+constexpr int kJT = kLatDv / 4;
+constexpr int kJLanes = (kMaxClusters + 31) / 32;
 
 __global__ void __launch_bounds__(kJT) chunk_join_kernel(ChunkArgs a, Plan plan, uint16_t* __restrict__ out,
                                                          float* __restrict__ lse) {
-    __shared__ int s_group;
-    __shared__ float s_w[kMaxClusters][kJRows];
-    __shared__ float s_L[kJRows], s_M[kJRows];
+    __shared__ Cut s_cut[kMaxClusters];
+    __shared__ int s_n;
     pdl_wait();
-    const int tid = threadIdx.x, i = blockIdx.x + 1;
-    const PlanHead head = *plan.head;
-    if (i >= head.parts) return;
-    const int64_t u = share_start(head.total, head.parts, i);
+    const int tid = threadIdx.x, lane = tid & 31;
     if (tid < 32) {
-        const int g = find_group(plan.cum, head.groups, u);
-        if (tid == 0) s_group = g;
+        int n = 0;
+        for (int i0 = 1; i0 < plan.clusters; i0 += 32) {
+            const int i = i0 + lane;
+            Cut x = {0, 0, 0, 0};
+            if (i < plan.clusters) x = plan.cut[i];
+            const uint32_t m = __ballot_sync(0xffffffffu, x.n > 0);
+            if (x.n > 0) s_cut[n + __popc(m & ((1u << lane) - 1u))] = x;
+            n += __popc(m);
+        }
+        if (lane == 0) s_n = n;
     }
     __syncthreads();
-    const Group g = plan.group[s_group];
-    const int64_t c = plan.cum[s_group];
-    const int tiles = tiles_of(g.nv);
-    if (u <= c + kOver || share_start(head.total, head.parts, i - 1) > c + kOver) return;  // no cut here, or not the group's first
-    const int i0 = i - 1, i1 = share_of(head.total, head.parts, c + kOver + tiles - 1);
-    const int n = i1 - i0 + 1, live = g.rows * a.heads;
-    const int m0 = blockIdx.y * kJRows;
-    if (m0 >= live) return;
-    // piece j is share i0 + j: the first starts at tile 0 (second slot), the others within (first slot)
-    const auto part = [&](int j) { return plan.part + static_cast<size_t>(2 * (i0 + j) + (j == 0 ? 1 : 0)) * kPartBytes; };
-    for (int x = tid; x < n * kJRows; x += kJT)
-        s_w[x / kJRows][x % kJRows] = reinterpret_cast<const float*>(part(x / kJRows) + kPartO)[m0 + x % kJRows];
-    __syncthreads();
-    if (tid < kJRows) {
+    for (int task = blockIdx.x; task < s_n * kM; task += gridDim.x) {
+        const Cut x = s_cut[task / kM];
+        const int mi = task % kM;
+        if (mi >= x.live) continue;
+        // piece j is share i0 + j: the first starts at tile 0 (second slot), the others within (first slot)
+        const auto part = [&](int j) { return plan.part + static_cast<size_t>(2 * (x.i0 + j) + (j == 0 ? 1 : 0)) * kPartBytes; };
+        float w[kJLanes], l[kJLanes];
         float M = -INFINITY;
-        for (int j = 0; j < n; ++j) M = fmaxf(M, s_w[j][tid]);
+#pragma unroll
+        for (int i = 0; i < kJLanes; ++i) {
+            const int j = 32 * i + lane;
+            w[i] = -INFINITY;
+            l[i] = 0.f;
+            if (j < x.n) {
+                const float* ml = reinterpret_cast<const float*>(part(j) + kPartO);
+                w[i] = ml[mi];
+                l[i] = ml[kM + mi];
+            }
+            M = fmaxf(M, w[i]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float L = 0.f;
-        for (int j = 0; j < n; ++j) {
-            const float w = M == -INFINITY ? 0.f : exp2f(s_w[j][tid] - M);
-            L += w * reinterpret_cast<const float*>(part(j) + kPartO)[kM + m0 + tid];
-            s_w[j][tid] = w;
+#pragma unroll
+        for (int i = 0; i < kJLanes; ++i) {
+            w[i] = M == -INFINITY ? 0.f : exp2f(w[i] - M);
+            L += w[i] * l[i];
         }
-        s_M[tid] = M;
-        s_L[tid] = L;
-    }
-    __syncthreads();
-    const int64_t at0 = static_cast<int64_t>(g.row0) * a.heads + m0;
-    for (int x = tid; x < kJRows * kLatDv / 4; x += kJT) {
-        const int r = x / (kLatDv / 4), d = x % (kLatDv / 4);
-        if (m0 + r >= live) continue;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-            const float w = s_w[j][r];
-            const float4 v = reinterpret_cast<const float4*>(part(j))[static_cast<size_t>(m0 + r) * (kLatDv / 4) + d];
-            s.x += w * v.x;
-            s.y += w * v.y;
-            s.z += w * v.z;
-            s.w += w * v.w;
+        for (int j0 = 0; j0 < x.n; j0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = j0 + j < x.n ? reinterpret_cast<const float4*>(part(j0 + j))[mi * kJT + tid] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int at = j0 + j;
+                float wj = __shfl_sync(0xffffffffu, w[0], at & 31);
+#pragma unroll
+                for (int i = 1; i < kJLanes; ++i) {
+                    const float o = __shfl_sync(0xffffffffu, w[i], at & 31);
+                    if (at >= 32 * i) wj = o;
+                }
+                s.x += wj * v[j].x;
+                s.y += wj * v[j].y;
+                s.z += wj * v[j].z;
+                s.w += wj * v[j].w;
+            }
         }
-        const float f = s_L[r] > 0.f ? 1.f / s_L[r] : 0.f;
-        const bool any = s_L[r] > 0.f;
+        const bool any = L > 0.f;
+        const float f = any ? 1.f / L : 0.f;
         const __nv_bfloat162 b0 = __floats2bfloat162_rn(any ? s.x * f : 0.f, any ? s.y * f : 0.f);
         const __nv_bfloat162 b1 = __floats2bfloat162_rn(any ? s.z * f : 0.f, any ? s.w * f : 0.f);
-        reinterpret_cast<uint2*>(out + (at0 + r) * kLatDv)[d] =
+        const int64_t at = static_cast<int64_t>(x.row0) * a.heads + mi;
+        reinterpret_cast<uint2*>(out + at * kLatDv)[tid] =
             make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
-        if (d == 0) lse[at0 + r] = any ? (s_M[r] + log2f(s_L[r])) * 0.69314718055994531f : -INFINITY;
+        if (tid == 0) lse[at] = any ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
     }
 }
 
@@ -748,6 +853,7 @@ extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int
     const int rc = check_chunk(B, row_off, n_rows, heads, q, tok_off, n_tokens, pages, window, sinks, scale, status);
     if (rc) return rc;
     if (sel && (k <= 0 || window || sinks)) return ECHO_EINVAL;
+    if (sel && k > kMaxLen) return ECHO_EUNSUPPORTED;
     if (n_rows == 0) return ECHO_OK;
     if (!out || !lse || !ws || !is_aligned(out, 16) || !is_aligned(ws, 256)) return ECHO_EINVAL;
     if (ws_bytes < echo_mla_chunk_workspace_size(n_rows, heads, B)) return ECHO_EINVAL;
@@ -759,6 +865,7 @@ extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int
     uint8_t* const w = static_cast<uint8_t*>(ws);
     Plan plan;
     plan.head = reinterpret_cast<PlanHead*>(w);
+    plan.cut = reinterpret_cast<Cut*>(w + 256);
     plan.group = reinterpret_cast<Group*>(w + l.group);
     plan.cum = reinterpret_cast<int64_t*>(w + l.cum);
     plan.part = w + l.part;
@@ -773,7 +880,6 @@ extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int
     ECHO_CUDA_OK(launch_after(chunk_kernel, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan,
                               scale * 1.4426950408889634f, out, lse));
     if (plan.clusters > 1)
-        ECHO_CUDA_OK(launch_after(chunk_join_kernel, dim3(static_cast<unsigned>(plan.clusters - 1), kM / kJRows), kJT, 0, s,
-                                  a, plan, out, lse));
+        ECHO_CUDA_OK(launch_after(chunk_join_kernel, dim3(static_cast<unsigned>(16 * sm_count())), kJT, 0, s, a, plan, out, lse));
     return ECHO_OK;
 }

@@ -13,6 +13,8 @@ constexpr int kLatDqk = ECHO_MLA_DQK;            // 576
 constexpr int kLatDv = ECHO_MLA_DV;              // 512
 constexpr int64_t kLatRowBytes = kLatDqk * 2;    // 1152
 
+constexpr int64_t kMaxLen = ECHO_CHUNK_MAX_TOKENS;  // tile ends stay below 2^31
+
 // The arguments of a chunk call that the kernels read (device pointers).
 struct ChunkArgs {
     int B;
@@ -78,7 +80,7 @@ inline ChunkArgs chunk_args(int B, const int64_t* row_off, int64_t n_rows, int h
 
 // Rows [r0, r0 + n) of request b, its token rows from off on and its length.
 // False: the row bounds are inconsistent (n = 0).  Inconsistent token bounds,
-// more rows than tokens or more tokens than an int32 index holds leave len = 0.
+// more rows than tokens, or more than kMaxLen tokens leave len = 0.
 __device__ __forceinline__ bool chunk_request(const ChunkArgs& a, int b, int64_t* r0, int64_t* n, int64_t* off,
                                               int64_t* len) {
     const int64_t lo = a.row_off[b], hi = a.row_off[b + 1];
@@ -94,7 +96,7 @@ __device__ __forceinline__ bool chunk_request(const ChunkArgs& a, int b, int64_t
         set_status(a.status, ECHO_ST_BADDATA);
         return false;
     }
-    if (hi > lo && (!ok || *len < *n || *len > 0x7FFFFFFF)) {
+    if (hi > lo && (!ok || *len < *n || *len > kMaxLen)) {
         set_status(a.status, ECHO_ST_BADDATA);
         *len = 0;
     }
@@ -119,29 +121,35 @@ __device__ __forceinline__ PageView page_view(const ChunkArgs& a, int b, int64_t
     return v;
 }
 
-// Cache row of token t (t < 2^31), -1 when it has none.  *bad: its table entry leaves the pool.
-__device__ __forceinline__ int64_t token_row(const ChunkArgs& a, const PageView& v, uint32_t t, bool* bad) {
-    uint32_t e = 0, r = 0;
+// Table entry (from v.tab on) that holds token t (t < 2^31), and the token's offset in its page.
+__device__ __forceinline__ uint32_t page_of(const ChunkArgs& a, const PageView& v, uint32_t t, uint32_t* at) {
+    uint32_t e;
     if (a.page == 1) {
         e = t;
-    } else {
-        const uint64_t x = static_cast<uint64_t>(v.shift) + t;  // page may be near 2^31
-        if (x < 0xFFFFFFFFull) {
-            e = static_cast<uint32_t>(x) / a.page;
-            r = static_cast<uint32_t>(x) - e * a.page;
-        } else {
-            e = static_cast<uint32_t>(x / a.page);
-            r = static_cast<uint32_t>(x - static_cast<uint64_t>(e) * a.page);
-        }
+        *at = 0;
+        return e;
     }
-    const int32_t p = v.tab[e];
-    if (p < 0) return -1;
-    const int64_t row = static_cast<int64_t>(p) * a.page + r;
+    const uint64_t x = static_cast<uint64_t>(v.shift) + t;  // below 2^32: both are below 2^31
+    e = static_cast<uint32_t>(x) / a.page;
+    *at = static_cast<uint32_t>(x) - e * a.page;
+    return e;
+}
+
+// Cache row `at` of the page a table entry p >= 0 names, -1 (and *bad) when that leaves the pool.
+__device__ __forceinline__ int64_t page_row(const ChunkArgs& a, const PageView& v, int32_t p, uint32_t at, bool* bad) {
+    const int64_t row = static_cast<int64_t>(p) * a.page + at;
     if (row >= v.rows) {
         *bad = true;
         return -1;
     }
     return v.base + row;
+}
+
+// Cache row of token t, -1 when it has none.
+__device__ __forceinline__ int64_t token_row(const ChunkArgs& a, const PageView& v, uint32_t t, bool* bad) {
+    uint32_t at;
+    const int32_t p = v.tab[page_of(a, v, t, &at)];
+    return p < 0 ? -1 : page_row(a, v, p, at, bad);
 }
 
 // ---------------------------------------------------------------- shares of a row of units
@@ -184,14 +192,16 @@ __device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* scratch, int
     }
     if (lane == 31) scratch[warp] = x;
     __syncthreads();
-    int64_t before = 0, sum = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) before += scratch[w];
-        sum += scratch[w];
+    int64_t w = lane < NT / 32 ? scratch[lane] : 0;  // every warp scans the warps' sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
     __syncthreads();
-    *total = sum;
-    return before + x - v;
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : 0) + x - v;
 }
 
 // Sets a two-CTA cluster kernel up for `smem` bytes; how many of its clusters the device holds at
