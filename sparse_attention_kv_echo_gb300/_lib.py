@@ -169,8 +169,13 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(s):
     if s is None:
+        if _raw_stream is not None:  # the same handle as below, without making a Stream object (3 us a call)
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -370,12 +375,12 @@ def mla_decode(q, sel_slot, dev_kv, C, scale, out, lse, status, stream=None):
         _ptr(status), _stream(stream)))
 
 
-def _expect(call, name, t, dtype, shape):
-    # the layouts the C ABI takes: contiguous tensors of the given type, on the current device
-    if (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
-            or t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
-        raise ValueError(f"{call}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current "
-                         f"CUDA device, not {t.dtype} {tuple(t.shape)} on {t.device}")
+def _expect(call, dev, *tensors):
+    # the layouts the C ABI takes: contiguous tensors of the given type and shape, on the current device
+    for name, t, dtype, shape in tensors:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{call}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the current "
+                             f"CUDA device, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 class KVPages:
@@ -387,9 +392,10 @@ class KVPages:
     def __init__(self, page_tab: torch.Tensor, kv: torch.Tensor, page: int, req_rows: int = 0):
         if page < 1 or req_rows < 0:
             raise ValueError("KVPages: page >= 1 and req_rows >= 0")
-        _expect("KVPages", "page_tab", page_tab, torch.int32, (page_tab.numel(),))
-        _expect("KVPages", "kv", kv, torch.bfloat16, (kv.shape[0], MLA_DQK))
+        _expect("KVPages", torch.cuda.current_device(), ("page_tab", page_tab, torch.int32, (page_tab.numel(),)),
+                ("kv", kv, torch.bfloat16, (kv.shape[0], MLA_DQK)))
         self.page_tab, self.kv, self.page, self.req_rows = page_tab, kv, int(page), int(req_rows)
+        self.tokens = page_tab.numel() * self.page
         s = EchoPagesStruct()
         s.page_tab, s.kv, s.kv_rows = _ptr(page_tab), _ptr(kv), kv.shape[0]
         s.req_rows, s.page, s.reserved = self.req_rows, self.page, 0
@@ -400,27 +406,21 @@ class KVPages:
         """The slots of a LayerCache as pages of one row (a token that is not resident has no row)."""
         return cls(cache.tok2slot, cache.dev_kv, 1, cache.C)
 
-    def check(self, call, n_tokens):
-        if self.page_tab.numel() * self.page < n_tokens:
-            raise ValueError(f"{call}: page_tab has {self.page_tab.numel()} pages of {self.page}, fewer than {n_tokens} "
-                             "token rows need")
-
 
 def mla_chunk_workspace_size(n_rows: int, heads: int, B: int) -> int:
     return int(load().echo_mla_chunk_workspace_size(int(n_rows), int(heads), int(B)))
 
 
-def _check_chunk(call, row_off, q, tok_off, n_tokens, pages, lse, status, tok_end):
-    B = tok_off.shape[0] - 1
-    n, heads = q.shape[0], q.shape[1]
-    _expect(call, "row_off", row_off, torch.int64, (B + 1,))
-    _expect(call, "tok_off", tok_off, torch.int64, (B + 1,))
-    _expect(call, "q", q, torch.bfloat16, (n, heads, MLA_DQK))
-    _expect(call, "lse", lse, torch.float32, (n, heads))
-    _expect(call, "status", status, torch.int32, (1,))
+def _check_chunk(call, row_off, q, tok_off, n_tokens, pages, lse, status, tok_end, *more):
+    B, n, heads, dev = tok_off.shape[0] - 1, q.shape[0], q.shape[1], torch.cuda.current_device()
+    _expect(call, dev, ("row_off", row_off, torch.int64, (B + 1,)), ("tok_off", tok_off, torch.int64, (B + 1,)),
+            ("q", q, torch.bfloat16, (n, heads, MLA_DQK)), ("lse", lse, torch.float32, (n, heads)),
+            ("status", status, torch.int32, (1,)), *more)
     if tok_end is not None:
-        _expect(call, "tok_end", tok_end, torch.int64, (B,))
-    pages.check(call, n_tokens)
+        _expect(call, dev, ("tok_end", tok_end, torch.int64, (B,)))
+    if pages.tokens < n_tokens or pages.kv.get_device() != dev:
+        raise ValueError(f"{call}: the page table covers {pages.tokens} token rows, not {n_tokens}, or lies on another "
+                         "device")
     return B, n, heads
 
 
@@ -430,12 +430,13 @@ def mla_chunk(row_off, q, tok_off, n_tokens, pages, scale, out, lse, ws, status,
     the end of its context) over the cache `pages` (a KVPages): causal; window > 0: the last
     `window` tokens and the first `sinks`; sel [n,k] int32: the tokens listed for each row -> out
     [n,heads,512] bf16, lse [n,heads] f32.  ws: uint8, mla_chunk_workspace_size(n, heads, B)."""
-    B, n, heads = _check_chunk("mla_chunk", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end)
-    _expect("mla_chunk", "out", out, torch.bfloat16, (n, heads, MLA_DV))
-    k = 0
-    if sel is not None:
+    k, more = 0, ("out", out, torch.bfloat16, (q.shape[0], q.shape[1], MLA_DV))
+    if sel is None:
+        B, n, heads = _check_chunk("mla_chunk", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end, more)
+    else:
         k = sel.shape[-1]
-        _expect("mla_chunk", "sel", sel, torch.int32, (n, k))
+        B, n, heads = _check_chunk("mla_chunk", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end, more,
+                                   ("sel", sel, torch.int32, (q.shape[0], k)))
     _check("echo_mla_chunk", load().echo_mla_chunk(
         B, _ptr(row_off), n, heads, _ptr(q), _ptr(tok_off), _ptr(tok_end), int(n_tokens),
         ctypes.byref(pages.struct), _ptr(sel), k, int(window), int(sinks), float(scale), _ptr(out), _ptr(lse),
@@ -452,9 +453,9 @@ def mla_mass(row_off, q, lse, tok_off, n_tokens, pages, scale, mass, mass_out, s
     receives from the rows of an mla_chunk call (the same q, pages, window and sinks, and its lse),
     summed over rows and heads.  mass_out may be mass.  ws: uint8, mla_mass_workspace_size(n_tokens,
     B) (None: one is taken from torch's allocator for the call)."""
-    B, n, heads = _check_chunk("mla_mass", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end)
-    _expect("mla_mass", "mass", mass, torch.float32, (n_tokens,))
-    _expect("mla_mass", "mass_out", mass_out, torch.float32, (n_tokens,))
+    B, n, heads = _check_chunk("mla_mass", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end,
+                               ("mass", mass, torch.float32, (n_tokens,)),
+                               ("mass_out", mass_out, torch.float32, (n_tokens,)))
     if ws is None:
         ws = torch.empty(mla_mass_workspace_size(n_tokens, B), dtype=torch.uint8, device=q.device)
         if isinstance(stream, torch.cuda.Stream):
@@ -474,12 +475,14 @@ def evict_select(tok_off, n_tokens, slot2tok, mass, keep, evict_tok, evict_slot,
     `recent` tokens spared -> evict_tok / evict_slot [B,C] (ascending slots, -1 behind), evict_cnt [B]."""
     B = tok_off.shape[0] - 1
     C = slot2tok.numel() // B
-    _expect("evict_select", "tok_off", tok_off, torch.int64, (B + 1,))
-    _expect("evict_select", "slot2tok", slot2tok, torch.int32, (B * C,) if slot2tok.dim() == 1 else (B, C))
-    _expect("evict_select", "mass", mass, torch.float32, (n_tokens,))
-    _expect("evict_select", "evict_tok", evict_tok, torch.int32, (B, C))
-    _expect("evict_select", "evict_slot", evict_slot, torch.int32, (B, C))
-    _expect("evict_select", "evict_cnt", evict_cnt, torch.int32, (B,))
+    dev = torch.cuda.current_device()
+    _expect("evict_select", dev, ("tok_off", tok_off, torch.int64, (B + 1,)),
+            ("slot2tok", slot2tok, torch.int32, (B * C,) if slot2tok.dim() == 1 else (B, C)),
+            ("mass", mass, torch.float32, (n_tokens,)), ("evict_tok", evict_tok, torch.int32, (B, C)),
+            ("evict_slot", evict_slot, torch.int32, (B, C)), ("evict_cnt", evict_cnt, torch.int32, (B,)),
+            ("status", status, torch.int32, (1,)))
+    if tok_end is not None:
+        _expect("evict_select", dev, ("tok_end", tok_end, torch.int64, (B,)))
     _check("echo_evict_select", load().echo_evict_select(
         B, _ptr(tok_off), _ptr(tok_end), int(n_tokens), _ptr(slot2tok), C, _ptr(mass), int(keep), int(sinks),
         int(recent), _ptr(evict_tok), _ptr(evict_slot), _ptr(evict_cnt), _ptr(status), _stream(stream)))
@@ -490,9 +493,18 @@ def cache_release(tok_off, n_tokens, tok, cache, status, mass=None, tok_end=None
     resident in `cache`; with mass [n_tokens], their masses become 0."""
     B = tok_off.shape[0] - 1
     m = tok.shape[-1]
-    _expect("cache_release", "tok", tok, torch.int32, (B, m))
+    dev = torch.cuda.current_device()
+    _expect("cache_release", dev, ("tok_off", tok_off, torch.int64, (B + 1,)), ("tok", tok, torch.int32, (B, m)),
+            ("status", status, torch.int32, (1,)))
+    if tok_end is not None:
+        _expect("cache_release", dev, ("tok_end", tok_end, torch.int64, (B,)))
     if mass is not None:
-        _expect("cache_release", "mass", mass, torch.float32, (n_tokens,))
+        _expect("cache_release", dev, ("mass", mass, torch.float32, (n_tokens,)))
+    whole = getattr(cache, "parent", cache)             # of a CacheView
+    requests = cache.B if whole is cache else cache.b1 - cache.b0
+    if whole.n_tokens < n_tokens or requests != B:
+        raise ValueError(f"cache_release: a cache of {requests} requests and {whole.n_tokens} token rows, not {B} and "
+                         f"{n_tokens}")
     _check("echo_cache_release", load().echo_cache_release(
         B, _ptr(tok_off), _ptr(tok_end), int(n_tokens), _ptr(tok), m, ctypes.byref(cache.struct), _ptr(mass),
         _ptr(status), _stream(stream)))

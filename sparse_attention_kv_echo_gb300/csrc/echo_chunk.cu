@@ -20,7 +20,7 @@
 // Neither product is done twice, and the softmax needs nothing from the other
 // CTA.  Warps of a CTA: 0-3 softmax (thread = TMEM lane; the two threads of a
 // row exchange their tile maxima in shared memory), 4-7 gather K, 8-11 gather V
-// and Q (16-byte cp.async: any row for any token; two stages of each, K in
+// (16-byte cp.async: any row for any token; two stages of each, K in
 // thirds that are refilled as their MMAs end), 12 of CTA 0 issues the MMAs, 13
 // and 14 report what has landed in their CTA to it (one barrier for both CTAs: each
 // wait costs the issuing warp a hundred cycles).  QK of tile t + 1 is
@@ -54,11 +54,16 @@ constexpr int kChunks = 1;               // parts in which K of a tile comes and
 constexpr uint32_t kKBytes = kAtoms * kKAtom;
 constexpr uint32_t kVBytes = 4 * kVAtom;
 constexpr uint32_t kPBytes = 64 * 128;
-constexpr uint32_t kTmemCols = 512;      // O [0, 256) | S0 [256, 288) | S1 [288, 320)
+constexpr uint32_t kTmemCols = 512;      // O [0, 256) | S buffers of 32 columns
+constexpr int kSBufs = 4;                // two would hold QK of tile t up until P of tile t - 2 is written
 constexpr uint32_t kSCol = 256;
+// Tokens that one or two groups read come from memory, whose latency two stages do not cover:
+// their rows are brought to L2 this many tiles ahead of the copy (32 ragged decode rows 72 -> 67 us).
+// Tokens that many groups read are in L2 already (2048 rows of 8192 tokens 3015 -> 3087 us with it).
+constexpr int kAhead = 1;
 constexpr float kLazy = 8.f;
-constexpr int kOver = 3;                 // a group's fixed cost in tiles
-constexpr int kMinUnits = 4;             // least units per cluster
+constexpr int kOver = 5;                 // a group's fixed cost in tiles
+constexpr int kMinUnits = 2;             // least units per cluster
 constexpr int kMaxClusters = 96;         // bounds the workspace (the device has 76 pairs of SMs)
 constexpr uint32_t kIdescS = idesc_bf16_f32(kM, kTok);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kM, 256) | (1u << 16);  // B (V) MN-major
@@ -97,6 +102,7 @@ struct Plan {
     uint8_t* part;  // [2 * kMaxClusters] partial results
     int cap;
     int clusters;
+    int ahead;      // tiles that K rows are brought to L2 ahead of their copy, 0: not
 };
 
 __host__ __device__ __forceinline__ int rows_per_group(int heads, bool sel) { return sel ? 1 : kM / heads; }
@@ -255,15 +261,17 @@ struct Gather {
         }
         if (t >= 0) entry = pv.tab[page_of(a, pv, static_cast<uint32_t>(t), &at)];
     }
-    __device__ __forceinline__ void start(const ChunkArgs& a, const Piece& p, int r) {
+    // r: token within the tile; ahead: tiles to start past the piece's first.
+    __device__ __forceinline__ void start(const ChunkArgs& a, const Piece& p, int r, int ahead = 0) {
         sel = a.sel ? a.sel + static_cast<int64_t>(p.g.row0) * a.k : nullptr;
         pv = page_view(a, p.g.req, p.g.off);
         lo_tok = p.g.pos0 + p.g.rows + p.g.kept - p.g.nv;
-        v = p.lo * kTok + r;
         bad = false;
         at = 0;
-        const int t0 = token(p, v);
-        tok = p.lo + 1 < p.hi ? token(p, v + kTok) : -1;
+        const int64_t first = static_cast<int64_t>(p.lo + ahead) * kTok + r, end = static_cast<int64_t>(p.hi) * kTok;
+        v = static_cast<int>(min(first, end));  // at the end: nothing to look up any more
+        const int t0 = v < end ? token(p, v) : -1;
+        tok = v < end - kTok ? token(p, v + kTok) : -1;
         look(a, p, t0);
     }
     // The cache row of the current tile's token, -1 when it has none.
@@ -274,29 +282,36 @@ struct Gather {
         return r;
     }
     __device__ __forceinline__ void next(const ChunkArgs& a, const Piece& p) {
-        v += kTok;
-        const int t = tok;
-        tok = v + kTok < p.hi * kTok ? token(p, v + kTok) : -1;
+        const int t = tok, end = p.hi * kTok;
+        v = min(v + kTok, end);
+        tok = v < end - kTok ? token(p, v + kTok) : -1;
         look(a, p, t);
     }
 };
 
 // ---------------------------------------------------------------- attention
+constexpr int kValid = 8;
+static_assert(kValid >= kSBufs + 3, "valid flags");
+
 struct Ctl {
     // here: landed in this CTA; the *_ready barriers of CTA 0: landed in both
     uint64_t q_full, q_ready;                            // Q of a group
     uint64_t k_full[2][kChunks], k_ready[2][kChunks];    // a third of a stage's K
-    uint64_t k_free[2][kChunks];                         // its MMAs are done; the last third: S of the tile is ready
+    uint64_t k_free[2][kChunks];                         // its MMAs are done
     uint64_t v_full[2];                                  // V of a stage
     uint64_t pv_ready[2];                                // V, and P of the tile, in both CTAs
     uint64_t pv_done[2];                                 // P V of a tile done: V stage and P buffer free, O ready
+    uint64_t s_full[kSBufs];                             // S of a tile done
+    uint64_t s_free[kSBufs];                             // S of a tile has been read in both CTAs
     uint64_t drain[2];
     uint32_t tmem;
     int abort;
     int first;                                           // the share's first group
     float mx[2][2][64];                                  // tile maxima by (tile parity, token half, row)
     float l[2][2][64];                                   // sums by (piece parity, token half, row)
-    alignas(16) uint8_t valid[4][kTok];                  // tokens of a tile that have a row
+    // tokens of a tile that have a row: written for tile t when QK of t - 2 is done, hence S of t - 6 read
+    // and tile t - 7 finished
+    alignas(16) uint8_t valid[kValid][kTok];
 };
 constexpr uint32_t kSmem = kQBytes + 2 * kKBytes + 2 * kVBytes + 2 * kPBytes + ((sizeof(Ctl) + 15u) & ~15u);
 static_assert(kSmem <= 227u * 1024u, "chunk shared memory");
@@ -318,12 +333,12 @@ __device__ __forceinline__ bool softmax_sync_or(bool v) {
 // The MMAs of stage ST.  The stage is a constant so that every descriptor is one too: with
 // descriptors computed from a variable stage an MMA took 100 cycles to issue, four times what it runs.
 template <int ST>
-__device__ __forceinline__ void issue_qk(uint32_t tmem, uint32_t sQ, uint32_t sK, int ch) {
+__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t sQ, uint32_t sK, int ch) {
     const uint64_t ad = sw128_kmajor_desc(sQ), bd = sw128_kmajor_desc(sK + ST * kKBytes);
 #pragma unroll
     for (int kk = 0; kk < 4 * kAtoms; ++kk)
         if (kk / (4 * kAtoms / kChunks) == ch)
-            mma2_bf16(tmem + kSCol + ST * 32u, ad + (((kk >> 2) * kQAtom + (kk & 3) * 32u) >> 4),
+            mma2_bf16(d, ad + (((kk >> 2) * kQAtom + (kk & 3) * 32u) >> 4),
                       bd + (((kk >> 2) * kKAtom + (kk & 3) * 32u) >> 4), kIdescS, kk > 0 ? 1u : 0u);
 }
 template <int ST>
@@ -338,7 +353,7 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t sP, uint32_t sV
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    chunk_kernel(ChunkArgs a, Plan plan, float scale_log2, uint16_t* __restrict__ out, float* __restrict__ lse) {
+    chunk_kernel(ChunkArgs a, Plan plan, const __grid_constant__ CUtensorMap qmap, float scale_log2, uint16_t* __restrict__ out, float* __restrict__ lse) {
     extern __shared__ __align__(1024) uint8_t chunk_smem[];  // the swizzled tiles need 1024 bytes
     uint8_t* const gbase = chunk_smem;
     const uint32_t base = smem_addr(gbase);
@@ -355,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     volatile int* const abort = &ctl->abort;
 
     if (tid == 0) {
-        mbar_init(smem_addr(&ctl->q_full), kLoad);
+        mbar_init(smem_addr(&ctl->q_full), 1);
         mbar_init(smem_addr(&ctl->q_ready), 2);
         for (int i = 0; i < 2; ++i) {
             for (int j = 0; j < kChunks; ++j) {
@@ -367,9 +382,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&ctl->pv_ready[i]), 2 * kSoftmax / 32 + 2);
             mbar_init(smem_addr(&ctl->pv_done[i]), 1);
         }
+        for (int i = 0; i < kSBufs; ++i) {
+            mbar_init(smem_addr(&ctl->s_full[i]), 1);
+            mbar_init(smem_addr(&ctl->s_free[i]), 2 * kSoftmax / 32);
+        }
         for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&ctl->drain[i]), 1);
         ctl->abort = 0;
         fence_barrier_init();
+        prefetch_tmap(&qmap);
     }
     if (warp == 0) tmem_alloc2(smem_addr(&ctl->tmem), kTmemCols);
     pdl_wait();
@@ -434,13 +454,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.f;
             for (int it = p.lo; it < p.hi; ++it, ++t) {
                 const uint32_t st = t & 1u;
-                ok = ok && mbar_wait(smem_addr(&ctl->k_free[st][kChunks - 1]), (t >> 1) & 1u, abort);
+                ok = ok && mbar_wait(smem_addr(&ctl->s_full[t & (kSBufs - 1)]), (t / kSBufs) & 1u, abort);
                 tc_fence_after();
                 __syncwarp();
                 float s[32];
-                tmem_ld_x32(tmem + lane_base + kSCol + st * 32u, s);
+                tmem_ld_x32(tmem + lane_base + kSCol + (t & (kSBufs - 1)) * 32u, s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->s_free[t & (kSBufs - 1)]), 0);
                 const int v0 = it * kTok + half * 32;
-                const uint4* vf = reinterpret_cast<const uint4*>(&ctl->valid[t & 3u][half * 32]);
+                const uint4* vf = reinterpret_cast<const uint4*>(&ctl->valid[t & (kValid - 1)][half * 32]);
                 const uint4 f0 = vf[0], f1 = vf[1];
                 const bool all = ((f0.x & f0.y & f0.z & f0.w) & (f1.x & f1.y & f1.z & f1.w)) == 0x01010101u;
                 const bool clean = all && v0 + 32 <= vhi && (vb <= va || v0 >= vb || v0 + 32 <= va);
@@ -575,13 +598,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && walk.next(&p)) {
             if (p.hi == p.lo) continue;
-            const int mine = static_cast<int>(lane < 8 ? c : c ^ 1u) * 32 + 8 * w + (lane & 7);
+            const int mine = static_cast<int>(lane < 8 || lane >= 16 ? c : c ^ 1u) * 32 + 8 * w + (lane & 7);
             Gather own;
-            own.start(a, p, mine);
+            own.start(a, p, mine, lane >= 16 ? plan.ahead : 0);
             for (int it = p.lo; it < p.hi; ++it, ++t) {
                 const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
                 const int64_t row = own.row(a);
                 own.next(a, p);
+                if (plan.ahead && lane >= 16 && lane < 24 && row >= 0)
+                    prefetch_l2(a.kv + row * kLatRowBytes, kLatRowBytes);
                 const uint8_t* src[2];
                 uint32_t n[2], dst[2];
 #pragma unroll
@@ -602,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 2; ++i) cp_async_16(dst[i] + j * kKAtom, src[i] + 128 * j, n[i]);
                     cp_async_arrive_noinc(smem_addr(&ctl->k_full[st][ch]));
                     if (ch == 0) {
-                        if (lane < 16) ctl->valid[t & 3u][mine] = row < 0 ? 0 : 1;
+                        if (lane < 16) ctl->valid[t & (kValid - 1)][mine] = row < 0 ? 0 : 1;
                         mbar_arrive(smem_addr(&ctl->k_full[st][0]));
                     }
                 }
@@ -613,30 +638,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) *abort = 1;
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < 12) {
-        // ---- Q of a group, and V: this CTA's 256 dims of the tile's 64 tokens, 16 to a warp, copied like K
-        const int lt = tid - kSoftmax - kLoad, w = warp - 8, x = lane & 7, r4 = lane >> 3;
+        // ---- V: this CTA's 256 dims of the tile's 64 tokens, 16 to a warp, copied like K
+        const int w = warp - 8, x = lane & 7, r4 = lane >> 3;
         bool ok = true;
         while (ok && walk.next(&p)) {
             if (p.hi == p.lo) continue;
             Gather own;
             own.start(a, p, 16 * w + (lane & 15));
-            // Q once the group before has no QK left
-            if (t >= 1) ok = mbar_wait(smem_addr(&ctl->k_free[(t - 1) & 1u][kChunks - 1]), ((t - 1) >> 1) & 1u, abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            {
-                const int live = p.g.rows * a.heads - static_cast<int>(c) * 64;
-                const uint8_t* const q = reinterpret_cast<const uint8_t*>(a.q) +
-                                         (static_cast<int64_t>(p.g.row0) * a.heads + static_cast<int64_t>(c) * 64) * kLatRowBytes;
-#pragma unroll 4
-                for (int i = lt; i < 64 * 72; i += kLoad) {
-                    const int r = i / 72, y = i - r * 72;
-                    const bool in = r < live;
-                    cp_async_16(sQ + sw_offset(r, y, kQAtom), in ? q + static_cast<int64_t>(r) * kLatRowBytes + 16 * y : a.kv,
-                                in ? 16u : 0u);
-                }
-                cp_async_arrive_noinc(smem_addr(&ctl->q_full));
-            }
             for (int it = p.lo; it < p.hi; ++it, ++t) {
                 const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
                 const int64_t row = own.row(a);
@@ -678,17 +686,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
                     const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
                     if (qk) {
-                        // S(t - 2) has been read once its P is written
-                        if (t >= 2) ok = mbar_wait_cluster(smem_addr(&ctl->pv_ready[st]), ph ^ 1u, abort);
+                        if (t >= kSBufs)
+                            ok = mbar_wait_cluster(smem_addr(&ctl->s_free[t & (kSBufs - 1)]), ((t / kSBufs) & 1u) ^ 1u, abort);
 #pragma unroll
                         for (int ch = 0; ch < kChunks; ++ch) {
                             ok = ok && mbar_wait_cluster(smem_addr(&ctl->k_ready[st][ch]), ph, abort);
                             if (!ok) break;
                             tc_fence_after();
-                            if (st == 0) issue_qk<0>(tmem, sQ, sK, ch);
-                            else issue_qk<1>(tmem, sQ, sK, ch);
+                            const uint32_t d = tmem + kSCol + (t & (kSBufs - 1)) * 32u;
+                            if (st == 0) issue_qk<0>(d, sQ, sK, ch);
+                            else issue_qk<1>(d, sQ, sK, ch);
                             mma2_commit_both(smem_addr(&ctl->k_free[st][ch]));
                         }
+                        if (ok) mma2_commit_both(smem_addr(&ctl->s_full[t & (kSBufs - 1)]));
                     } else {  // O += P V
                         ok = mbar_wait_cluster(smem_addr(&ctl->pv_ready[st]), ph, abort);
                         if (!ok) break;
@@ -712,9 +722,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && walk.next(&p)) {
             if (p.hi == p.lo) continue;
-            ok = mbar_wait(smem_addr(&ctl->q_full), groups & 1u, abort);
+            // Q of the group, once the group before has no QK left.  Its (row, head) pairs are consecutive in q;
+            // pairs past the group's own are another group's, or zeros, and their results are dropped
+            if (t >= 1) ok = mbar_wait(smem_addr(&ctl->k_free[(t - 1) & 1u][kChunks - 1]), ((t - 1) >> 1) & 1u, abort);
+            if (!ok) break;
+            if (elect_one()) {
+                const uint32_t bar = smem_addr(&ctl->q_full);
+                mbar_arrive_expect_tx(bar, kQBytes);
+                for (int i = 0; i < kAtoms; ++i)
+                    tma_load_2d(sQ + i * kQAtom, &qmap, bar, i * 128, p.g.row0 * a.heads + static_cast<int>(c) * 64);
+            }
+            __syncwarp();
+            ok = mbar_wait(smem_addr(&ctl->q_full), groups & 1u, nullptr);  // always: the load lands before the CTA ends
             ++groups;
-            fence_proxy_async_smem();
             if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->q_ready), 0);
             for (int it = p.lo; ok && it < p.hi; ++it, ++t)
                 for (int ch = 0; ok && ch < kChunks; ++ch) {
@@ -750,6 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // A block takes (cut group, (row, head)) tasks in turn: thread = 4 dims, and every warp
 // works out the pieces' weights for itself (lane = piece).
 constexpr int kJT = kLatDv / 4;
+constexpr int kJBatch = 8;  // pieces in flight
 constexpr int kJLanes = (kMaxClusters + 31) / 32;
 
 __global__ void __launch_bounds__(kJT) chunk_join_kernel(ChunkArgs a, Plan plan, uint16_t* __restrict__ out,
@@ -777,6 +798,13 @@ __global__ void __launch_bounds__(kJT) chunk_join_kernel(ChunkArgs a, Plan plan,
         if (mi >= x.live) continue;
         // piece j is share i0 + j: the first starts at tile 0 (second slot), the others within (first slot)
         const auto part = [&](int j) { return plan.part + static_cast<size_t>(2 * (x.i0 + j) + (j == 0 ? 1 : 0)) * kPartBytes; };
+        const auto load = [&](int j0, float4 (&v)[kJBatch]) {
+#pragma unroll
+            for (int j = 0; j < kJBatch; ++j)
+                v[j] = j0 + j < x.n ? reinterpret_cast<const float4*>(part(j0 + j))[mi * kJT + tid] : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float4 v[kJBatch];
+        load(0, v);  // in flight while the weights are worked out
         float w[kJLanes], l[kJLanes];
         float M = -INFINITY;
 #pragma unroll
@@ -802,13 +830,10 @@ __global__ void __launch_bounds__(kJT) chunk_join_kernel(ChunkArgs a, Plan plan,
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j0 = 0; j0 < x.n; j0 += 8) {
-            float4 v[8];
+        for (int j0 = 0; j0 < x.n; j0 += kJBatch) {
+            if (j0 > 0) load(j0, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = j0 + j < x.n ? reinterpret_cast<const float4*>(part(j0 + j))[mi * kJT + tid] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kJBatch; ++j) {
                 const int at = j0 + j;
                 float wj = __shfl_sync(0xffffffffu, w[0], at & 31);
 #pragma unroll
@@ -870,6 +895,9 @@ extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int
     plan.cum = reinterpret_cast<int64_t*>(w + l.cum);
     plan.part = w + l.part;
     plan.cap = static_cast<int>(cap);
+    plan.ahead = cap <= 2 * B ? kAhead : 0;
+    CUtensorMap qmap;
+    if (encode_tmap_bytes_2d(&qmap, q, kLatRowBytes, static_cast<uint64_t>(n_rows) * heads, 128, 64)) return ECHO_ECUDA;
     static int cached[64];
     plan.clusters = cluster2_count(chunk_kernel, kThreads, kSmem, kMaxClusters, cached);
     if (plan.clusters < 1) return ECHO_ECUDA;
@@ -877,7 +905,7 @@ extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int
     ECHO_CUDA_OK(prefer_max_shared(chunk_join_kernel));
     chunk_plan_kernel<<<1, kPT, 0, s>>>(a, plan);
     ECHO_CUDA_OK(cudaGetLastError());
-    ECHO_CUDA_OK(launch_after(chunk_kernel, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan,
+    ECHO_CUDA_OK(launch_after(chunk_kernel, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan, qmap,
                               scale * 1.4426950408889634f, out, lse));
     if (plan.clusters > 1)
         ECHO_CUDA_OK(launch_after(chunk_join_kernel, dim3(static_cast<unsigned>(16 * sm_count())), kJT, 0, s, a, plan, out, lse));

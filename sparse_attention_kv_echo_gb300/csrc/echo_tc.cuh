@@ -105,6 +105,11 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+// Bring `bytes` (a multiple of 16) at p (16-byte aligned) to L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
+}
+
 // ---------------------------------------------------------------- one elected lane
 // True on one lane of a converged warp.  MMAs issued under it take the hardware's own
 // rate; issued by a thread that left its warp, each costs at least 44 cycles (measured,
