@@ -767,12 +767,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- join
-// A block takes (cut group, (row, head)) tasks in turn: thread = 4 dims, and every warp
-// works out the pieces' weights for itself (lane = piece).
-constexpr int kJT = kLatDv / 4;
-constexpr int kJBatch = 8;  // pieces in flight
+constexpr int kJT = 128;
 constexpr int kJLanes = (kMaxClusters + 31) / 32;
 
+// One (row, head) pair of a cut group: this warp's dims 4 (first + 32 i) of it, i < NV, lane = piece for the
+// pieces' weights, the loads of the first pieces in flight meanwhile.
+template <int NV>
+__device__ __forceinline__ void join_pair(const Plan& plan, const Cut& x, int mi, int first, int heads, uint16_t* out,
+                                          float* lse) {
+    constexpr int kBatch = 8 / NV;  // pieces in flight
+    const int lane = threadIdx.x & 31;
+    // piece j is share i0 + j: the first starts at tile 0 (second slot), the others within (first slot)
+    const auto part = [&](int j) { return plan.part + static_cast<size_t>(2 * (x.i0 + j) + (j == 0 ? 1 : 0)) * kPartBytes; };
+    float4 v[kBatch][NV];
+    const auto load = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                v[j][i] = j0 + j < x.n ? reinterpret_cast<const float4*>(part(j0 + j))[mi * (kLatDv / 4) + first + 32 * i]
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    float w[kJLanes], l[kJLanes];
+    float M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kJLanes; ++i) {
+        const int j = 32 * i + lane;
+        w[i] = -INFINITY;
+        l[i] = 0.f;
+        if (j < x.n) {
+            const float* ml = reinterpret_cast<const float*>(part(j) + kPartO);
+            w[i] = ml[mi];
+            l[i] = ml[kM + mi];
+        }
+        M = fmaxf(M, w[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJLanes; ++i) {
+        w[i] = M == -INFINITY ? 0.f : exp2f(w[i] - M);
+        L += w[i] * l[i];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float4 s[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < x.n; j0 += kBatch) {
+        if (j0 > 0) load(j0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int at = j0 + j;
+            float wj = __shfl_sync(0xffffffffu, w[0], at & 31);
+#pragma unroll
+            for (int i = 1; i < kJLanes; ++i) {
+                const float o = __shfl_sync(0xffffffffu, w[i], at & 31);
+                if (at >= 32 * i) wj = o;
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                s[i].x += wj * v[j][i].x;
+                s[i].y += wj * v[j][i].y;
+                s[i].z += wj * v[j][i].z;
+                s[i].w += wj * v[j][i].w;
+            }
+        }
+    }
+    const bool any = L > 0.f;
+    const float f = any ? 1.f / L : 0.f;
+    const int64_t at = static_cast<int64_t>(x.row0) * heads + mi;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const __nv_bfloat162 b0 = __floats2bfloat162_rn(any ? s[i].x * f : 0.f, any ? s[i].y * f : 0.f);
+        const __nv_bfloat162 b1 = __floats2bfloat162_rn(any ? s[i].z * f : 0.f, any ? s[i].w * f : 0.f);
+        reinterpret_cast<uint2*>(out + at * kLatDv)[first + 32 * i] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+    }
+    if (first == 0) lse[at] = any ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Many pairs: a warp to each.  Few (long contexts cut into many pieces): the four warps of a block share one.
 __global__ void __launch_bounds__(kJT) chunk_join_kernel(ChunkArgs a, Plan plan, uint16_t* __restrict__ out,
                                                          float* __restrict__ lse) {
     __shared__ Cut s_cut[kMaxClusters];
@@ -792,69 +869,17 @@ __global__ void __launch_bounds__(kJT) chunk_join_kernel(ChunkArgs a, Plan plan,
         if (lane == 0) s_n = n;
     }
     __syncthreads();
-    for (int task = blockIdx.x; task < s_n * kM; task += gridDim.x) {
-        const Cut x = s_cut[task / kM];
-        const int mi = task % kM;
-        if (mi >= x.live) continue;
-        // piece j is share i0 + j: the first starts at tile 0 (second slot), the others within (first slot)
-        const auto part = [&](int j) { return plan.part + static_cast<size_t>(2 * (x.i0 + j) + (j == 0 ? 1 : 0)) * kPartBytes; };
-        const auto load = [&](int j0, float4 (&v)[kJBatch]) {
-#pragma unroll
-            for (int j = 0; j < kJBatch; ++j)
-                v[j] = j0 + j < x.n ? reinterpret_cast<const float4*>(part(j0 + j))[mi * kJT + tid] : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-        float4 v[kJBatch];
-        load(0, v);  // in flight while the weights are worked out
-        float w[kJLanes], l[kJLanes];
-        float M = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kJLanes; ++i) {
-            const int j = 32 * i + lane;
-            w[i] = -INFINITY;
-            l[i] = 0.f;
-            if (j < x.n) {
-                const float* ml = reinterpret_cast<const float*>(part(j) + kPartO);
-                w[i] = ml[mi];
-                l[i] = ml[kM + mi];
-            }
-            M = fmaxf(M, w[i]);
+    const int pairs = s_n * kM;
+    if (pairs <= static_cast<int>(gridDim.x)) {
+        for (int task = blockIdx.x; task < pairs; task += gridDim.x) {
+            const Cut x = s_cut[task / kM];
+            if (task % kM < x.live) join_pair<1>(plan, x, task % kM, tid, a.heads, out, lse);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float L = 0.f;
-#pragma unroll
-        for (int i = 0; i < kJLanes; ++i) {
-            w[i] = M == -INFINITY ? 0.f : exp2f(w[i] - M);
-            L += w[i] * l[i];
+    } else {
+        for (int task = 4 * blockIdx.x + (tid >> 5); task < pairs; task += 4 * gridDim.x) {
+            const Cut x = s_cut[task / kM];
+            if (task % kM < x.live) join_pair<4>(plan, x, task % kM, lane, a.heads, out, lse);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j0 = 0; j0 < x.n; j0 += kJBatch) {
-            if (j0 > 0) load(j0, v);
-#pragma unroll
-            for (int j = 0; j < kJBatch; ++j) {
-                const int at = j0 + j;
-                float wj = __shfl_sync(0xffffffffu, w[0], at & 31);
-#pragma unroll
-                for (int i = 1; i < kJLanes; ++i) {
-                    const float o = __shfl_sync(0xffffffffu, w[i], at & 31);
-                    if (at >= 32 * i) wj = o;
-                }
-                s.x += wj * v[j].x;
-                s.y += wj * v[j].y;
-                s.z += wj * v[j].z;
-                s.w += wj * v[j].w;
-            }
-        }
-        const bool any = L > 0.f;
-        const float f = any ? 1.f / L : 0.f;
-        const __nv_bfloat162 b0 = __floats2bfloat162_rn(any ? s.x * f : 0.f, any ? s.y * f : 0.f);
-        const __nv_bfloat162 b1 = __floats2bfloat162_rn(any ? s.z * f : 0.f, any ? s.w * f : 0.f);
-        const int64_t at = static_cast<int64_t>(x.row0) * a.heads + mi;
-        reinterpret_cast<uint2*>(out + at * kLatDv)[tid] =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
-        if (tid == 0) lse[at] = any ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
     }
 }
 
