@@ -17,7 +17,8 @@ quantised query) and issues the calls of a step:
                           recall joins the step's stream after both;
     echo_mla_decode    -> (attention=True) sparse MLA attention of each request
                           group over its selected slots, as soon as the group's
-                          rows are in the cache.
+                          rows are in the cache; with a shared pool
+                          echo_mla_chunk over the batch's selections in it.
 Every buffer keeps its address and size, so ``step`` can be captured into a
 CUDA graph and replayed; ``q_in``/``w_in`` are the inputs a graph reads.
 ``capture_host_step`` captures the step together with its host I/O (inputs
@@ -84,8 +85,8 @@ class DecodeLayer:
         # pool_slots > 0: one cache pool of that many slots shared by every request (the worker's
         # device cache) instead of C slots per request; one request group
         self.pool_slots = int(pool_slots)
-        if self.pool_slots and (cross_layer or attention):
-            raise ValueError("the shared pool goes with neither cross_layer nor attention")
+        if self.pool_slots and cross_layer:
+            raise ValueError("the shared pool does not go with cross_layer")
         if self.cross_layer or self.pool_slots:
             groups = 1
         if groups is None:
@@ -128,8 +129,14 @@ class DecodeLayer:
             if self.cache.row_bytes != 2 * L.MLA_DQK:
                 raise ValueError("attention needs 576-dim bf16 cache rows")
             self.mla_q = torch.zeros((self.B, L.MLA_HEADS, L.MLA_DQK), dtype=torch.bfloat16, device=device)
-            self.attn_out = torch.zeros((self.B, L.MLA_HEADS, L.MLA_DV), **f32)
+            self.attn_out = torch.zeros((self.B, L.MLA_HEADS, L.MLA_DV), device=device,
+                                        dtype=torch.bfloat16 if self.pool_slots else torch.float32)
             self.attn_lse = torch.zeros((self.B, L.MLA_HEADS), **f32)
+            if self.pool_slots:  # the pool's rows belong to no request: the paged call, one row per request
+                self.pages = L.KVPages(self.cache.tok2slot, self.cache.dev_kv, 1)
+                self.row_off = torch.arange(self.B + 1, dtype=torch.int64, device=device)
+                self.attn_ws = torch.zeros(L.mla_chunk_workspace_size(self.B, L.MLA_HEADS, self.B), dtype=torch.uint8,
+                                           device=device)
         self.views = [] if self.pool_slots else [self.cache.view(b0, b1) for b0, b1 in self.groups]
         # candidate lists: the score kernel lists each request's tokens above a cut that top-k sets
         # for the next step, and top-k selects among them when they hold the top-k
@@ -200,7 +207,7 @@ class DecodeLayer:
             L.topk_select(off, self.n_tokens, self.scores, self.k, self.hist[sl], self.theta[sl], self.alpha,
                           self.sel_idx[sl], self.kth[sl], self.status, stats=self.stats, stream=stream, tok_end=end)
 
-    def _step_pool(self, q, w, main, out_host):
+    def _step_pool(self, q, w, main, out_host, mla_q):
         # per-request scores and marks; the early fetch, top-k's slots and the cache step on the pool
         n, end = self.n_tokens, self.tok_end
         self._quantize(q, w, main)
@@ -228,6 +235,9 @@ class DecodeLayer:
             with torch.cuda.stream(side):
                 self._write_out(out_host, 0, self.B)
         main.wait_stream(side)
+        if self.attention:  # both copies are on main or side
+            L.mla_chunk(self.row_off, mla_q, self.tok_off, n, self.pages, self.mla_scale, self.attn_out, self.attn_lse,
+                        self.attn_ws, self.status, tok_end=end, sel=self.sel_idx, stream=main)
 
     def _step_seeded(self, q, w, main, out_host, mla_q):
         # scores without threshold bits or snapshot; top-k and the cache step take the seeded set
@@ -274,7 +284,8 @@ class DecodeLayer:
         written there by a kernel as soon as its cache step is done, while the late misses
         are still being recalled.
         mla_q: with attention=True, the step's MLA queries [B,128,576] bf16 (default
-        self.mla_q); attn_out / attn_lse receive the attention of every request.
+        self.mla_q); attn_out (f32; bf16 with a shared pool) / attn_lse receive the attention of
+        every request.
         seeded: (cross_layer) the early set is the one seed_from enqueued for this step."""
         q = self.q_in if q is None else q
         if self.attention:
@@ -282,7 +293,7 @@ class DecodeLayer:
         w = self.w_in if w is None else w
         main = torch.cuda.current_stream() if stream is None else stream
         if self.pool_slots:
-            self._step_pool(q, w, main, out_host)
+            self._step_pool(q, w, main, out_host, mla_q)
             return
         if seeded:
             if not self.cross_layer:
@@ -417,7 +428,7 @@ class DecodeLayer:
         # quantize, then per group: score (+ early fetch) + top-k + cache step + late recall
         att = 1 if self.attention else 0
         if self.pool_slots:  # quantize, score, top-k, select, cache step, recall, slots (+ marks, early fetch)
-            return 7 + (2 if self.predictor else 0)
+            return 7 + (2 if self.predictor else 0) + 3 * att  # attention: plan, tiles, join
         if not self.predictor:
             return 5 + att
         if self.cross_layer:  # quantize, score, top-k, cache step, recall + seed, early fetch (seeded steps)

@@ -407,3 +407,79 @@ def test_wrapper_refuses(what):
         sel = torch.zeros((1, 4), dtype=torch.int32, device=dev)
     with pytest.raises(ValueError):
         L.mla_chunk(row_off, q, tok_off, n, pages, bt.scale, out, lse, ws, st, tok_end=tok_end, sel=sel)
+
+
+# ---------------------------------------------------------------- in the framework's own paths
+def _plain_selected(q, host, off, sel, scale):
+    """A Batch over the host rows, one row each: the attention of the rows over their listed tokens."""
+    bt = P.Batch.__new__(P.Batch)
+    B = len(off) - 1
+    bt.lens, bt.heads, bt.page, bt.req_rows = [int(off[b + 1] - off[b]) for b in range(B)], q.shape[1], 1, 0
+    bt.tok_off, bt.tok_end = torch.as_tensor(off), torch.as_tensor(off)[1:]
+    bt.n_tokens, bt.n, bt.kv, bt.q, bt.scale = int(off[-1]), q.shape[0], host, q, scale
+    bt.rows = [q.shape[0]] if B == 1 else [1] * B
+    bt.row_off = torch.tensor([0] + bt.rows).cumsum(0)
+    bt.tab = torch.arange(int(off[-1]), dtype=torch.int32)
+    return bt
+
+
+@pytest.mark.parametrize("heads", [128, 16])
+def test_prefill_blocks_attend_over_their_selections(heads):
+    from sparse_attention_kv_echo_gb300 import workloads as wl
+    from sparse_attention_kv_echo_gb300.prefill import PrefillRunner
+    w = wl.scaled(wl.WORKLOADS["prefill"], "attn", lengths=(700,), k=96, C=704, prefill_block=200)
+    k8, ks = wl.make_keys(w, 0)
+    host = wl.make_host_pool(w, 0, pin=True)
+    pr = PrefillRunner(k8.to(dev), ks.to(dev), w.k, w.C, host, w.prefill_block, attention=True, heads=heads)
+    g = torch.Generator().manual_seed(5)
+    got = []
+    for i in range(pr.blocks()):                     # enqueued back to back: block i attends beside block i + 1
+        q, wt = wl.make_prefill_queries(w, i)
+        mq = torch.randn((q.shape[0], heads, 576), generator=g).to(torch.bfloat16)
+        _, R = pr.block(i, q.to(dev), wt.to(dev), mla_q=mq.to(dev))
+        with torch.cuda.stream(pr.copy):
+            got.append((mq, pr.sel_idx[:R].clone(), pr.attn_out[:R].clone(), pr.attn_lse[:R].clone()))
+    torch.cuda.synchronize()
+    assert int(pr.status.item()) == 0
+    for i, (mq, sel, out, lse) in enumerate(got):
+        rows = torch.tensor([0, 1, len(mq) // 2, len(mq) - 1])
+        sel = sel.cpu()
+        p = i * w.prefill_block + rows
+        assert torch.all((sel[rows] >= 0).sum(1) == torch.clamp(p + 1, max=w.k))
+        bt = _plain_selected(mq[rows], host, [0, w.total_tokens], sel[rows], pr.mla_scale)
+        _compare(bt, (out.cpu()[rows], lse.cpu()[rows]), sel=sel[rows])
+    with pytest.raises(ValueError):
+        pr.block(0, q.to(dev), wt.to(dev))
+
+
+@pytest.mark.parametrize("hold_early,graph", [(False, True), (True, False)])
+def test_a_shared_pool_attends(hold_early, graph):
+    from sparse_attention_kv_echo_gb300 import DecodeLayer
+    from sparse_attention_kv_echo_gb300 import workloads as wl
+    w = wl.scaled(wl.WORKLOADS["batch"], "poolattn", B=3, lengths=(1500, 90, 2100), k=128, C=512)
+    off = wl.tok_offsets(w.lengths)
+    k8, ks = wl.make_keys(w, 0)
+    host = wl.make_host_pool(w, 0, pin=True)
+    lay = DecodeLayer(off, k8.to(dev), ks.to(dev), w.k, w.C, host, pool_slots=1024, hold_early=hold_early, attention=True)
+    main = torch.cuda.Stream()
+    lay.w_in.copy_(wl.make_weights(w, 0).to(dev))
+    torch.cuda.synchronize()
+    if graph:
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg, stream=main):
+            lay.step(stream=main)
+        torch.cuda.synchronize()
+        lay.reset()
+    qs = wl.QueryStream(w, 0)
+    g = torch.Generator().manual_seed(9)
+    for _ in range(3):
+        mq = torch.randn((3, L.MLA_HEADS, 576), generator=g).to(torch.bfloat16)
+        with torch.cuda.stream(main):
+            lay.q_in.copy_(qs.next().to(dev))
+            lay.mla_q.copy_(mq.to(dev))
+            cg.replay() if graph else lay.step(stream=main)
+        torch.cuda.synchronize()
+        assert int(lay.status.item()) == 0
+        sel = lay.sel_idx.cpu()
+        bt = _plain_selected(mq, host, off, sel, lay.mla_scale)
+        _compare(bt, (lay.attn_out.cpu(), lay.attn_lse.cpu()), sel=sel)
