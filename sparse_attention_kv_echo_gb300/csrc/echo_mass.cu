@@ -596,10 +596,10 @@ extern "C" int echo_mla_mass(int B, const int64_t* row_off, int64_t n_rows, int 
     ECHO_CUDA_OK(prefer_max_shared(mass_join_kernel));
     mass_plan_kernel<<<1, kPT, 0, s>>>(a, plan);
     ECHO_CUDA_OK(cudaGetLastError());
-    ECHO_CUDA_OK(launch_after(mass_kernel, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan,
+    ECHO_CUDA_OK(launch_after(false, mass_kernel, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan,
                               qmap, scale * 1.4426950408889634f, lse, mass, mass_out, decay));
     if (plan.clusters > 1)
-        ECHO_CUDA_OK(launch_after(mass_join_kernel, dim3(static_cast<unsigned>(plan.clusters - 1)), kTok, 0, s, plan, mass,
+        ECHO_CUDA_OK(launch_after(false, mass_join_kernel, dim3(static_cast<unsigned>(plan.clusters - 1)), kTok, 0, s, plan, mass,
                                   mass_out, decay));
     return ECHO_OK;
 }

@@ -113,7 +113,7 @@ struct PageView {
 
 __device__ __forceinline__ PageView page_view(const ChunkArgs& a, int b, int64_t off) {
     PageView v;
-    const int64_t e = off / a.page;
+    const int64_t e = off < (1ll << 31) ? static_cast<uint32_t>(off) / a.page : off / a.page;
     v.tab = a.page_tab + e;
     v.shift = static_cast<uint32_t>(off - e * a.page);
     v.base = a.req_rows ? b * a.req_rows : 0;
@@ -155,7 +155,11 @@ __device__ __forceinline__ int64_t token_row(const ChunkArgs& a, const PageView&
 // ---------------------------------------------------------------- shares of a row of units
 // `parts` shares of `total` units (total >= parts): share i is units
 // [share_start(i), share_start(i + 1)).
-__device__ __forceinline__ int64_t share_start(int64_t total, int parts, int i) { return total * i / parts; }
+__device__ __forceinline__ int64_t share_start(int64_t total, int parts, int i) {
+    if (total < (1 << 24))  // parts is at most 128: a 32-bit division does
+        return static_cast<uint32_t>(total) * static_cast<uint32_t>(i) / static_cast<uint32_t>(parts);
+    return total * i / parts;
+}
 
 // The share that holds unit u.
 __device__ __forceinline__ int share_of(int64_t total, int parts, int64_t u) {
@@ -233,9 +237,10 @@ int cluster2_count(Kernel kernel, int threads, uint32_t smem, int most, int (&ca
     return cached[dev];
 }
 
-// Launch as a programmatic dependent of the kernel before it on the stream.
+// Launch, as a programmatic dependent of the kernel before it on the stream unless `plain` (for
+// kernels that let dependents start early; a kernel of another call may not).
 template <class... Args>
-cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+cudaError_t launch_after(bool plain, void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -245,7 +250,7 @@ cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, int threads, size_t
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = plain ? 0 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
