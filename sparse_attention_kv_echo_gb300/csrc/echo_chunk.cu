@@ -63,7 +63,7 @@ constexpr uint32_t kSCol = 256;
 constexpr int kAhead = 1;
 constexpr int kInline = 32;              // groups and requests of a call that needs no plan kernel (at most a warp's lanes)
 constexpr float kLazy = 8.f;
-constexpr int kOver = 5;                 // a group's fixed cost in tiles
+constexpr int kOver = 3;                 // a group's fixed cost in tiles
 constexpr int kMinUnits = 2;             // least units per cluster
 constexpr int kMaxClusters = 96;         // bounds the workspace (the device has 76 pairs of SMs)
 constexpr uint32_t kIdescS = idesc_bf16_f32(kM, kTok);

@@ -12,12 +12,14 @@
 // epilogue owns a token and adds its weights over the columns in a fixed
 // order, so no sum crosses threads; which pairs see a token is one range of
 // columns (rows from the token's own position on, up to the window's end).
-// K lives in ten 16 KB slots of 64 dims each: it stays while an item walks its
+// K lives in nine 16 KB slots of 64 dims each: it stays while an item walks its
 // blocks, and in the item's last block every slot takes the next item's dims as
 // soon as its MMAs are done, so that single-block items (decode) stream too.  Q
-// comes by TMA through three slots.  Warps: 0-3 epilogue, 4-7 gather K (16-byte
-// cp.async), 8 issues the MMAs (CTA 0) or reports CTA 1's K, 9 loads Q, 10 reports
-// CTA 1's Q.
+// comes by TMA through five slots (three did not cover the way to L2: 1024 rows over
+// 8192 tokens 777 us, with four 671).  Warps: 0-3 epilogue, 4-7 gather K (16-byte
+// cp.async), 8 of CTA 0 issues the MMAs, 9 loads Q, 10 and 11 report what K and Q
+// have landed in their CTA to CTA 0 (one barrier for both CTAs: a look at a barrier
+// costs the issuing thread over a hundred cycles of the 512 that an atom's MMAs run).
 //
 // Shares of the work are cut as in echo_chunk.cu, by blocks; the parts of a cut item are
 // 256 sums in the workspace, joined in order.
@@ -29,11 +31,11 @@ namespace {
 
 constexpr int kTok = 256;               // tokens per item, 128 per CTA
 constexpr int kCols = 256;              // (row, head) pairs per block
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kLoad = 128;
 constexpr int kAtoms = kLatDqk / 64;    // 9
 constexpr uint32_t kSlot = 128 * 128;   // 128 rows of 64 dims
-constexpr int kKSlots = 10, kQSlots = 3;
+constexpr int kKSlots = 9, kQSlots = 5;
 constexpr uint32_t kTmemCols = 512;     // two D buffers of 256 columns
 constexpr int kMaxClusters = 96;
 // units of an item: its K, each block; only to decay
@@ -192,20 +194,19 @@ struct Walk {
 };
 
 struct Ctl {
-    uint64_t k_full[kKSlots], pk_full[kKSlots], k_free[kKSlots];
-    uint64_t q_full[kQSlots], pq_full[kQSlots], q_free[kQSlots];
+    // *_full: landed here; *_ready of CTA 0: landed in both CTAs
+    uint64_t k_full[kKSlots], k_ready[kKSlots], k_free[kKSlots];
+    uint64_t q_full[kQSlots], q_ready[kQSlots], q_free[kQSlots];
     uint64_t d_full[2], d_free[2];
     uint64_t drain;
     uint32_t tmem;
     int abort;
     int first;
     alignas(16) float nl[2][kCols];       // -lse * log2(e) of a block's pairs
-    int64_t row[2][128];                  // cache rows of an item's tokens (by item parity)
 };
-constexpr uint32_t kSmem = (kKSlots + kQSlots) * kSlot + ((sizeof(Ctl) + 15u) & ~15u) + 1024;
+constexpr uint32_t kSmem = (kKSlots + kQSlots) * kSlot + ((sizeof(Ctl) + 15u) & ~15u);
 static_assert(kSmem <= 227u * 1024u, "mass shared memory");
 
-__device__ __forceinline__ void bar_sync128(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool bar_or128(int id, bool v) {
     uint32_t r;
     asm volatile(
@@ -238,11 +239,14 @@ __device__ __forceinline__ int block_cols(const Item& g, int heads, int cb) {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mass_kernel(ChunkArgs a, Plan plan, const __grid_constant__ CUtensorMap qmap, float scale_log2,
                 const float* __restrict__ lse, const float* mass, float* mass_out, float decay) {
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
+    extern __shared__ __align__(1024) uint8_t mass_smem[];  // the swizzled tiles need 1024 bytes
+    const uint32_t base = smem_addr(mass_smem);
+    if (base & 1023u) {  // the same in every CTA
+        set_status(a.status, ECHO_ST_TIMEOUT);
+        return;
+    }
     const uint32_t sK = base, sQ = sK + kKSlots * kSlot;
-    Ctl* const ctl = reinterpret_cast<Ctl*>(smem_raw + (base - raw) + (kKSlots + kQSlots) * kSlot);
+    Ctl* const ctl = reinterpret_cast<Ctl*>(mass_smem + (kKSlots + kQSlots) * kSlot);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t c = cluster_rank();
     const int ci = blockIdx.x >> 1;
@@ -250,12 +254,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kKSlots; ++i) {
             mbar_init(smem_addr(&ctl->k_full[i]), kLoad);
-            mbar_init(smem_addr(&ctl->pk_full[i]), 1);
+            mbar_init(smem_addr(&ctl->k_ready[i]), 2);
             mbar_init(smem_addr(&ctl->k_free[i]), 1);
         }
         for (int i = 0; i < kQSlots; ++i) {
             mbar_init(smem_addr(&ctl->q_full[i]), 1);
-            mbar_init(smem_addr(&ctl->pq_full[i]), 1);
+            mbar_init(smem_addr(&ctl->q_ready[i]), 2);
             mbar_init(smem_addr(&ctl->q_free[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -371,41 +375,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!ok) *abort = 1;
     } else if (warp < 8) {
-        // ---- K: 8 threads per token row, 16 bytes each, 128 rows in 8 passes
-        const int lt = tid - 128, x = lt & 7, r0 = lt >> 3;
+        // ---- K: 8 lanes per token row, 16 bytes each: a warp copies rows 4w + i + 16j, i < 4 at a time, having
+        // looked up the 32 of them (lane i + 4j)
+        const int w = warp - 4, x = lane & 7, i4 = lane >> 3;
         Ring k;
-        uint32_t filled = 0, items = 0;
+        uint32_t filled = 0;
         bool ok = true;
         while (ok && walk.next(&p)) {
             if (p.hi == p.lo) continue;
-            int64_t* const row = ctl->row[items++ & 1u];
+            int64_t mine = -1;
             {
-                const int64_t tok = p.g.tok0 + c * 128 + lt;
+                const int64_t tok = p.g.tok0 + c * 128 + 4 * w + (lane & 3) + 16 * (lane >> 2);
                 bool bad = false;
-                row[lt] = tok < p.g.len ? token_row(a, page_view(a, p.g.req, p.g.off), static_cast<uint32_t>(tok), &bad) : -1;
+                if (tok < p.g.len) mine = token_row(a, page_view(a, p.g.req, p.g.off), static_cast<uint32_t>(tok), &bad);
+                if (bad) set_status(a.status, ECHO_ST_BADDATA);
             }
-            bar_sync128(2);
             const uint8_t* src[8];
             uint32_t live = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int64_t r = row[r0 + 16 * j];
+                const int64_t r = __shfl_sync(0xffffffffu, mine, i4 + 4 * j);
                 live |= (r >= 0 ? 1u : 0u) << j;
                 src[j] = a.kv + (r < 0 ? 0 : r * kLatRowBytes) + 16 * x;
             }
             for (int at = 0; at < kAtoms; ++at, k.step(kKSlots), ++filled) {
-                if (ok && filled >= kKSlots) ok = mbar_wait(smem_addr(&ctl->k_free[k.slot]), k.phase ^ 1u, abort);
-                if (!ok) continue;  // every thread passes the items' barriers together
+                if (filled >= kKSlots) ok = mbar_wait(smem_addr(&ctl->k_free[k.slot]), k.phase ^ 1u, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 const uint32_t dst = sK + static_cast<uint32_t>(k.slot) * kSlot;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int r = r0 + 16 * j;
+                    const int r = 4 * w + i4 + 16 * j;
                     cp_async_16(dst + static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>((x ^ r) & 7) << 4), src[j] + at * 128,
                                 (live >> j) & 1u ? 16u : 0u);
                 }
                 cp_async_arrive_noinc(smem_addr(&ctl->k_full[k.slot]));
             }
-            ok = !bar_or128(2, !ok);
         }
         if (!ok) *abort = 1;
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -441,31 +446,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 (void)mbar_wait(smem_addr(&ctl->q_full[f % kQSlots]), (f / kQSlots) & 1u, nullptr);
             }
         }
-    } else if (warp == 8 && c == 0) {
-        // ---- the MMAs of both CTAs
-        Ring k, q;
-        uint32_t d = 0;
-        bool ok = true;
-        while (ok && walk.next(&p)) {
-            const Ring k0 = k;
-            for (int b = p.lo; ok && b < p.hi; ++b, ++d) {
-                const int n = (block_cols(p.g, a.heads, p.g.cb0 + b) + 31) & ~31;
-                const uint32_t db = d & 1u, idesc = idesc_bf16_f32(256, static_cast<uint32_t>(n));
-                if (d >= 2 && !mbar_wait_cluster(smem_addr(&ctl->d_free[db]), ((d >> 1) & 1u) ^ 1u, abort)) {
-                    ok = false;
-                    break;
-                }
-                k = k0;
-                for (int at = 0; at < kAtoms; ++at, k.step(kKSlots), q.step(kQSlots)) {
-                    if (b == p.lo)
-                        ok = mbar_wait(smem_addr(&ctl->k_full[k.slot]), k.phase, abort) &&
-                             mbar_wait_cluster(smem_addr(&ctl->pk_full[k.slot]), k.phase, abort);
-                    ok = ok && mbar_wait(smem_addr(&ctl->q_full[q.slot]), q.phase, abort) &&
-                         mbar_wait_cluster(smem_addr(&ctl->pq_full[q.slot]), q.phase, abort);
-                    if (!ok) break;
-                    fence_proxy_async_smem();
-                    tc_fence_after();
-                    if (elect_one()) {
+    } else if (warp == 8) {
+        // ---- the MMAs of both CTAs, by one thread of CTA 0
+        if (c == 0 && elect_one()) {
+            Ring k, q;
+            uint32_t d = 0;
+            bool ok = true;
+            while (ok && walk.next(&p)) {
+                const Ring k0 = k;
+                for (int b = p.lo; ok && b < p.hi; ++b, ++d) {
+                    const int n = (block_cols(p.g, a.heads, p.g.cb0 + b) + 31) & ~31;
+                    const uint32_t db = d & 1u, idesc = idesc_bf16_f32(256, static_cast<uint32_t>(n));
+                    if (d >= 2 && !mbar_wait_cluster(smem_addr(&ctl->d_free[db]), ((d >> 1) & 1u) ^ 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    k = k0;
+                    for (int at = 0; at < kAtoms; ++at, k.step(kKSlots), q.step(kQSlots)) {
+                        if (b == p.lo) ok = mbar_wait_cluster(smem_addr(&ctl->k_ready[k.slot]), k.phase, abort);
+                        ok = ok && mbar_wait_cluster(smem_addr(&ctl->q_ready[q.slot]), q.phase, abort);
+                        if (!ok) break;
+                        tc_fence_after();
                         const uint64_t ad = sw128_kmajor_desc(sK + static_cast<uint32_t>(k.slot) * kSlot);
                         const uint64_t bd = sw128_kmajor_desc(sQ + static_cast<uint32_t>(q.slot) * kSlot);
 #pragma unroll
@@ -476,18 +477,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (b + 1 == p.hi) mma2_commit_both(smem_addr(&ctl->k_free[k.slot]));
                         if (at + 1 == kAtoms) mma2_commit_both(smem_addr(&ctl->d_full[db]));
                     }
-                    __syncwarp();
                 }
             }
+            if (!ok) {
+                *abort = 1;
+                mma2_commit_both(smem_addr(&ctl->drain));
+                (void)mbar_wait(smem_addr(&ctl->drain), 0, nullptr);
+            }
         }
-        if (!ok) {
-            if (lane == 0) *abort = 1;
-            if (elect_one()) mma2_commit_both(smem_addr(&ctl->drain));
-            __syncwarp();
-            (void)mbar_wait(smem_addr(&ctl->drain), 0, nullptr);
-        }
-    } else if (warp == 8) {
-        // ---- CTA 1: K has landed here
+        __syncwarp();
+    } else if (warp == 10) {
+        // ---- K has landed here
         Ring k;
         bool ok = true;
         while (ok && walk.next(&p)) {
@@ -495,18 +495,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int at = 0; ok && at < kAtoms; ++at, k.step(kKSlots)) {
                 ok = mbar_wait(smem_addr(&ctl->k_full[k.slot]), k.phase, abort);
                 fence_proxy_async_smem();
-                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->pk_full[k.slot]), 0);
+                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->k_ready[k.slot]), 0);
             }
         }
         if (!ok && lane == 0) *abort = 1;
-    } else if (c == 1) {
-        // ---- CTA 1, warp 10: Q has landed here
+    } else {
+        // ---- Q has landed here
         Ring q;
         bool ok = true;
         while (ok && walk.next(&p)) {
             for (int i = 0; ok && i < (p.hi - p.lo) * kAtoms; ++i, q.step(kQSlots)) {
                 ok = mbar_wait(smem_addr(&ctl->q_full[q.slot]), q.phase, abort);
-                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->pq_full[q.slot]), 0);
+                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->q_ready[q.slot]), 0);
             }
         }
         if (!ok && lane == 0) *abort = 1;
