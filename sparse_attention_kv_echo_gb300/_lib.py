@@ -430,17 +430,16 @@ def mla_chunk(row_off, q, tok_off, n_tokens, pages, scale, out, lse, ws, status,
     the end of its context) over the cache `pages` (a KVPages): causal; window > 0: the last
     `window` tokens and the first `sinks`; sel [n,k] int32: the tokens listed for each row -> out
     [n,heads,512] bf16, lse [n,heads] f32.  ws: uint8, mla_chunk_workspace_size(n, heads, B)."""
-    k, more = 0, ("out", out, torch.bfloat16, (q.shape[0], q.shape[1], MLA_DV))
-    if sel is None:
-        B, n, heads = _check_chunk("mla_chunk", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end, more)
-    else:
+    k, more = 0, [("out", out, torch.bfloat16, (q.shape[0], q.shape[1], MLA_DV)),
+                  ("ws", ws, torch.uint8, (ws.numel(),))]
+    if sel is not None:
         k = sel.shape[-1]
-        B, n, heads = _check_chunk("mla_chunk", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end, more,
-                                   ("sel", sel, torch.int32, (q.shape[0], k)))
+        more.append(("sel", sel, torch.int32, (q.shape[0], k)))
+    B, n, heads = _check_chunk("mla_chunk", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end, *more)
     _check("echo_mla_chunk", load().echo_mla_chunk(
         B, _ptr(row_off), n, heads, _ptr(q), _ptr(tok_off), _ptr(tok_end), int(n_tokens),
         ctypes.byref(pages.struct), _ptr(sel), k, int(window), int(sinks), float(scale), _ptr(out), _ptr(lse),
-        _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+        _ptr(ws), ws.numel(), _ptr(status), _stream(stream)))
 
 
 def mla_mass_workspace_size(n_tokens: int, B: int) -> int:
@@ -462,10 +461,12 @@ def mla_mass(row_off, q, lse, tok_off, n_tokens, pages, scale, mass, mass_out, s
             ws.record_stream(stream)
         elif stream is not None:
             raise ValueError("mla_mass: a stream given by its handle needs ws")
+    else:
+        _expect("mla_mass", torch.cuda.current_device(), ("ws", ws, torch.uint8, (ws.numel(),)))
     _check("echo_mla_mass", load().echo_mla_mass(
         B, _ptr(row_off), n, heads, _ptr(q), _ptr(lse), _ptr(tok_off), _ptr(tok_end), int(n_tokens),
         ctypes.byref(pages.struct), int(window), int(sinks), float(scale), _ptr(mass), _ptr(mass_out), float(decay),
-        _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+        _ptr(ws), ws.numel(), _ptr(status), _stream(stream)))
 
 
 def evict_select(tok_off, n_tokens, slot2tok, mass, keep, evict_tok, evict_slot, evict_cnt, status, sinks=0, recent=0,
@@ -502,9 +503,9 @@ def cache_release(tok_off, n_tokens, tok, cache, status, mass=None, tok_end=None
         _expect("cache_release", dev, ("mass", mass, torch.float32, (n_tokens,)))
     whole = getattr(cache, "parent", cache)             # of a CacheView
     requests = cache.B if whole is cache else cache.b1 - cache.b0
-    if whole.n_tokens < n_tokens or requests != B:
+    if whole.n_tokens < n_tokens or requests != B or whole.tok2slot.get_device() != dev:
         raise ValueError(f"cache_release: a cache of {requests} requests and {whole.n_tokens} token rows, not {B} and "
-                         f"{n_tokens}")
+                         f"{n_tokens}, or on another device")
     _check("echo_cache_release", load().echo_cache_release(
         B, _ptr(tok_off), _ptr(tok_end), int(n_tokens), _ptr(tok), m, ctypes.byref(cache.struct), _ptr(mass),
         _ptr(status), _stream(stream)))

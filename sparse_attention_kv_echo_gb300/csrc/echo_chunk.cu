@@ -625,7 +625,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // store wants whole lines of few rows.  Straight from the registers the result took 5 us a group.
             const int live = p.g.rows * a.heads, m0 = static_cast<int>(c) * 64 + (warp & 1) * 32;  // the warp's first pair
             if (whole) {
-                const float f = L > 0.f ? 1.f / L : 0.f;
+                const bool any = L != 0.f;  // a NaN among the scores stays one
+                const float f = any ? 1.f / L : 0.f;
                 uint8_t* const dst = reinterpret_cast<uint8_t*>(out + (static_cast<int64_t>(p.g.row0) * a.heads + m0) * kLatDv + half * 256);
 #pragma unroll 1
                 for (uint32_t x = 0; x < 256u; x += 64u) {
@@ -644,8 +645,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             uint32_t w[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(L > 0.f ? o[8 * j + 2 * i] * f : 0.f,
-                                                                                L > 0.f ? o[8 * j + 2 * i + 1] * f : 0.f);
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(any ? o[8 * j + 2 * i] * f : 0.f,
+                                                                                any ? o[8 * j + 2 * i + 1] * f : 0.f);
                                 w[i] = *reinterpret_cast<const uint32_t*>(&b2);
                             }
                             u[4 * h + j] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -653,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     store_rows(gP + warp * 4096, u, dst + 2 * x, kLatDv * 2, live - m0);
                 }
-                if (lives && half == 0) lse[at] = L > 0.f ? (m + log2f(L)) * 0.69314718055994531f : -INFINITY;
+                if (lives && half == 0) lse[at] = any ? (m + log2f(L)) * 0.69314718055994531f : -INFINITY;
             } else {
                 uint8_t* const part = plan.part + static_cast<size_t>(2 * ci + (p.lo > 0 ? 0 : 1)) * kPartBytes;
                 uint8_t* const dst = part + (static_cast<size_t>(m0) * kLatDv + half * 256) * 4;
@@ -935,7 +936,7 @@ __device__ __forceinline__ void join_pair(const Plan& plan, const Cut& x, int mi
             }
         }
     }
-    const bool any = L > 0.f;
+    const bool any = L != 0.f;
     const float f = any ? 1.f / L : 0.f;
     const int64_t at = static_cast<int64_t>(x.row0) * heads + mi;
 #pragma unroll

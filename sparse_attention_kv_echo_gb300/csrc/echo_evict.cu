@@ -274,6 +274,33 @@ __global__ void __launch_bounds__(kET)
     cluster.sync();  // no CTA leaves while another reads its counts
 }
 
+// Whether the device holds a cluster of kEMaxCtas (more than the portable 8) at once, with the most
+// shared memory (queried once per device).
+bool wide_clusters_fit() {
+    static int cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (cached[dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kEMaxCtas);
+        cfg.blockDim = dim3(kET);
+        cfg.dynamicSmemBytes = kECap * 4;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kEMaxCtas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, evict_kernel, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        cached[dev] = n > 0 ? 1 : 2;
+    }
+    return cached[dev] == 1;
+}
+
 constexpr int kRT = 256;
 
 __global__ void __launch_bounds__(kRT)
@@ -316,10 +343,11 @@ extern "C" int echo_evict_select(int B, const int64_t* tok_off, const int64_t* t
     // CTAs of a request: while each has kESlots slots and the batch leaves SMs free
     int n = 1;
     while (n < kEMaxCtas && C >= 2 * n * kESlots && 2 * n * B <= sm_count()) n *= 2;
-    const int per = ((C + 31) / 32 + n - 1) / n * 32;
-    const size_t smem = static_cast<size_t>(per < kECap ? per : kECap) * 4;
     ECHO_CUDA_OK(cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kECap * 4));
     ECHO_CUDA_OK(cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    if (n > 8 && !wide_clusters_fit()) n = 8;
+    const int per = ((C + 31) / 32 + n - 1) / n * 32;
+    const size_t smem = static_cast<size_t>(per < kECap ? per : kECap) * 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(B * n));
     cfg.blockDim = dim3(kET);

@@ -51,7 +51,7 @@ class PrefillRunner:
             if self.cache.row_bytes != 2 * L.MLA_DQK:
                 raise ValueError("attention needs 576-dim bf16 cache rows")
             self.pages = L.KVPages.of_cache(self.cache)
-            self._sel = [self.sel_idx, torch.full_like(self.sel_idx, -1)]
+            self._sel = [self.sel_idx, torch.full_like(self.sel_idx, -1)]   # taken in turn
             self.tok_off = torch.tensor([0, self.n_keys], dtype=torch.int64, device=device)
             last = self.n_keys - (self.blocks() - 1) * self.R
             self._row_off = {r: torch.tensor([0, r], dtype=torch.int64, device=device) for r in (self.R, last)}
@@ -67,15 +67,17 @@ class PrefillRunner:
         """Enqueue block i (q [R_i,64,128], w [R_i,64] on the device).
 
         mla_q: with attention=True, the block's MLA queries [R_i,heads,576] bf16; attn_out and attn_lse
-        (first R_i rows) receive the attention of its rows.  It runs on the copy stream: mla_q has to stay as
-        it is, and the results are there, until / from wait_recall on."""
+        (first R_i rows) receive the attention of its rows over sel_idx.  It runs on the copy stream,
+        after the block's recall: mla_q has to stay as it is until wait_recall, and the results, there
+        from then on, are the next call's to overwrite."""
         if self.attention != (mla_q is not None):
             raise ValueError("mla_q goes with attention=True, and only with it")
         row0 = i * self.R
         R = min(self.R, self.n_keys - row0)
         assert q.shape[0] == R and w.shape[0] == R
         if self.attention:
-            self.sel_idx = self._sel[i % 2]
+            self._sel.reverse()
+            self.sel_idx = self._sel[0]
         L.prefill_block(R, row0, self.n_keys, q, w, self.k8, self.ks, self.k, self.theta, self.alpha,
                         self.scores, self.W, self.hist, self.sel_idx, self.kth, self.union_list,
                         self.union_count, self.union_bits, self.cache, self.sel_slot, self.ws, self.status,

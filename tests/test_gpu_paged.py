@@ -63,6 +63,8 @@ CASES = [
     ([90, 40], [2, 9], 127, 256),
     ([4500], [1], 128, 64),                    # one request over many splits
     ([2100, 1, 0, 900], [1, 1, 0, 1], 128, 64),
+    ([1 + 7 * i % 90 for i in range(40)], [i % 2 for i in range(40)], 128, 16),          # more requests than a warp has lanes
+    ([3 + i % 5 for i in range(1100)], [(0, 1, 3)[i % 3] for i in range(1100)], 16, 4),  # more than a block has threads
 ]
 
 
@@ -149,6 +151,74 @@ def test_unseen_rows_may_hold_anything():
     bt.kv[torch.nonzero(~seen)[::2, 0]] = math.inf
     dirty = _attend(bt, 60, 3)
     assert torch.equal(clean[0], dirty[0]) and torch.equal(clean[1], dirty[1])
+
+
+def test_a_nan_query_stays_in_its_row():
+    # the rows packed with it, and the pieces of its own context that are joined, keep to theirs
+    for lens, heads in ([300], 16), ([3000], 128):
+        bt = P.Batch(lens, [6], heads, 16, seed=3)
+        clean = _attend(bt)
+        bt.q[2, 5, 7] = math.nan
+        bt.q[4, 1, 100] = math.inf
+        out, lse = _attend(bt)
+        hurt = torch.zeros((6, heads), dtype=torch.bool)
+        hurt[2, 5] = hurt[4, 1] = True
+        assert torch.all(torch.isnan(out[hurt])) and torch.all(torch.isnan(lse[hurt]))
+        assert torch.equal(out[~hurt], clean[0][~hurt]) and torch.equal(lse[~hurt], clean[1][~hurt])
+
+
+def test_rows_past_4_gib():
+    bt = P.Batch([150, 70], [1, 30], 128, 16, seed=13)
+    want = _attend(bt)
+    row_off, q, tok_off, tok_end, _ = bt.on(dev, L)
+    far = 4_000_000 // 16                        # the pages lie from 4.6 GB on
+    kv = torch.zeros((far * 16 + bt.kv.shape[0], 576), dtype=torch.bfloat16, device=dev)
+    kv[far * 16:] = bt.kv.to(dev)
+    pages = L.KVPages((bt.tab + far).to(dev), kv, 16)
+    out, lse, ws, st = _buffers(bt.n, 128, 2)
+    L.mla_chunk(row_off, q, tok_off, bt.n_tokens, pages, bt.scale, out, lse, ws, st, tok_end=tok_end)
+    assert int(st.item()) == 0 and torch.equal(out.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+
+
+def test_token_rows_past_2_to_the_31():
+    # the second request's region starts behind 2^31 token rows; pages of 1024
+    gap, page = 2 ** 31 + 5, 1024
+    bt = P.Batch([90, 200], [1, 3], 128, 64, seed=14)
+    n = gap + 300
+    tab = torch.full((n // page + 1,), -1, dtype=torch.int32)
+    tab[0], tab[gap // page] = 1, 0
+    kv = torch.randn((2 * page, 576), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    bt.tok_off = torch.tensor([0, gap, n])
+    bt.tok_end, bt.n_tokens, bt.tab, bt.kv, bt.page = torch.tensor([90, gap + 200]), n, tab, kv, page
+    _compare(bt, _attend(bt))
+    row_off, q, tok_off, tok_end, pages = bt.on(dev, L)
+    lse = bt.attend()[1].float().to(dev)
+    mass = torch.zeros(n, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    L.mla_mass(row_off, q, lse, tok_off, n, pages, bt.scale, mass, mass, st, tok_end=tok_end)
+    assert int(st.item()) == 0
+    assert abs(float(mass[:90].sum()) - 128) < 128 * 1e-4 and abs(float(mass[gap:gap + 200].sum()) - 3 * 128) < 384 * 1e-4
+    assert float(mass[90:gap].abs().max()) == 0.0
+
+
+def test_two_calls_at_once():
+    a, b = P.Batch([2000, 300], [1, 100], 128, 64, seed=15), P.Batch([900], [200], 32, 16, seed=16)
+    want = [_attend(x) for x in (a, b)]
+    streams, held = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for x, s in zip((a, b), streams):
+            row_off, q, tok_off, tok_end, pages = x.on(dev, L)
+            bufs = _buffers(x.n, x.heads, len(x.lens))
+            torch.cuda.current_stream().synchronize()
+            held.append((bufs, row_off, q, tok_off, tok_end, pages))
+    for i, (bufs, row_off, q, tok_off, tok_end, pages) in enumerate(held):
+        x = (a, b)[i % 2]
+        L.mla_chunk(row_off, q, tok_off, x.n_tokens, pages, x.scale, *bufs, tok_end=tok_end, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for i, (bufs, *_) in enumerate(held):
+        assert int(bufs[3].item()) == 0
+        assert torch.equal(bufs[0].cpu(), want[i % 2][0]) and torch.equal(bufs[1].cpu(), want[i % 2][1])
 
 
 def test_growing_scores_move_the_maximum():
@@ -389,7 +459,7 @@ def test_release_of_repeated_and_absent_tokens():
     assert int(st.item()) == L.ST_BADDATA
 
 
-@pytest.mark.parametrize("what", ["dtype", "shape", "pages", "strides", "sel"])
+@pytest.mark.parametrize("what", ["dtype", "shape", "pages", "strides", "sel", "ws"])
 def test_wrapper_refuses(what):
     bt = P.Batch([40], [2], 16, 16, seed=1)
     row_off, q, tok_off, tok_end, pages = bt.on(dev, L)
@@ -403,6 +473,8 @@ def test_wrapper_refuses(what):
         n = bt.n_tokens + 1000
     if what == "strides":
         q = torch.cat([q, q], -1)[:, :, :576]
+    if what == "ws":
+        ws = ws.cpu()
     if what == "sel":
         sel = torch.zeros((1, 4), dtype=torch.int32, device=dev)
     with pytest.raises(ValueError):
