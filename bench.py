@@ -75,7 +75,8 @@ def parse_args(argv=None):
                    help="early-fetch cap per request and layer (-1: only the free slots cap it)")
     p.add_argument("--hold-early", action="store_true",
                    help="the held-slot variant of the cache step (the late recall need not wait for the early copy)")
-    p.add_argument("--part", choices=["step", "mla", "append", "layers", "pool", "prefill", "kernels"], default="step",
+    p.add_argument("--part", choices=["step", "mla", "append", "layers", "pool", "prefill", "kernels", "paged"],
+                   default="step",
                    help="step: the decode step (default); mla: the sparse MLA attention over the selected "
                         "slots alone, at the batch workload's batch, k and GPU slots; append: the append of one "
                         "new token per request (key, host-pool row, cache slot) at the batch workload; layers: "
@@ -83,7 +84,9 @@ def parse_args(argv=None):
                         "cross-layer early fetch; pool: the decode step with one cache pool shared by the "
                         "batch (B x C slots, and 260000) against per-request slot ranges; prefill: the "
                         "chunked prefill of a 102400-token prompt in 2048-row blocks; kernels: the score and "
-                        "top-k kernels alone on one layer of 32 requests x 131072 tokens")
+                        "top-k kernels alone on one layer of 32 requests x 131072 tokens; paged: the calls over a "
+                        "paged latent cache (chunk attention, attention weights, victims) at the batch workload's "
+                        "contexts and one 2048-row block of the prompt")
     p.add_argument("--first-share", type=float, default=None,
                    help="share of the requests in the first of two groups (default: the layer's choice)")
     return p.parse_args(argv)
@@ -728,6 +731,93 @@ def run_mla(args):
     }), flush=True)
 
 
+PAGED_METRIC = "attention of a 2048-row prompt block over a paged latent cache: rows/s"
+
+
+def run_paged(args):
+    """The calls over a paged latent cache, alone: the fourth 2048-row block of the prompt over its 8192
+    tokens (causal, through a 1024-token window, and over 2048 selected tokens a row), one row of each of 8
+    requests over 32768 tokens, the attention weights of both, and the victims of 8 x 4096 slots."""
+    import torch
+    from sparse_attention_kv_echo_gb300 import _lib as L
+    from sparse_attention_kv_echo_gb300 import workloads as wl
+
+    rank, world, local = dist_env()
+    torch.cuda.set_device(local)
+    dev = f"cuda:{local}"
+    L.load(build_if_missing=True)
+    batch, R = wl.WORKLOADS["batch"], wl.WORKLOADS["prefill"].prefill_block
+    H, page, scale = L.MLA_HEADS, 64, 1.0 / math.sqrt(192.0)
+    g = torch.Generator(device=dev).manual_seed(13 + rank)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    main = torch.cuda.Stream()
+
+    def cache(lens, rows):
+        off = torch.tensor([0] + list(lens), dtype=torch.int64).cumsum(0)
+        n = int(off[-1])
+        c = dict(n=n, off=off.to(dev), row_off=torch.tensor([0] + list(rows), dtype=torch.int64).cumsum(0).to(dev),
+                 tab=torch.randperm(-(-n // page), generator=g, device=dev).to(torch.int32),
+                 kv=torch.randn((-(-n // page) * page, L.MLA_DQK), generator=g, device=dev).to(torch.bfloat16),
+                 q=torch.randn((sum(rows), H, L.MLA_DQK), generator=g, device=dev).to(torch.bfloat16))
+        c["pages"] = L.KVPages(c["tab"], c["kv"], page)
+        c["out"] = torch.empty((sum(rows), H, L.MLA_DV), dtype=torch.bfloat16, device=dev)
+        c["lse"] = torch.empty((sum(rows), H), dtype=torch.float32, device=dev)
+        c["mass"] = torch.zeros(n, dtype=torch.float32, device=dev)
+        c["ws"] = torch.empty(max(L.mla_chunk_workspace_size(sum(rows), H, len(rows)),
+                                  L.mla_mass_workspace_size(n, len(rows))), dtype=torch.uint8, device=dev)
+        return c
+
+    blk, dec = cache([4 * R], [R]), cache(batch.lengths, [1] * batch.B)
+    sel = torch.rand((R, 3 * R), generator=g, device=dev).argsort(1)[:, :batch.k].to(torch.int32)  # before every row
+
+    def attend(c, **kw):
+        L.mla_chunk(c["row_off"], c["q"], c["off"], c["n"], c["pages"], scale, c["out"], c["lse"], c["ws"], st,
+                    stream=main, **kw)
+
+    def weigh(c):
+        L.mla_mass(c["row_off"], c["q"], c["lse"], c["off"], c["n"], c["pages"], scale, c["mass"], c["mass"], st,
+                   decay=0.9375, ws=c["ws"], stream=main)
+
+    B, C = batch.B, batch.C
+    s2t = torch.rand((B, batch.lengths[0]), generator=g, device=dev).argsort(1)[:, :C].to(torch.int32).contiguous()
+    et, es = torch.empty_like(s2t), torch.empty_like(s2t)
+    ec = torch.empty(B, dtype=torch.int32, device=dev)
+    parts = {
+        "block_causal": lambda: attend(blk), "block_window_1024": lambda: attend(blk, window=1024, sinks=16),
+        "block_selected_2048": lambda: attend(blk, sel=sel), "decode_8x32768": lambda: attend(dec),
+        "weights_block": lambda: weigh(blk), "weights_decode_8x32768": lambda: weigh(dec),
+        "victims_8x4096": lambda: L.evict_select(dec["off"], dec["n"], s2t, dec["mass"], C // 2, et, es, ec, st, sinks=4,
+                                                 recent=256, stream=main)}
+    flush = torch.empty(FLUSH_BYTES // 4, dtype=torch.float32, device=dev)
+    torch.cuda.synchronize()
+    us = {}
+    for name, call in parts.items():
+        ev = []
+        for i in range(args.warmup + args.steps):
+            if i == args.warmup:
+                torch.cuda.synchronize()
+                park(main)
+            with torch.cuda.stream(main):
+                flush.zero_()
+                a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                a.record(main)
+                call()
+                b.record(main)
+            ev.append((a, b))
+        torch.cuda.synchronize()
+        us[name] = round(1e3 * statistics.median(a.elapsed_time(b) for a, b in ev[args.warmup:]), 2)
+    pairs = sum(range(3 * R + 1, 4 * R + 1))
+    t = us["block_causal"] * 1e-6
+    print(json.dumps({
+        "metric": PAGED_METRIC, "value": round(R / t, 1), "unit": "rows/s", "n_gpus": world, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": round(1e3 * t, 5), "higher_is_better": True,
+        "dtype": "bf16 MMA, fp32 accumulate/softmax", "data": "synthetic (seeded)",
+        "config": {"workload": f"{R} rows of {4 * R} tokens, 128 heads; {B} requests x {batch.lengths[0]} tokens; pages of "
+                               f"{page}", "l2": "flushed by a 256 MB write before every timed call"},
+        "us": us, "tflops": round(2.0 * pairs * H * (L.MLA_DQK + L.MLA_DV) / t / 1e12, 1), "status": int(st.item()),
+    }), flush=True)
+
+
 KERNELS_METRIC = "indexer score and exact top-k alone, one layer: GB/s of the score kernel against HBM"
 
 
@@ -1179,6 +1269,8 @@ def main(argv=None):
         run_append(args)
     elif args.part == "mla":
         run_mla(args)
+    elif args.part == "paged":
+        run_paged(args)
     else:
         run_ours(args)
 

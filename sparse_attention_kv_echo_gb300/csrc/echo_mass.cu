@@ -16,7 +16,7 @@
 // blocks, and in the item's last block every slot takes the next item's dims as
 // soon as its MMAs are done, so that single-block items (decode) stream too.  Q
 // comes by TMA through five slots (three did not cover the way to L2: 1024 rows over
-// 8192 tokens 777 us, with four 671).  Warps: 0-3 epilogue, 4-7 gather K (16-byte
+// 8192 tokens 777 us, with four 671).  Warps: 0-3 epilogue, 4-7 and 12-15 gather K (16-byte
 // cp.async), 8 of CTA 0 issues the MMAs, 9 loads Q, 10 and 11 report what K and Q
 // have landed in their CTA to CTA 0 (one barrier for both CTAs: a look at a barrier
 // costs the issuing thread over a hundred cycles of the 512 that an atom's MMAs run).
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kTok = 256;               // tokens per item, 128 per CTA
 constexpr int kCols = 256;              // (row, head) pairs per block
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kLoad = 128;
 constexpr int kAtoms = kLatDqk / 64;    // 9
 constexpr uint32_t kSlot = 128 * 128;   // 128 rows of 64 dims
@@ -195,7 +195,8 @@ struct Walk {
 
 struct Ctl {
     // *_full: landed here; *_ready of CTA 0: landed in both CTAs
-    uint64_t k_full[kKSlots], k_ready[kKSlots], k_free[kKSlots];
+    uint64_t k_full[kKSlots], k_ready[kKSlots];
+    uint64_t k_free[2][kKSlots];          // by the parity of the item that leaves the slot
     uint64_t q_full[kQSlots], q_ready[kQSlots], q_free[kQSlots];
     uint64_t d_full[2], d_free[2];
     uint64_t drain;
@@ -255,7 +256,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kKSlots; ++i) {
             mbar_init(smem_addr(&ctl->k_full[i]), kLoad);
             mbar_init(smem_addr(&ctl->k_ready[i]), 2);
-            mbar_init(smem_addr(&ctl->k_free[i]), 1);
+            mbar_init(smem_addr(&ctl->k_free[0][i]), 1);
+            mbar_init(smem_addr(&ctl->k_free[1][i]), 1);
         }
         for (int i = 0; i < kQSlots; ++i) {
             mbar_init(smem_addr(&ctl->q_full[i]), 1);
@@ -302,17 +304,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && walk.next(&p)) {
             const int64_t tok = p.g.tok0 + c * 128 + tid;
-            // the columns that see the token
-            int64_t lo = 0, hi = 0;
-            if (p.hi > p.lo && tok < p.g.len) {
-                bool bad = false;
-                if (token_row(a, page_view(a, p.g.req, p.g.off), static_cast<uint32_t>(tok), &bad) >= 0) {
-                    lo = max(static_cast<int64_t>(0), tok - p.g.pos0) * a.heads;
-                    hi = (a.window && tok >= a.sinks ? min(static_cast<int64_t>(p.g.rows), tok - p.g.pos0 + a.window)
-                                                     : static_cast<int64_t>(p.g.rows)) * a.heads;
-                }
-                if (bad) set_status(a.status, ECHO_ST_BADDATA);
+            // The token's table entry and old mass are loaded here and looked at after the first block's MMAs: one
+            // after the other, the loads of an item took longer than its products
+            const bool in = tok < p.g.len, whole = p.lo == 0 && p.hi == p.g.nb;
+            PageView pv = {};
+            uint32_t in_page = 0;
+            int32_t entry = -1;
+            if (p.hi > p.lo && in) {
+                pv = page_view(a, p.g.req, p.g.off);
+                entry = pv.tab[page_of(a, pv, static_cast<uint32_t>(tok), &in_page)];
             }
+            const float old = in && whole && decay > 0.f ? mass[p.g.off + tok] : 0.f;
+            int64_t lo = 0, hi = 0;  // the columns that see the token
             float sum = 0.f, rest = 0.f;  // compensated over the blocks
             for (int b = p.lo; b < p.hi; ++b, ++d) {
                 const int cb = p.g.cb0 + b, n = block_cols(p.g, a.heads, cb);
@@ -329,6 +332,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = !bar_or128(1, !ok);
                 if (!ok) break;
                 tc_fence_after();
+                if (b == p.lo && entry >= 0) {
+                    bool bad = false;
+                    if (page_row(a, pv, entry, in_page, &bad) >= 0) {
+                        lo = max(static_cast<int64_t>(0), tok - p.g.pos0) * a.heads;
+                        hi = (a.window && tok >= a.sinks ? min(static_cast<int64_t>(p.g.rows), tok - p.g.pos0 + a.window)
+                                                         : static_cast<int64_t>(p.g.rows)) * a.heads;
+                    }
+                    if (bad) set_status(a.status, ECHO_ST_BADDATA);
+                }
                 const int64_t first = static_cast<int64_t>(cb) * kCols;
                 const int vlo = static_cast<int>(max(static_cast<int64_t>(0), min(lo - first, static_cast<int64_t>(kCols))));
                 const int vhi = static_cast<int>(max(static_cast<int64_t>(0), min(hi - first, static_cast<int64_t>(n))));
@@ -364,25 +376,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 sum = z;
             }
             if (!ok) break;
-            if (p.lo == 0 && p.hi == p.g.nb) {
-                if (tok < p.g.len) {
-                    const int64_t g = p.g.off + tok;
-                    mass_out[g] = (decay > 0.f ? decay * mass[g] : 0.f) + sum;
-                }
+            if (whole) {
+                if (in) mass_out[p.g.off + tok] = decay * old + sum;
             } else {
                 plan.part[static_cast<size_t>(2 * ci + (p.lo > 0 ? 0 : 1)) * kTok + c * 128 + tid] = sum;
             }
         }
         if (!ok) *abort = 1;
-    } else if (warp < 8) {
+    } else if (warp < 8 || warp >= 12) {
         // ---- K: 8 lanes per token row, 16 bytes each: a warp copies rows 4w + i + 16j, i < 4 at a time, having
-        // looked up the 32 of them (lane i + 4j)
-        const int w = warp - 4, x = lane & 7, i4 = lane >> 3;
-        Ring k;
-        uint32_t filled = 0;
+        // looked up the 32 of them (lane i + 4j).  Two sets of four warps take the items in turn, so that one looks
+        // its rows up while the other copies (32 decode rows 49.5 -> 43.5 us)
+        const int w = warp & 3, set = warp < 8 ? 0 : 1, x = lane & 7, i4 = lane >> 3;
+        static_assert(kKSlots == kAtoms, "an item takes every slot once");
         bool ok = true;
-        while (ok && walk.next(&p)) {
+        for (int item = 0; ok && walk.next(&p);) {
             if (p.hi == p.lo) continue;
+            if ((item & 1) != set) {
+                ++item;
+                continue;
+            }
             int64_t mine = -1;
             {
                 const int64_t tok = p.g.tok0 + c * 128 + 4 * w + (lane & 3) + 16 * (lane >> 2);
@@ -398,19 +411,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 live |= (r >= 0 ? 1u : 0u) << j;
                 src[j] = a.kv + (r < 0 ? 0 : r * kLatRowBytes) + 16 * x;
             }
-            for (int at = 0; at < kAtoms; ++at, k.step(kKSlots), ++filled) {
-                if (filled >= kKSlots) ok = mbar_wait(smem_addr(&ctl->k_free[k.slot]), k.phase ^ 1u, abort);
+            // a slot is free when the item before, the other set's, has left it: this set sees every phase of that
+            // parity's barriers, each before the next can end
+            for (int at = 0; at < kAtoms; ++at) {
+                if (item >= 1)
+                    ok = ok && mbar_wait(smem_addr(&ctl->k_free[(item - 1) & 1][at]), static_cast<uint32_t>((item - 1) >> 1) & 1u,
+                                         abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const uint32_t dst = sK + static_cast<uint32_t>(k.slot) * kSlot;
+                const uint32_t dst = sK + static_cast<uint32_t>(at) * kSlot;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int r = 4 * w + i4 + 16 * j;
                     cp_async_16(dst + static_cast<uint32_t>(r) * 128u + (static_cast<uint32_t>((x ^ r) & 7) << 4), src[j] + at * 128,
                                 (live >> j) & 1u ? 16u : 0u);
                 }
-                cp_async_arrive_noinc(smem_addr(&ctl->k_full[k.slot]));
+                cp_async_arrive_noinc(smem_addr(&ctl->k_full[at]));
             }
+            ++item;
         }
         if (!ok) *abort = 1;
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -450,10 +468,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- the MMAs of both CTAs, by one thread of CTA 0
         if (c == 0 && elect_one()) {
             Ring k, q;
-            uint32_t d = 0;
+            uint32_t d = 0, item = 0;
             bool ok = true;
             while (ok && walk.next(&p)) {
                 const Ring k0 = k;
+                const uint32_t parity = item & 1u;
+                if (p.hi > p.lo) ++item;
                 for (int b = p.lo; ok && b < p.hi; ++b, ++d) {
                     const int n = (block_cols(p.g, a.heads, p.g.cb0 + b) + 31) & ~31;
                     const uint32_t db = d & 1u, idesc = idesc_bf16_f32(256, static_cast<uint32_t>(n));
@@ -474,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             mma2_bf16(tmem + db * kCols, ad + ((kk * 32u) >> 4), bd + ((kk * 32u) >> 4), idesc,
                                       (at > 0 || kk > 0) ? 1u : 0u);
                         mma2_commit_both(smem_addr(&ctl->q_free[q.slot]));
-                        if (b + 1 == p.hi) mma2_commit_both(smem_addr(&ctl->k_free[k.slot]));
+                        if (b + 1 == p.hi) mma2_commit_both(smem_addr(&ctl->k_free[parity][k.slot]));
                         if (at + 1 == kAtoms) mma2_commit_both(smem_addr(&ctl->d_full[db]));
                     }
                 }
@@ -499,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
         if (!ok && lane == 0) *abort = 1;
-    } else {
+    } else {  // warp 11
         // ---- Q has landed here
         Ring q;
         bool ok = true;
