@@ -19,7 +19,7 @@
 //               MN-major operand.
 // Neither product is done twice, and the softmax needs nothing from the other
 // CTA.  Warps of a CTA: 0-3 softmax (thread = TMEM lane; the two threads of a
-// row exchange their tile maxima in shared memory), 4-7 gather K, 8-11 gather V
+// row exchange their tile maxima in shared memory), 16-19 store O, 4-7 gather K, 8-11 gather V
 // (16-byte cp.async: any row for any token; two stages of each, K in
 // thirds that are refilled as their MMAs end), 12 of CTA 0 issues the MMAs, 13
 // and 14 report what has landed in their CTA to it (one barrier for both CTAs: each
@@ -43,7 +43,7 @@ namespace {
 
 constexpr int kTok = 64;                 // tokens per tile
 constexpr int kM = 128;                  // (row, head) pairs per group
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kSoftmax = 128, kLoad = 128;
 constexpr int kAtoms = kLatDqk / 64;     // 9 swizzle atoms of 64 dims
 constexpr uint32_t kQAtom = 64 * 128;    // 64 rows x 128 B
@@ -379,27 +379,31 @@ struct Ctl {
     PlanHead head;
     Group group[kInline];
     int64_t cum[kInline + 1];
-    // tokens of a tile that have a row: written for tile t when QK of t - 2 is done, hence S of t - 6 read
-    // and tile t - 7 finished
-    alignas(16) uint8_t valid[kValid][kTok];
+    uint64_t fin_ready, fin_free;                        // a piece's factors are in fin / have been read
+    uint64_t o_free;                                     // O of a piece has been read in both CTAs
+    float fin[64];                                       // what O of a row is multiplied by
+    // tokens of a tile that have a row, a bit each: written for tile t when QK of t - 2 is done, hence S of t - 6
+    // read and tile t - 7 finished
+    uint32_t valid[kValid][2];
 };
 constexpr uint32_t kSmem = kQBytes + 2 * kKBytes + 2 * kVBytes + 2 * kPBytes + ((sizeof(Ctl) + 15u) & ~15u);
 static_assert(kSmem <= 227u * 1024u, "chunk shared memory");
 
-// 128 bytes of each lane's row (u) to 32 rows `stride` bytes apart, the first `rows` of them, as whole
-// lines: through 4 KB of shared memory of this warp (generic writes of it, by it, only).
-__device__ __forceinline__ void store_rows(uint8_t* stage, const uint4 (&u)[8], uint8_t* dst, int stride, int rows) {
-    const int lane = threadIdx.x & 31;
+// 4 x 4 transposition among the four lanes of a quad: lane q's w[j] becomes lane j's w[q].
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int q) {
+    const bool odd = q & 1, high = q & 2;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = u[j];
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int r = 4 * j + (lane >> 3), x = lane & 7;
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((x ^ (r & 7)) << 4));
-        if (r < rows) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(r) * stride + 16 * x) = v;
+    for (int i = 0; i < 4; i += 2) {
+        const uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? w[i] : w[i + 1], 1);
+        if (odd) w[i] = x;
+        else w[i + 1] = x;
     }
-    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = __shfl_xor_sync(0xffffffffu, high ? w[i] : w[i + 2], 2);
+        if (high) w[i] = x;
+        else w[i + 2] = x;
+    }
 }
 
 // Barrier over the softmax warps; true when any thread votes so.
@@ -472,6 +476,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&ctl->s_full[i]), 1);
             mbar_init(smem_addr(&ctl->s_free[i]), 2 * kSoftmax / 32);
         }
+        mbar_init(smem_addr(&ctl->fin_ready), kSoftmax / 32);
+        mbar_init(smem_addr(&ctl->fin_free), kSoftmax / 32);
+        mbar_init(smem_addr(&ctl->o_free), 2 * kSoftmax / 32);
         for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&ctl->drain[i]), 1);
         ctl->abort = 0;
         fence_barrier_init();
@@ -511,7 +518,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int half = tid >> 6, row = tid & 63, mi = static_cast<int>(c) * 64 + row;
         const int rig = mi / a.heads;  // row within the group
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-        bool ok = true;
+        bool ok = true, over = false;
+        uint32_t pieces = 0;  // with tiles
         while (ok && walk.next(&p)) {
             const bool lives = rig < p.g.rows;
             const int lo_tok = p.g.pos0 + p.g.rows + p.g.kept - p.g.nv;
@@ -541,16 +549,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->s_free[t & (kSBufs - 1)]), 0);
                 const int v0 = it * kTok + half * 32;
-                const uint4* vf = reinterpret_cast<const uint4*>(&ctl->valid[t & (kValid - 1)][half * 32]);
-                const uint4 f0 = vf[0], f1 = vf[1];
-                const bool all = ((f0.x & f0.y & f0.z & f0.w) & (f1.x & f1.y & f1.z & f1.w)) == 0x01010101u;
-                const bool clean = all && v0 + 32 <= vhi && (vb <= va || v0 >= vb || v0 + 32 <= va);
+                const uint32_t there = ctl->valid[t & (kValid - 1)][half];
+                const bool clean = there == 0xFFFFFFFFu && v0 + 32 <= vhi && (vb <= va || v0 >= vb || v0 + 32 <= va);
                 if (!__all_sync(0xffffffffu, clean)) {
-                    const uint32_t f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const int v = v0 + j;
-                        const bool see = ((f[j >> 2] >> (8 * (j & 3))) & 1u) && v < vhi && !(v >= va && v < vb);
+                        const bool see = ((there >> j) & 1u) && v < vhi && !(v >= va && v < vb);
                         s[j] = see ? s[j] : -INFINITY;
                     }
                 }
@@ -563,7 +568,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < w; ++j) mx[j] = fmaxf(mx[j], mx[j + w]);
                 ctl->mx[st][half][row] = mx[0];
                 ok = !softmax_sync_or(!ok);
-                if (!ok) break;  // all four warps together
+                over = !ok;
+                if (over) break;  // all four warps together
                 const float tmx = fmaxf(mx[0], ctl->mx[st][half ^ 1][row]) * scale_log2;
                 const bool need = tmx > m + kLazy;  // also m = -inf with a visible token
                 const bool moves = __any_sync(0xffffffffu, need);
@@ -609,72 +615,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->pv_ready[st]), 0);
             }
-            if (!ok) break;
-            // ---- the group's result, or this piece's part of it
-            if (p.hi > p.lo) ok = ok && mbar_wait(smem_addr(&ctl->pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, abort);
-            tc_fence_after();
-            __syncwarp();
-            ctl->mx[t & 1u][half][row] = l;
-            ok = !softmax_sync_or(!ok);
-            if (!ok) break;
-            const float L = l + ctl->mx[t & 1u][half ^ 1][row];
-            (void)softmax_sync_or(false);  // read before the next tile's maxima
+            if (over) break;
+            // ---- the piece's sums: its lse, or this part's, and the factors of O for the warps that store it
+            float L = 0.f;
+            if (p.hi > p.lo) {
+                ctl->mx[t & 1u][half][row] = l;
+                if (pieces >= 1) ok = ok && mbar_wait(smem_addr(&ctl->fin_free), (pieces - 1) & 1u, abort);
+                ++pieces;
+                ok = !softmax_sync_or(!ok);
+                if (!ok) break;
+                L = l + ctl->mx[t & 1u][half ^ 1][row];
+            }
             const bool whole = p.lo == 0 && p.hi == p.tiles;
-            const int64_t at = static_cast<int64_t>(p.g.row0) * a.heads + mi;
-            // Rows leave through this warp's 4 KB of the P buffers (free until the next P): a lane has a row, a
-            // store wants whole lines of few rows.  Straight from the registers the result took 5 us a group.
-            const int live = p.g.rows * a.heads, m0 = static_cast<int>(c) * 64 + (warp & 1) * 32;  // the warp's first pair
-            if (whole) {
+            if (half == 0) {
                 const bool any = L != 0.f;  // a NaN among the scores stays one
-                const float f = any ? 1.f / L : 0.f;
-                uint8_t* const dst = reinterpret_cast<uint8_t*>(out + (static_cast<int64_t>(p.g.row0) * a.heads + m0) * kLatDv + half * 256);
-#pragma unroll 1
-                for (uint32_t x = 0; x < 256u; x += 64u) {
-                    uint4 u[8];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float o[32];
-                        if (p.tiles > 0) {
-                            tmem_ld_x32(tmem + lane_base + x + 32u * h, o);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = 0.f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(any ? o[8 * j + 2 * i] * f : 0.f,
-                                                                                any ? o[8 * j + 2 * i + 1] * f : 0.f);
-                                w[i] = *reinterpret_cast<const uint32_t*>(&b2);
-                            }
-                            u[4 * h + j] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    }
-                    store_rows(gP + warp * 4096, u, dst + 2 * x, kLatDv * 2, live - m0);
-                }
-                if (lives && half == 0) lse[at] = any ? (m + log2f(L)) * 0.69314718055994531f : -INFINITY;
-            } else {
-                uint8_t* const part = plan.part + static_cast<size_t>(2 * ci + (p.lo > 0 ? 0 : 1)) * kPartBytes;
-                uint8_t* const dst = part + (static_cast<size_t>(m0) * kLatDv + half * 256) * 4;
-#pragma unroll 1
-                for (uint32_t x = 0; x < 256u; x += 32u) {
-                    float o[32];
-                    tmem_ld_x32(tmem + lane_base + x, o);
-                    uint4 u[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        u[j] = make_uint4(__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]), __float_as_uint(o[4 * j + 2]),
-                                          __float_as_uint(o[4 * j + 3]));
-                    store_rows(gP + warp * 4096, u, dst + 4 * x, kLatDv * 4, live - m0);
-                }
-                if (half == 0) {
-                    reinterpret_cast<float*>(part + kPartO)[mi] = m;
-                    reinterpret_cast<float*>(part + kPartO)[kM + mi] = L;
+                if (p.hi > p.lo) ctl->fin[row] = !whole ? 1.f : any ? 1.f / L : 0.f;
+                if (!whole) {
+                    float* const ml = reinterpret_cast<float*>(plan.part + static_cast<size_t>(2 * ci + (p.lo > 0 ? 0 : 1)) * kPartBytes + kPartO);
+                    ml[mi] = m;
+                    ml[kM + mi] = L;
+                } else if (lives) {
+                    lse[static_cast<int64_t>(p.g.row0) * a.heads + mi] = any ? (m + log2f(L)) * 0.69314718055994531f : -INFINITY;
                 }
             }
-            tc_fence_before();  // O is read: the next group's first PV, ordered by its P, may overwrite it
+            if (p.hi > p.lo) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl->fin_ready));
+                (void)softmax_sync_or(false);  // mx is read before the next tile's maxima
+            }
         }
         if (!ok) *abort = 1;
     } else if (warp < 8) {
@@ -692,6 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int it = p.lo; it < p.hi; ++it, ++t) {
                 const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
                 const int64_t row = own.row(a);
+                const uint32_t bits = __ballot_sync(0xffffffffu, row >= 0);  // 8 of this CTA's tokens, 8 of the other's
                 own.next(a, p);
                 if (plan.ahead && lane >= 16 && lane < 24 && row >= 0)
                     prefetch_l2(a.kv + row * kLatRowBytes, kLatRowBytes);
@@ -715,7 +684,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 2; ++i) cp_async_16(dst[i] + j * kKAtom, src[i] + 128 * j, n[i]);
                     cp_async_arrive_noinc(smem_addr(&ctl->k_full[st][ch]));
                     if (ch == 0) {
-                        if (lane < 16) ctl->valid[t & (kValid - 1)][mine] = row < 0 ? 0 : 1;
+                        if (lane < 2)
+                            reinterpret_cast<uint8_t*>(ctl->valid[t & (kValid - 1)])[(c ^ lane) * 4 + w] =
+                                static_cast<uint8_t>(bits >> (8 * lane));
                         mbar_arrive(smem_addr(&ctl->k_full[st][0]));
                     }
                 }
@@ -770,6 +741,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             while (ok && walk.next(&p)) {
                 if (p.hi == p.lo) continue;
                 if (qk) ok = mbar_wait_cluster(smem_addr(&ctl->q_ready), groups & 1u, abort);
+                else if (groups > 0) ok = mbar_wait_cluster(smem_addr(&ctl->o_free), (groups - 1) & 1u, abort);
                 ++groups;
                 for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
                     const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
@@ -832,6 +804,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
         }
         if (!ok && lane == 0) *abort = 1;
+    } else if (warp >= 16) {
+        // ---- the results.  Read 16 rows x 32 columns at a time, four lanes to a row, so that stores are whole
+        // sectors: a lane a row, straight to memory, took 5 us a group, through shared memory by the softmax warps 3
+        const int half = (warp & 3) >> 1, r_cta = (warp & 1) * 32;  // dims 256 half .., rows of this CTA's 64
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int q = lane & 3;
+        uint32_t pieces = 0;
+        bool ok = true;
+        while (ok && walk.next(&p)) {
+            const bool whole = p.lo == 0 && p.hi == p.tiles;
+            const int live = p.g.rows * a.heads - static_cast<int>(c) * 64 - r_cta;  // of this warp's 32 rows
+            const int64_t at = static_cast<int64_t>(p.g.row0) * a.heads + static_cast<int>(c) * 64 + r_cta;
+            uint8_t* const dst = whole ? reinterpret_cast<uint8_t*>(out + at * kLatDv + half * 256) : nullptr;
+            if (p.hi == p.lo) {  // nothing was seen
+                for (int i = lane; i < 32 * 32; i += 32)
+                    if ((i >> 5) < live) reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i >> 5) * (kLatDv * 2))[i & 31] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            t += static_cast<uint32_t>(p.hi - p.lo);
+            // (P of the last tile was written after PV of the one two before)
+            ok = mbar_wait(smem_addr(&ctl->fin_ready), pieces & 1u, abort) &&
+                 mbar_wait(smem_addr(&ctl->pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, abort);
+            ++pieces;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            uint8_t* const part = plan.part + static_cast<size_t>(2 * ci + (p.lo > 0 ? 0 : 1)) * kPartBytes +
+                                  (static_cast<size_t>(static_cast<int>(c) * 64 + r_cta) * kLatDv + half * 256) * 4;
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = ctl->fin[r_cta + 8 * i + (lane >> 2)];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&ctl->fin_free));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll 1
+                for (uint32_t x = 0; x < 256u; x += 32u) {
+                    float o[16];
+                    tmem_ld_16x256_x4(tmem + lane_base + (static_cast<uint32_t>(16 * h) << 16) + x, o);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int r = 16 * h + 8 * g + (lane >> 2);
+                        const float ff = f[2 * h + g];
+                        if (whole) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[4 * b + 2 * g] * ff, o[4 * b + 2 * g + 1] * ff);
+                                w[b] = *reinterpret_cast<const uint32_t*>(&b2);
+                            }
+                            quad_transpose(w, q);  // lane q now has columns 8q .. 8q + 7 of the 32
+                            if (r < live)
+                                *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(r) * (kLatDv * 2) + 2 * x + 16 * q) =
+                                    make_uint4(w[0], w[1], w[2], w[3]);
+                        } else if (r < live) {
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                *reinterpret_cast<float2*>(part + static_cast<int64_t>(r) * (kLatDv * 4) + 4 * x + 32 * b + 8 * q) =
+                                    make_float2(o[4 * b + 2 * g], o[4 * b + 2 * g + 1]);
+                        }
+                    }
+                }
+            tc_fence_before();  // O is read: the next group's first PV may overwrite it
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->o_free), 0);
+        }
+        if (!ok) *abort = 1;
     } else {
         // ---- V has landed here
         if (c == 0 && ci > 0 && lane == 0) {  // first, for the join: whether this share starts the second part of a group
