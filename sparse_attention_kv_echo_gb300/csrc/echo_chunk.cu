@@ -18,16 +18,23 @@
 //               dims [256c, 256c + 256) of all 64 tokens, read in place as an
 //               MN-major operand.
 // Neither product is done twice, and the softmax needs nothing from the other
-// CTA.  Warps of a CTA: 0-3 softmax (thread = TMEM lane; the two threads of a
-// row exchange their tile maxima in shared memory), 16-19 store O, 4-7 gather K, 8-11 gather V
-// (16-byte cp.async: any row for any token; two stages of each, K in
-// thirds that are refilled as their MMAs end), 12 of CTA 0 issues the MMAs, 13
-// and 14 report what has landed in their CTA to it (one barrier for both CTAs: each
-// wait costs the issuing warp a hundred cycles).  QK of tile t + 1 is
-// issued before PV of tile t and P has two buffers, so the softmax runs under the
-// tensor cores.  The softmax reference moves only when a score exceeds it by
-// more than 2^8 (P <= 256 in bf16, exact after the final division); O in TMEM is
-// rescaled then.
+// CTA.  Warps of a CTA: 0-3 softmax (thread = TMEM lane; the two threads of a row
+// exchange their tile maxima in shared memory), 4-7 gather K, 8-11 gather V
+// (16-byte cp.async: any row for any token; two stages of each), 12 and 13 of CTA 0
+// issue the MMAs of QK and of PV, 14 loads Q by TMA, 14 and 15 report what has
+// landed in their CTA to CTA 0, 16-19 store O.  There are four S buffers and two of P, so QK runs up
+// to four tiles ahead and the softmax under the tensor cores.  Its reference moves
+// only when a score exceeds it by more than 2^8 (P <= 256 in bf16, exact after the
+// final division); O in TMEM is rescaled then.
+//
+// What bounds it: an MMA of QK reads 3 KB of shared memory for 16 cycles of
+// products and takes 25, one of PV 6 KB for 64; a tile's 36 + 8 take 1421 cycles
+// (2261 us of the 2.76 ms of 2048 rows over 8192 tokens at 1.9 GHz).  More tokens to
+// a tile would help QK and do not fit: Q 72 KB, two stages of K 36 KB and V 32 KB,
+// P 16 KB.  Left out for a measurement, the copies give 7% and the exponentials 5%;
+// a group's change costs 3000 cycles (Q can only be replaced when its last QK is done).
+// Decode is bound by the same loop and by its ends: the first loads, the parts' 256 KB
+// a piece and their join.
 //
 // Work: every tile costs the same and a group costs kOver tiles more (its Q, its
 // result).  chunk_plan_kernel lays the groups' costs in a row; cluster i takes the
@@ -50,7 +57,6 @@ constexpr uint32_t kQAtom = 64 * 128;    // 64 rows x 128 B
 constexpr uint32_t kKAtom = 32 * 128;    // this CTA's 32 tokens
 constexpr uint32_t kVAtom = kTok * 128;  // 64 tokens x 64 dims
 constexpr uint32_t kQBytes = kAtoms * kQAtom;
-constexpr int kChunks = 1;               // parts in which K of a tile comes and goes
 constexpr uint32_t kKBytes = kAtoms * kKAtom;
 constexpr uint32_t kVBytes = 4 * kVAtom;
 constexpr uint32_t kPBytes = 64 * 128;
@@ -363,8 +369,8 @@ static_assert(kValid >= kSBufs + 3, "valid flags");
 struct Ctl {
     // here: landed in this CTA; the *_ready barriers of CTA 0: landed in both
     uint64_t q_full, q_ready;                            // Q of a group
-    uint64_t k_full[2][kChunks], k_ready[2][kChunks];    // a third of a stage's K
-    uint64_t k_free[2][kChunks];                         // its MMAs are done
+    uint64_t k_full[2], k_ready[2];                      // K of a stage
+    uint64_t k_free[2];                                  // its MMAs are done
     uint64_t v_full[2];                                  // V of a stage
     uint64_t pv_ready[2];                                // V, and P of the tile, in both CTAs
     uint64_t pv_done[2];                                 // P V of a tile done: V stage and P buffer free, O ready
@@ -423,13 +429,12 @@ __device__ __forceinline__ bool softmax_sync_or(bool v) {
 // The MMAs of stage ST.  The stage is a constant so that every descriptor is one too: with
 // descriptors computed from a variable stage an MMA took 100 cycles to issue, four times what it runs.
 template <int ST>
-__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t sQ, uint32_t sK, int ch) {
+__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t sQ, uint32_t sK) {
     const uint64_t ad = sw128_kmajor_desc(sQ), bd = sw128_kmajor_desc(sK + ST * kKBytes);
 #pragma unroll
     for (int kk = 0; kk < 4 * kAtoms; ++kk)
-        if (kk / (4 * kAtoms / kChunks) == ch)
-            mma2_bf16(d, ad + (((kk >> 2) * kQAtom + (kk & 3) * 32u) >> 4),
-                      bd + (((kk >> 2) * kKAtom + (kk & 3) * 32u) >> 4), kIdescS, kk > 0 ? 1u : 0u);
+        mma2_bf16(d, ad + (((kk >> 2) * kQAtom + (kk & 3) * 32u) >> 4), bd + (((kk >> 2) * kKAtom + (kk & 3) * 32u) >> 4),
+                  kIdescS, kk > 0 ? 1u : 0u);
 }
 template <int ST>
 __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t sP, uint32_t sV, bool add) {
@@ -463,11 +468,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&ctl->q_full), 1);
         mbar_init(smem_addr(&ctl->q_ready), 2);
         for (int i = 0; i < 2; ++i) {
-            for (int j = 0; j < kChunks; ++j) {
-                mbar_init(smem_addr(&ctl->k_full[i][j]), j == 0 ? 2 * kLoad : kLoad);  // the copies; first: the valid flags too
-                mbar_init(smem_addr(&ctl->k_ready[i][j]), 2);
-                mbar_init(smem_addr(&ctl->k_free[i][j]), 1);
-            }
+            mbar_init(smem_addr(&ctl->k_full[i]), 2 * kLoad);  // the copies, and the valid flags
+            mbar_init(smem_addr(&ctl->k_ready[i]), 2);
+            mbar_init(smem_addr(&ctl->k_free[i]), 1);
             mbar_init(smem_addr(&ctl->v_full[i]), kLoad);
             mbar_init(smem_addr(&ctl->pv_ready[i]), 2 * kSoftmax / 32 + 2);
             mbar_init(smem_addr(&ctl->pv_done[i]), 1);
@@ -646,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!ok) *abort = 1;
     } else if (warp < 8) {
-        // ---- K of this CTA's 32 tokens, a third of the dims at a time.  A warp has 8 tokens and copies
+        // ---- K of this CTA's 32 tokens.  A warp has 8 tokens and copies
         // four 128-byte row pieces per instruction (8 lanes each): with 64-byte pieces of 8 rows the
         // copies took twice the shared-memory cycles.  Lanes 0-7 look up the warp's tokens, lanes 8-15
         // those of the other CTA, for the valid flags.
@@ -674,24 +677,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     n[i] = rk < 0 ? 0u : 16u;
                     dst[i] = sK + st * kKBytes + static_cast<uint32_t>(8 * w + r) * 128u + (static_cast<uint32_t>(x ^ r) << 4);
                 }
-#pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch) {
-                    if (t >= 2 && ok) ok = mbar_wait(smem_addr(&ctl->k_free[st][ch]), ph ^ 1u, abort);
-                    if (!ok) break;
-#pragma unroll
-                    for (int j = kAtoms / kChunks * ch; j < kAtoms / kChunks * (ch + 1); ++j)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) cp_async_16(dst[i] + j * kKAtom, src[i] + 128 * j, n[i]);
-                    cp_async_arrive_noinc(smem_addr(&ctl->k_full[st][ch]));
-                    if (ch == 0) {
-                        if (lane < 2)
-                            reinterpret_cast<uint8_t*>(ctl->valid[t & (kValid - 1)])[(c ^ lane) * 4 + w] =
-                                static_cast<uint8_t>(bits >> (8 * lane));
-                        mbar_arrive(smem_addr(&ctl->k_full[st][0]));
-                    }
-                }
+                if (t >= 2) ok = mbar_wait(smem_addr(&ctl->k_free[st]), ph ^ 1u, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < kAtoms; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) cp_async_16(dst[i] + j * kKAtom, src[i] + 128 * j, n[i]);
+                cp_async_arrive_noinc(smem_addr(&ctl->k_full[st]));
+                if (lane < 2)
+                    reinterpret_cast<uint8_t*>(ctl->valid[t & (kValid - 1)])[(c ^ lane) * 4 + w] =
+                        static_cast<uint8_t>(bits >> (8 * lane));
+                mbar_arrive(smem_addr(&ctl->k_full[st]));
             }
         }
         if (!ok) *abort = 1;
@@ -748,17 +745,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (qk) {
                         if (t >= kSBufs)
                             ok = mbar_wait_cluster(smem_addr(&ctl->s_free[t & (kSBufs - 1)]), ((t / kSBufs) & 1u) ^ 1u, abort);
-#pragma unroll
-                        for (int ch = 0; ch < kChunks; ++ch) {
-                            ok = ok && mbar_wait_cluster(smem_addr(&ctl->k_ready[st][ch]), ph, abort);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t d = tmem + kSCol + (t & (kSBufs - 1)) * 32u;
-                            if (st == 0) issue_qk<0>(d, sQ, sK, ch);
-                            else issue_qk<1>(d, sQ, sK, ch);
-                            mma2_commit_both(smem_addr(&ctl->k_free[st][ch]));
-                        }
-                        if (ok) mma2_commit_both(smem_addr(&ctl->s_full[t & (kSBufs - 1)]));
+                        ok = ok && mbar_wait_cluster(smem_addr(&ctl->k_ready[st]), ph, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + kSCol + (t & (kSBufs - 1)) * 32u;
+                        if (st == 0) issue_qk<0>(d, sQ, sK);
+                        else issue_qk<1>(d, sQ, sK);
+                        mma2_commit_both(smem_addr(&ctl->k_free[st]));
+                        mma2_commit_both(smem_addr(&ctl->s_full[t & (kSBufs - 1)]));
                     } else {  // O += P V
                         ok = mbar_wait_cluster(smem_addr(&ctl->pv_ready[st]), ph, abort);
                         if (!ok) break;
@@ -784,7 +778,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (p.hi == p.lo) continue;
             // Q of the group, once the group before has no QK left.  Its (row, head) pairs are consecutive in q;
             // pairs past the group's own are another group's, or zeros, and their results are dropped
-            if (t >= 1) ok = mbar_wait(smem_addr(&ctl->k_free[(t - 1) & 1u][kChunks - 1]), ((t - 1) >> 1) & 1u, abort);
+            if (t >= 1) ok = mbar_wait(smem_addr(&ctl->k_free[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, abort);
             if (!ok) break;
             if (elect_one()) {
                 const uint32_t bar = smem_addr(&ctl->q_full);
@@ -796,12 +790,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = mbar_wait(smem_addr(&ctl->q_full), groups & 1u, nullptr);  // always: the load lands before the CTA ends
             ++groups;
             if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->q_ready), 0);
-            for (int it = p.lo; ok && it < p.hi; ++it, ++t)
-                for (int ch = 0; ok && ch < kChunks; ++ch) {
-                    ok = mbar_wait(smem_addr(&ctl->k_full[t & 1u][ch]), (t >> 1) & 1u, abort);
-                    fence_proxy_async_smem();
-                    if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->k_ready[t & 1u][ch]), 0);
-                }
+            for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
+                ok = mbar_wait(smem_addr(&ctl->k_full[t & 1u]), (t >> 1) & 1u, abort);
+                fence_proxy_async_smem();
+                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->k_ready[t & 1u]), 0);
+            }
         }
         if (!ok && lane == 0) *abort = 1;
     } else if (warp >= 16) {
