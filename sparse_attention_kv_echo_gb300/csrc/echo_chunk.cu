@@ -1068,6 +1068,6 @@ extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int
     ECHO_CUDA_OK(launch_after(plan.small, chunk_kernel, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan, qmap,
                               scale * 1.4426950408889634f, out, lse));
     if (plan.clusters > 1)
-        ECHO_CUDA_OK(launch_after(false, chunk_join_kernel, dim3(static_cast<unsigned>(16 * sm_count())), kJT, 0, s, a, plan, out, lse));
+        ECHO_CUDA_OK(launch_after(false, chunk_join_kernel, dim3(static_cast<unsigned>(8 * sm_count())), kJT, 0, s, a, plan, out, lse));
     return ECHO_OK;
 }

@@ -14,9 +14,9 @@
 // shared memory as order keys (up to 53248 a CTA; further ones are gathered
 // again).  The histograms of a pass are added up over the cluster in distributed shared
 // memory by every CTA for itself.  Bound by the latency of its steps (two dependent
-// loads, 2 to 8 passes with two cluster barriers each), not by its bytes: 1 x 260000
-// slots take 40 us with 16 CTAs and 70 with 8, 8 x 4096 take 16 us with 4 CTAs a
-// request and 24 with one.
+// loads, 2 to 8 passes with a cluster barrier each), not by its bytes: 1 x 260000
+// slots take 41 us with 16 CTAs and 70 with 8 (the random gather of the masses by 16
+// SMs is 10 of them), 8 x 4096 take 17 us with 4 CTAs a request and 24 with one.
 #include <cooperative_groups.h>
 
 #include "echo_common.cuh"
@@ -64,7 +64,7 @@ struct Keys {
 };
 
 struct EvictShared {
-    uint32_t hist[256];       // this CTA's
+    uint32_t hist[2][256];    // this CTA's, by pass parity
     uint32_t sum[256];        // the cluster's
     uint32_t held, cand, victims;
     uint32_t digit, below;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kET)
     k.len = hi - lo;
     k.sinks = sinks;
     k.late = recent < k.len ? k.len - recent : 0;
-    if (tid < 256) sh.hist[tid] = 0;
+    if (tid < 256) sh.hist[0][tid] = 0;
     if (tid == 0) sh.held = sh.cand = 0;
     __syncthreads();
     // ---- the keys, and how many there are
@@ -167,26 +167,29 @@ __global__ void __launch_bounds__(kET)
     uint32_t need = want;
     bool all_keys = want == 0 || want == cand;
     // One pass: the boundary digit of `need` among f(slot, &value) at `shift`.  True when its bin is wanted whole.
+    int parity = 0;
     const auto pass = [&](int shift, auto f) {
+        uint32_t* const hist = sh.hist[parity];
         for (int s0 = w0; s0 < w1; s0 += 32) {
             const int s = s0 + lane;
             uint32_t v = 0;
             const bool in = s < w1 && f(s, &v);
-            if (in) atomicAdd(&sh.hist[(v >> shift) & 255u], 1u);
+            if (in) atomicAdd(&hist[(v >> shift) & 255u], 1u);
         }
-        cluster.sync();
+        cluster.sync();  // the counts are there; and every CTA is done with the other buffer
         if (tid < 256) {
             uint32_t x = 0;
-            for (int r = 0; r < n_cta; ++r) x += cluster.map_shared_rank(&sh, r)->hist[tid];
+            for (int r = 0; r < n_cta; ++r) x += cluster.map_shared_rank(&sh, r)->hist[parity][tid];
             sh.sum[tid] = x;
+        } else if (tid < 512) {
+            sh.hist[parity ^ 1][tid - 256] = 0;
         }
         __syncthreads();
         if (warp == 0) digit_from_below(sh.sum, need, &sh.digit, &sh.below);
-        cluster.sync();  // every CTA has read the histograms
-        if (tid < 256) sh.hist[tid] = 0;
+        __syncthreads();
+        parity ^= 1;
         need -= sh.below;
-        const bool whole = sh.sum[sh.digit] == need;
-        return whole;
+        return sh.sum[sh.digit] == need;
     };
     if (!all_keys) {
         uint32_t prefix = 0;
@@ -198,8 +201,7 @@ __global__ void __launch_bounds__(kET)
                 *v = k.at(c0, s);
                 return *v != kNone && (*v & top) == prefix;
             });
-            prefix |= sh.digit << shift;
-            __syncthreads();  // sh.digit and sh.sum are read
+            prefix |= sh.digit << shift;  // (read before the next pass's cluster barrier, written after it)
             if (whole) break;
         }
         if (whole) {
@@ -217,7 +219,6 @@ __global__ void __launch_bounds__(kET)
                     return (*v & top) == last_tok;
                 });
                 last_tok |= sh.digit << shift;
-                __syncthreads();
                 if (whole) break;
             }
             if (shift > 0) last_tok |= (1u << shift) - 1u;
