@@ -28,8 +28,9 @@
 // final division); O in TMEM is rescaled then.
 //
 // What bounds it: an MMA of QK reads 3 KB of shared memory for 16 cycles of
-// products and takes 25, one of PV 6 KB for 64; a tile's 36 + 8 take 1421 cycles
-// (2261 us of the 2.76 ms of 2048 rows over 8192 tokens at 1.9 GHz).  More tokens to
+// products and takes 25, one of PV 6 KB for 64 (rates of single MMAs); a tile's 36 + 8
+// come to 1421 cycles, 2.47 ms of the 2.81 ms of 2048 rows over 8192 tokens at the 1747 MHz
+// (median) that the power cap leaves in repeated calls.  More tokens to
 // a tile would help QK and do not fit: Q 72 KB, two stages of K 36 KB and V 32 KB,
 // P 16 KB.  Left out for a measurement, the copies give 7% and the exponentials 5%;
 // a group's change costs 3000 cycles (Q can only be replaced when its last QK is done).
