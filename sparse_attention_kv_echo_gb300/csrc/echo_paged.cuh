@@ -70,7 +70,7 @@ inline ChunkArgs chunk_args(int B, const int64_t* row_off, int64_t n_rows, int h
     a.page = static_cast<uint32_t>(pg->page);
     a.sel = sel;
     a.k = sel ? k : 0;
-    a.window = window;
+    a.window = window < kMaxLen ? window : kMaxLen;  // no context is longer: positions + window stay in 64 bits
     a.sinks = sinks;
     a.q = q;
     a.scale = scale;

@@ -303,6 +303,14 @@ def test_weights_window(lens, rows, heads, window, sinks, decay, absent):
     _weigh(P.Batch(lens, rows, heads, 1, seed=window, absent=absent), decay, window, sinks, in_place=decay == 1.0)
 
 
+@pytest.mark.parametrize("window", [2 ** 63 - 1, 2 ** 62, 0x7FFFFF00, 701])
+def test_a_window_as_wide_as_any_context_hides_nothing(window):
+    bt = P.Batch([700, 90], [200, 1], 16, 16, seed=9)
+    for sinks in (0, 2 ** 63 - 1):
+        _weigh(bt, 0.5, window, sinks)
+        _compare(bt, _attend(bt, window, sinks), window, sinks)
+
+
 def test_weights_without_decay_read_no_old_mass():
     bt = P.Batch([70], [4], 128, 16, seed=1)
     row_off, q, tok_off, tok_end, pages = bt.on(dev, L)
