@@ -428,7 +428,8 @@ class DecodeLayer:
         # quantize, then per group: score (+ early fetch) + top-k + cache step + late recall
         att = 1 if self.attention else 0
         if self.pool_slots:  # quantize, score, top-k, select, cache step, recall, slots (+ marks, early fetch)
-            return 7 + (2 if self.predictor else 0) + 3 * att  # attention: plan, tiles, join
+            # attention: tiles and join; more requests than a warp has lanes take a plan kernel before them
+            return 7 + (2 if self.predictor else 0) + (2 + (self.B > 32)) * att
         if not self.predictor:
             return 5 + att
         if self.cross_layer:  # quantize, score, top-k, cache step, recall + seed, early fetch (seeded steps)

@@ -563,3 +563,32 @@ def test_a_shared_pool_attends(hold_early, graph):
         sel = lay.sel_idx.cpu()
         bt = _plain_selected(mq, host, off, sel, lay.mla_scale)
         _compare(bt, (lay.attn_out.cpu(), lay.attn_lse.cpu()), sel=sel)
+
+
+@pytest.mark.parametrize("B", [3, 32, 33])
+def test_a_pool_steps_launches_are_what_it_says(B):
+    from torch.profiler import ProfilerActivity, profile
+    from sparse_attention_kv_echo_gb300 import DecodeLayer
+    from sparse_attention_kv_echo_gb300 import workloads as wl
+    w = wl.scaled(wl.WORKLOADS["batch"], "poolcount", B=B, lengths=(300,) * B, k=64, C=128)
+    k8, ks = wl.make_keys(w, 0)
+    host = wl.make_host_pool(w, 0, pin=True)
+    off, q = wl.tok_offsets(w.lengths), wl.QueryStream(w, 0).next().to(dev)
+    said, ran = [], []
+    with profile(activities=[ProfilerActivity.CUDA]):  # a process's first session may come out empty
+        torch.zeros(1, device=dev)
+        torch.cuda.synchronize()
+    for attention in (False, True):
+        lay = DecodeLayer(off, k8.to(dev), ks.to(dev), w.k, w.C, host, pool_slots=B * 96, attention=attention)
+        lay.w_in.copy_(wl.make_weights(w, 0).to(dev))
+        lay.q_in.copy_(q)
+        lay.step()
+        torch.cuda.synchronize()
+        with profile(activities=[ProfilerActivity.CUDA]) as prof:
+            lay.step()
+            torch.cuda.synchronize()
+        assert int(lay.status.item()) == 0
+        said.append(lay.kernel_launches_per_step())
+        ran.append(sum("echo::" in e.name and e.device_type == torch.autograd.DeviceType.CUDA for e in prof.events()))
+    assert said == ran
+    assert said[1] - said[0] == (2 if B <= 32 else 3)
