@@ -451,16 +451,17 @@ def mla_mass(row_off, q, lse, tok_off, n_tokens, pages, scale, mass, mass_out, s
     """echo_mla_mass: mass_out [n_tokens] f32 = decay * mass + the attention weight each token
     receives from the rows of an mla_chunk call (the same q, pages, window and sinks, and its lse),
     summed over rows and heads.  mass_out may be mass.  ws: uint8, mla_mass_workspace_size(n_tokens,
-    B) (None: one is taken from torch's allocator for the call)."""
+    B) (None: one is taken from torch's allocator, on `stream`, for the call)."""
     B, n, heads = _check_chunk("mla_mass", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end,
                                ("mass", mass, torch.float32, (n_tokens,)),
                                ("mass_out", mass_out, torch.float32, (n_tokens,)))
     if ws is None:
-        ws = torch.empty(mla_mass_workspace_size(n_tokens, B), dtype=torch.uint8, device=q.device)
-        if isinstance(stream, torch.cuda.Stream):
-            ws.record_stream(stream)
-        elif stream is not None:
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
             raise ValueError("mla_mass: a stream given by its handle needs ws")
+        # from the pool of the stream that uses it: a block of the current stream's pool may still be read or
+        # written by kernels pending there when it is handed out
+        with torch.cuda.stream(stream):
+            ws = torch.empty(mla_mass_workspace_size(n_tokens, B), dtype=torch.uint8, device=q.device)
     else:
         _expect("mla_mass", torch.cuda.current_device(), ("ws", ws, torch.uint8, (ws.numel(),)))
     _check("echo_mla_mass", load().echo_mla_mass(

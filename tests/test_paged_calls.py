@@ -1,0 +1,83 @@
+"""The wrappers of the paged calls on the CPU: what they hand to the library, with the library and the
+device replaced by recorders."""
+import contextlib
+
+import pytest
+import torch
+
+from sparse_attention_kv_echo_gb300 import _lib as L
+
+
+class _Recorder:
+    """Stands in for the loaded library: keeps every call's arguments and succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 4096 if name.endswith("_size") else L.ECHO_OK
+        return call
+
+
+class _Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """CPU tensors pass for the current device's (get_device() of both is -1); the current stream and every
+    torch.empty made under it are recorded."""
+    rec = _Recorder()
+    rec.current, rec.taken = _Stream(1), []
+
+    @contextlib.contextmanager
+    def use(s):
+        before = rec.current
+        rec.current = before if s is None else s
+        try:
+            yield
+        finally:
+            rec.current = before
+
+    empty = torch.empty
+
+    def recorded(*a, **kw):
+        t = empty(*a, **kw)
+        rec.taken.append((t.data_ptr(), rec.current.cuda_stream))
+        return t
+    monkeypatch.setattr(L, "load", lambda *a, **kw: rec)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(torch.cuda, "Stream", _Stream)
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: rec.current)
+    monkeypatch.setattr(L, "_raw_stream", None)
+    monkeypatch.setattr(torch, "empty", recorded)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda *a: None)
+    return rec
+
+
+def _weigh(**kw):
+    off = torch.tensor([0, 10])
+    pages = L.KVPages(torch.zeros(1, dtype=torch.int32), torch.zeros((16, 576), dtype=torch.bfloat16), 16)
+    mass = torch.zeros(10)
+    L.mla_mass(off, torch.zeros((10, 2, 576), dtype=torch.bfloat16), torch.zeros((10, 2)), off, 10, pages, 0.1, mass, mass,
+               torch.zeros(1, dtype=torch.int32), **kw)
+
+
+@pytest.mark.parametrize("stream", [None, 7])
+def test_a_workspace_taken_for_a_call_belongs_to_its_stream(host, stream):
+    # a block of another stream's pool may still be in use there when it is handed out
+    _weigh(stream=None if stream is None else _Stream(stream))
+    (name, args), = [c for c in host.calls if c[0] == "echo_mla_mass"]
+    ws, used_on = args[-4], args[-1]
+    assert used_on == (1 if stream is None else stream)
+    assert (ws, used_on) in host.taken
+
+
+def test_a_stream_handle_needs_a_workspace(host):
+    with pytest.raises(ValueError):
+        _weigh(stream=7)
+    _weigh(stream=7, ws=torch.zeros(4096, dtype=torch.uint8))
