@@ -596,7 +596,11 @@ int echo_mla_mass(int B, const int64_t* row_off, int64_t n_rows, int heads, cons
 /*
  * Eviction by accumulated attention weight: the victims of each request's cache
  * (slot2tok [B*C] as in echo_cache, any C >= 1) when it has to shrink to `keep`
- * resident tokens.  A slot with slot2tok >= 0 holds a resident.  Of the
+ * resident tokens.  A slot with slot2tok >= 0 holds a resident; under lazy reuse
+ * (ECHO_CACHE_LAZY), where a freed slot keeps its token, only when its free bit is
+ * clear: echo_evict_select_resident reads the free bits too (freebits [B*C/32] as in
+ * echo_cache, C a multiple of 32; NULL: the same as echo_evict_select, which is not
+ * for such a cache).  Of the
  * residents outside the request's first `sinks` and last `recent` tokens, the
  * max(0, residents - keep) with the lowest mass[tok_off[b] + token] are the
  * victims (all of them when they are fewer); equal masses: the lower token.
@@ -608,8 +612,12 @@ int echo_mla_mass(int B, const int64_t* row_off, int64_t n_rows, int heads, cons
  * victims and ECHO_ST_BADDATA.  The call changes no table; echo_cache_release
  * does.  mass [n_tokens] f32.  keep, sinks, recent >= 0.
  * Errors: ECHO_EINVAL (sizes, NULL pointers), ECHO_EUNSUPPORTED
- * (B > ECHO_MAX_REQUESTS, C > 524288), ECHO_ECUDA.
+ * (B > ECHO_MAX_REQUESTS, C > 524288), ECHO_ECAPACITY (C with freebits), ECHO_ECUDA.
  */
+int echo_evict_select_resident(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens,
+                               const int32_t* slot2tok, const uint32_t* freebits, int C, const float* mass, int64_t keep,
+                               int64_t sinks, int64_t recent, int32_t* evict_tok, int32_t* evict_slot,
+                               int32_t* evict_cnt, int32_t* status, echo_stream_t stream);
 int echo_evict_select(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens,
                       const int32_t* slot2tok, int C, const float* mass, int64_t keep, int64_t sinks, int64_t recent,
                       int32_t* evict_tok, int32_t* evict_slot, int32_t* evict_cnt, int32_t* status,

@@ -29,7 +29,7 @@ EARLY_FETCH_BLOCKS = 24      # CTAs of the early-fetch and late-recall kernels
 
 EXPORTS = ("echo_above_words", "echo_append_tokens", "echo_cache_release", "echo_cache_step", "echo_cache_step_resolved",
            "echo_debug_stall_epilogue", "echo_device_sm_count",
-           "echo_early_fetch", "echo_evict_select", "echo_host_device_alias", "echo_index_scores", "echo_index_scores_cands", "echo_mla_chunk",
+           "echo_early_fetch", "echo_evict_select", "echo_evict_select_resident", "echo_host_device_alias", "echo_index_scores", "echo_index_scores_cands", "echo_mla_chunk",
            "echo_mla_chunk_workspace_size", "echo_mla_decode", "echo_mla_mass",
            "echo_mla_mass_workspace_size", "echo_pool_above", "echo_pool_select",
            "echo_pool_slots", "echo_prefill_block",
@@ -120,6 +120,9 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         L.echo_mla_mass_workspace_size.argtypes = [i64, i32]
         L.echo_evict_select.restype = i32
         L.echo_evict_select.argtypes = [i32, _vp, _vp, i64, _vp, i32, _vp, i64, i64, i64, _vp, _vp, _vp, _vp, _vp]
+        L.echo_evict_select_resident.restype = i32
+        L.echo_evict_select_resident.argtypes = [i32, _vp, _vp, i64, _vp, _vp, i32, _vp, i64, i64, i64, _vp, _vp, _vp, _vp,
+                                                 _vp]
         L.echo_cache_release.restype = i32
         L.echo_cache_release.argtypes = [i32, _vp, _vp, i64, _vp, i32, ctypes.POINTER(EchoCacheStruct), _vp, _vp, _vp]
         L.echo_pool_above.restype = i32
@@ -471,10 +474,12 @@ def mla_mass(row_off, q, lse, tok_off, n_tokens, pages, scale, mass, mass_out, s
 
 
 def evict_select(tok_off, n_tokens, slot2tok, mass, keep, evict_tok, evict_slot, evict_cnt, status, sinks=0, recent=0,
-                 tok_end=None, stream=None):
+                 tok_end=None, stream=None, freebits=None):
     """echo_evict_select: the victims of each request's cache (slot2tok [B*C] or [B,C]) when it has to
     shrink to `keep` residents: those of the lowest mass [n_tokens], the first `sinks` and last
-    `recent` tokens spared -> evict_tok / evict_slot [B,C] (ascending slots, -1 behind), evict_cnt [B]."""
+    `recent` tokens spared -> evict_tok / evict_slot [B,C] (ascending slots, -1 behind), evict_cnt [B].
+    freebits: the cache's free bits (a LayerCache's, or a slice of them); a cache under lazy reuse needs them, as
+    its free slots keep their tokens."""
     B = tok_off.shape[0] - 1
     C = slot2tok.numel() // B
     dev = torch.cuda.current_device()
@@ -485,9 +490,11 @@ def evict_select(tok_off, n_tokens, slot2tok, mass, keep, evict_tok, evict_slot,
             ("status", status, torch.int32, (1,)))
     if tok_end is not None:
         _expect("evict_select", dev, ("tok_end", tok_end, torch.int64, (B,)))
-    _check("echo_evict_select", load().echo_evict_select(
-        B, _ptr(tok_off), _ptr(tok_end), int(n_tokens), _ptr(slot2tok), C, _ptr(mass), int(keep), int(sinks),
-        int(recent), _ptr(evict_tok), _ptr(evict_slot), _ptr(evict_cnt), _ptr(status), _stream(stream)))
+    if freebits is not None:
+        _expect("evict_select", dev, ("freebits", freebits, torch.int32, (B * C // 32,)))
+    _check("echo_evict_select_resident", load().echo_evict_select_resident(
+        B, _ptr(tok_off), _ptr(tok_end), int(n_tokens), _ptr(slot2tok), _ptr(freebits), C, _ptr(mass), int(keep),
+        int(sinks), int(recent), _ptr(evict_tok), _ptr(evict_slot), _ptr(evict_cnt), _ptr(status), _stream(stream)))
 
 
 def cache_release(tok_off, n_tokens, tok, cache, status, mass=None, tok_end=None, stream=None):

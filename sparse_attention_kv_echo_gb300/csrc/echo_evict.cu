@@ -37,7 +37,8 @@ constexpr uint32_t kNone = 0xFFFFFFFFu; // no candidate; a NaN mass is one below
 // The keys of one CTA's slots [c0, c1).
 struct Keys {
     const int32_t* s2t;
-    const float* mass;   // the request's
+    const uint32_t* free;  // the request's free bits, null: every slot with a token holds a resident
+    const float* mass;     // the request's
     uint32_t* key;       // shared: of slot c0 + i, i < kECap
     int64_t len, sinks, late;  // late: the first of the recent tokens
     __device__ __forceinline__ uint32_t of(int32_t t, bool* held, bool* bad, bool* nan) const {
@@ -56,10 +57,15 @@ struct Keys {
         }
         return order_key(m);
     }
+    // The token slot s holds as a resident, else -1 (lazy reuse: a free slot's token is a ghost).
+    __device__ __forceinline__ int32_t token(int s) const {
+        const int32_t t = s2t[s];
+        return free && ((free[s >> 5] >> (s & 31)) & 1u) ? -1 : t;
+    }
     __device__ __forceinline__ uint32_t at(int c0, int s) const {
         if (s - c0 < kECap) return key[s - c0];
         bool h, b, n;
-        return of(s2t[s], &h, &b, &n);
+        return of(token(s), &h, &b, &n);
     }
 };
 
@@ -95,8 +101,9 @@ __device__ __forceinline__ void digit_from_below(const uint32_t* h, uint32_t tar
 
 __global__ void __launch_bounds__(kET)
     evict_kernel(const int64_t* __restrict__ tok_off, const int64_t* __restrict__ tok_end, int64_t n_tokens,
-                 const int32_t* __restrict__ slot2tok, int C, const float* __restrict__ mass, int64_t keep,
-                 int64_t sinks, int64_t recent, int32_t* __restrict__ evict_tok, int32_t* __restrict__ evict_slot,
+                 const int32_t* __restrict__ slot2tok, const uint32_t* __restrict__ freebits, int C,
+                 const float* __restrict__ mass, int64_t keep, int64_t sinks, int64_t recent,
+                 int32_t* __restrict__ evict_tok, int32_t* __restrict__ evict_slot,
                  int32_t* __restrict__ evict_cnt, int32_t* status) {
     extern __shared__ uint32_t keys_smem[];
     __shared__ EvictShared sh;
@@ -111,6 +118,7 @@ __global__ void __launch_bounds__(kET)
     const int w0 = min(c1, c0 + warp * per_warp * 32), w1 = min(c1, w0 + per_warp * 32);
     Keys k;
     k.s2t = slot2tok + static_cast<int64_t>(b) * C;
+    k.free = freebits ? freebits + static_cast<int64_t>(b) * (C / 32) : nullptr;
     k.mass = mass + lo;
     k.key = keys_smem;
     k.len = hi - lo;
@@ -128,7 +136,7 @@ __global__ void __launch_bounds__(kET)
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int s = s0 + 32 * j + lane;
-            t[j] = s < w1 ? k.s2t[s] : -1;
+            t[j] = s < w1 ? k.token(s) : -1;
         }
         uint32_t key[kBatch];
 #pragma unroll
@@ -332,15 +340,17 @@ __global__ void __launch_bounds__(kRT)
 }  // namespace
 }  // namespace echo
 
-extern "C" int echo_evict_select(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens,
-                                 const int32_t* slot2tok, int C, const float* mass, int64_t keep, int64_t sinks,
-                                 int64_t recent, int32_t* evict_tok, int32_t* evict_slot, int32_t* evict_cnt,
-                                 int32_t* status, echo_stream_t stream) {
+extern "C" int echo_evict_select_resident(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens,
+                                          const int32_t* slot2tok, const uint32_t* freebits, int C, const float* mass,
+                                          int64_t keep, int64_t sinks, int64_t recent, int32_t* evict_tok,
+                                          int32_t* evict_slot, int32_t* evict_cnt, int32_t* status,
+                                          echo_stream_t stream) {
     using namespace echo;
     if (B <= 0 || C <= 0 || n_tokens < 0 || keep < 0 || sinks < 0 || recent < 0) return ECHO_EINVAL;
     if (B > ECHO_MAX_REQUESTS || C > kMaxSlots) return ECHO_EUNSUPPORTED;
     if (!tok_off || !slot2tok || (n_tokens > 0 && !mass) || !evict_tok || !evict_slot || !evict_cnt || !status)
         return ECHO_EINVAL;
+    if (freebits && C % 32) return ECHO_ECAPACITY;
     // CTAs of a request: while each has kESlots slots and the batch leaves SMs free
     int n = 1;
     while (n < kEMaxCtas && C >= 2 * n * kESlots && 2 * n * B <= sm_count()) n *= 2;
@@ -360,9 +370,17 @@ extern "C" int echo_evict_select(int B, const int64_t* tok_off, const int64_t* t
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    ECHO_CUDA_OK(cudaLaunchKernelEx(&cfg, evict_kernel, tok_off, tok_end, n_tokens, slot2tok, C, mass, keep, sinks, recent,
-                                    evict_tok, evict_slot, evict_cnt, status));
+    ECHO_CUDA_OK(cudaLaunchKernelEx(&cfg, evict_kernel, tok_off, tok_end, n_tokens, slot2tok, freebits, C, mass, keep, sinks,
+                                    recent, evict_tok, evict_slot, evict_cnt, status));
     return ECHO_OK;
+}
+
+extern "C" int echo_evict_select(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens,
+                                 const int32_t* slot2tok, int C, const float* mass, int64_t keep, int64_t sinks,
+                                 int64_t recent, int32_t* evict_tok, int32_t* evict_slot, int32_t* evict_cnt,
+                                 int32_t* status, echo_stream_t stream) {
+    return echo_evict_select_resident(B, tok_off, tok_end, n_tokens, slot2tok, nullptr, C, mass, keep, sinks, recent,
+                                      evict_tok, evict_slot, evict_cnt, status, stream);
 }
 
 extern "C" int echo_cache_release(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens,

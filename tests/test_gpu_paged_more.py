@@ -1,4 +1,4 @@
-"""More of the calls over a paged latent cache: workspaces on other streams."""
+"""More of the calls over a paged latent cache: workspaces on other streams, caches under lazy reuse."""
 import pytest
 import torch
 
@@ -47,3 +47,57 @@ def test_weights_on_another_stream_take_a_workspace_of_that_stream():
         torch.cuda.synchronize()
         assert int(st.item()) == 0 and int(st2.item()) == 0
         assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- caches under lazy reuse
+def _lazy_cache(n=200, C=64, keep=20):
+    """One request of n tokens whose cache of C slots holds `keep` residents and, in every other slot, a ghost."""
+    host = torch.zeros((n, 576), dtype=torch.bfloat16).pin_memory()
+    cache = L.LayerCache(1, n, C, host)
+    off = torch.tensor([0, n], device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    slots = torch.empty((1, C), dtype=torch.int32, device=dev)
+    first = torch.arange(3, 3 + 2 * C, 2, dtype=torch.int32, device=dev)[None]
+    L.cache_step(off, n, first, cache, slots, st, lazy=True)
+    left = torch.full_like(first, -1)
+    left[0, :keep] = first[0, C - 2 * keep::2]
+    L.cache_step(off, n, left, cache, slots, st, lazy=True)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    free = cache.freebits.cpu()
+    held = torch.tensor([not (int(free[s // 32]) >> (s % 32)) & 1 for s in range(C)])
+    assert int(held.sum()) == keep and torch.all(cache.slot2tok >= 0)
+    return cache, off, st, held
+
+
+@pytest.mark.parametrize("keep,sinks,recent", [(40, 0, 0), (20, 0, 0), (7, 0, 0), (0, 60, 80), (3, 10, 10)])
+def test_victims_of_a_lazy_cache_are_residents(keep, sinks, recent):
+    cache, off, st, held = _lazy_cache()
+    mass = torch.rand(200, generator=torch.Generator().manual_seed(keep)).to(dev)
+    s2t = cache.slot2tok.cpu()
+    mass[s2t[~held].long().to(dev)] = float("nan")         # a ghost's mass is not looked at
+    et = torch.full((1, 64), 9, dtype=torch.int32, device=dev)
+    es, ec = torch.full_like(et, 9), torch.full((1,), 9, dtype=torch.int32, device=dev)
+    L.evict_select(off, 200, cache.slot2tok, mass, keep, et, es, ec, st, sinks=sinks, recent=recent, freebits=cache.freebits)
+    t, s = P.victims(torch.where(held, s2t, -1), mass.cpu(), 0, 200, keep, sinks, recent)
+    assert int(st.item()) == 0 and int(ec) == len(t)
+    assert et[0].tolist() == t + [-1] * (64 - len(t)) and es[0].tolist() == s + [-1] * (64 - len(s))
+
+
+@pytest.mark.parametrize("B,C,length", [(2, 5024, 6000), (1, 100000, 120000)])
+def test_victims_with_free_bits_of_longer_caches(B, C, length):
+    g = torch.Generator().manual_seed(C)
+    off = torch.arange(B + 1) * length
+    s2t = torch.stack([torch.randperm(length, generator=g)[:C] for _ in range(B)]).to(torch.int32)
+    free = torch.rand((B, C), generator=g) < 0.3
+    bits = (free.view(B, C // 32, 32).long() << torch.arange(32)).sum(2)
+    bits = torch.where(bits >= 2 ** 31, bits - 2 ** 32, bits).to(torch.int32).flatten()
+    mass = (torch.rand(B * length, generator=g) * 50).floor()
+    et = torch.empty((B, C), dtype=torch.int32, device=dev)
+    es, ec, st = torch.empty_like(et), torch.empty(B, dtype=torch.int32, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    L.evict_select(off.to(dev), B * length, s2t.to(dev), mass.to(dev), C // 3, et, es, ec, st, sinks=4, recent=9,
+                   freebits=bits.to(dev))
+    assert int(st.item()) == 0
+    for b in range(B):
+        t, s = P.victims(torch.where(free[b], -1, s2t[b]), mass, int(off[b]), length, C // 3, 4, 9)
+        assert int(ec[b]) == len(t) and es[b].tolist() == s + [-1] * (C - len(s)) and et[b].tolist() == t + [-1] * (C - len(t))

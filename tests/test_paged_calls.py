@@ -1,6 +1,7 @@
-"""The wrappers of the paged calls on the CPU: what they hand to the library, with the library and the
-device replaced by recorders."""
+"""The paged calls on the CPU: what their wrappers hand to the library, with the library and the device
+replaced by recorders, and refusals before any CUDA call."""
 import contextlib
+import ctypes
 
 import pytest
 import torch
@@ -81,3 +82,25 @@ def test_a_stream_handle_needs_a_workspace(host):
     with pytest.raises(ValueError):
         _weigh(stream=7)
     _weigh(stream=7, ws=torch.zeros(4096, dtype=torch.uint8))
+
+
+def test_victims_of_residents_check_their_arguments():
+    from sparse_attention_kv_echo_gb300 import build
+    build.build()
+    lib, d = L.load(), ctypes.c_void_p(0x1000)
+
+    def evict(B=1, off=d, n=10, s2t=d, fb=d, C=64, m=d, keep=1, sinks=0, recent=0, et=d, es=d, ec=d, st=d):
+        return lib.echo_evict_select_resident(B, off, None, n, s2t, fb, C, m, keep, sinks, recent, et, es, ec, st, None)
+    for bad in (dict(B=0), dict(off=None), dict(n=-1), dict(s2t=None), dict(C=0), dict(m=None), dict(keep=-1),
+                dict(sinks=-1), dict(recent=-1), dict(et=None), dict(es=None), dict(ec=None), dict(st=None)):
+        assert evict(**bad) == L.ECHO_EINVAL, bad
+    assert evict(B=L.MAX_REQUESTS + 1) == L.ECHO_EUNSUPPORTED and evict(C=(1 << 19) + 32) == L.ECHO_EUNSUPPORTED
+    assert evict(C=48) == L.ECHO_ECAPACITY
+
+
+@pytest.mark.parametrize("words", [1, 3])
+def test_victims_refuse_free_bits_of_another_size(host, words):
+    i = torch.zeros((1, 64), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        L.evict_select(torch.tensor([0, 10]), 10, i, torch.zeros(10), 1, i, i, i[0, :1], i[0, :1],
+                       freebits=torch.zeros(words, dtype=torch.int32))
