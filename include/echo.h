@@ -629,8 +629,9 @@ int echo_evict_select(int B, const int64_t* tok_off, const int64_t* tok_end, int
  * table entries become -1, its slot's free bit is set and, with mass (may be
  * NULL), mass[tok_off[b] + token] = 0.  Its bytes stay; nothing is written back
  * (the host pool holds every row).  Entries that are not resident change
- * nothing (a token listed twice is released once); entries at or past the request's end
- * set ECHO_ST_BADDATA.  Enqueue between steps, on the step's stream, as
+ * nothing (a token listed twice is released once; under lazy reuse a token whose
+ * slot is free is not resident and keeps its entries); entries at or past the request's end,
+ * and tokens whose two table entries disagree (they stay as they are), set ECHO_ST_BADDATA.  Enqueue between steps, on the step's stream, as
  * echo_append_tokens, whose new token then finds a free slot.
  * Errors: ECHO_EINVAL, ECHO_EUNSUPPORTED, cache errors as echo_cache_step.
  */

@@ -326,15 +326,25 @@ __global__ void __launch_bounds__(kRT)
         set_status(status, ECHO_ST_BADDATA);
         return;
     }
-    const int32_t slot = atomicExch(&tok2slot[lo + t], -1);  // a token listed twice is released by one of its entries
+    // The entry is claimed after every check, so that bad tables stay as they are.  Of the entries that list a
+    // token one claims it; another may find slot2tok emptied already: then so is tok2slot, which went first.
+    const int64_t row = lo + t;
+    const int32_t slot = *static_cast<volatile int32_t*>(&tok2slot[row]);
     if (slot < 0) return;
-    if (slot >= C || slot2tok[static_cast<int64_t>(b) * C + slot] != t) {
-        set_status(status, ECHO_ST_BADDATA);
+    int32_t* const owner = slot2tok + static_cast<int64_t>(b) * C + slot;
+    if (slot >= C || *static_cast<volatile int32_t*>(owner) != t) {
+        __threadfence();
+        if (*static_cast<volatile int32_t*>(&tok2slot[row]) == slot) set_status(status, ECHO_ST_BADDATA);
         return;
     }
-    slot2tok[static_cast<int64_t>(b) * C + slot] = -1;
-    atomicOr(&freebits[static_cast<int64_t>(b) * (C / 32) + (slot >> 5)], 1u << (slot & 31));
-    if (mass) mass[lo + t] = 0.f;
+    uint32_t* const word = freebits + static_cast<int64_t>(b) * (C / 32) + (slot >> 5);
+    const uint32_t bit = 1u << (slot & 31);
+    if (*static_cast<volatile uint32_t*>(word) & bit) return;  // lazy reuse: freed before, its slot keeps it
+    if (atomicCAS(&tok2slot[row], slot, -1) != slot) return;
+    __threadfence();
+    *static_cast<volatile int32_t*>(owner) = -1;
+    atomicOr(word, bit);
+    if (mass) mass[row] = 0.f;
 }
 
 }  // namespace

@@ -101,3 +101,58 @@ def test_victims_with_free_bits_of_longer_caches(B, C, length):
     for b in range(B):
         t, s = P.victims(torch.where(free[b], -1, s2t[b]), mass, int(off[b]), length, C // 3, 4, 9)
         assert int(ec[b]) == len(t) and es[b].tolist() == s + [-1] * (C - len(s)) and et[b].tolist() == t + [-1] * (C - len(t))
+
+
+def test_release_leaves_freed_tokens_of_a_lazy_cache():
+    cache, off, st, held = _lazy_cache()
+    t2s, s2t, free = cache.tok2slot.cpu(), cache.slot2tok.cpu(), cache.freebits.cpu()
+    mass = torch.arange(1.0, 201.0, device=dev)
+    L.cache_release(off, 200, cache.slot2tok.clone()[None], cache, st, mass=mass)      # every token of the cache
+    assert int(st.item()) == 0
+    gone = s2t[held].long()
+    t2s[gone], s2t[held] = -1, -1
+    assert torch.equal(cache.tok2slot.cpu(), t2s) and torch.equal(cache.slot2tok.cpu(), s2t)
+    assert torch.all(cache.freebits == -1)
+    want = torch.arange(1.0, 201.0)
+    want[gone] = 0.0
+    assert torch.equal(mass.cpu(), want)
+
+
+def test_release_reports_tables_that_disagree_and_leaves_them():
+    host = torch.zeros((40, 576), dtype=torch.bfloat16).pin_memory()
+    cache = L.LayerCache(1, 40, 32, host)
+    off = torch.tensor([0, 40], device=dev)
+    mass = torch.ones(40, device=dev)
+    cache.freebits[0] = 0
+    cache.tok2slot[3], cache.slot2tok[7] = 7, 4             # slot 7 says another token
+    cache.tok2slot[5] = 32                                  # no such slot
+    cache.tok2slot[6], cache.slot2tok[8] = 8, 6
+    before = cache.tok2slot.cpu()
+    for bad in 3, 5:
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
+        L.cache_release(off, 40, torch.tensor([[bad, 6 if bad == 5 else -1]], dtype=torch.int32, device=dev), cache, st, mass=mass)
+        assert int(st.item()) == L.ST_BADDATA
+    before[6] = -1
+    assert torch.equal(cache.tok2slot.cpu(), before)
+    assert int(cache.slot2tok[7]) == 4 and int(cache.slot2tok[8]) == -1 and int(cache.freebits[0]) == 1 << 8
+    assert float(mass.sum()) == 39.0 and float(mass[6]) == 0.0
+
+
+def test_a_token_listed_many_times_is_released_once_and_is_no_bad_data():
+    B, n, C = 3, 500, 64
+    host = torch.zeros((B * n, 576), dtype=torch.bfloat16).pin_memory()
+    off = torch.arange(B + 1, device=dev) * n
+    g = torch.Generator().manual_seed(2)
+    for _ in range(8):
+        cache = L.LayerCache(B, B * n, C, host)
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
+        sel = torch.stack([torch.randperm(n, generator=g)[:C].sort().values for _ in range(B)]).to(torch.int32)
+        slots = torch.empty((B, C), dtype=torch.int32, device=dev)
+        L.cache_step(off, B * n, sel.to(dev), cache, slots, st)
+        tok = torch.stack([r[:20].repeat(60)[torch.randperm(1200, generator=g)] for r in sel])
+        L.cache_release(off, B * n, tok.to(dev), cache, st)
+        assert int(st.item()) == 0
+        s2t = cache.slot2tok.cpu().view(B, C)
+        for b in range(B):
+            assert sorted(s2t[b][s2t[b] >= 0].tolist()) == sel[b, 20:].tolist()
+        assert int((cache.tok2slot >= 0).sum()) == B * (C - 20)
