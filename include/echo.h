@@ -695,7 +695,8 @@ int echo_pool_slots(int B, const int32_t* sel, int k, const int32_t* slot_pool, 
  *   host pool row pos = kv_new[b] (row_bytes, through cache->host_kv);
  *   the request's lowest free slot s, if any, takes the token: freebits bit
  *   cleared, tok2slot[pos] = s, slot2tok[b*C+s] = pos - tok_off[b], device
- *   row b*C+s = kv_new[b]; with no free slot the token is host-only;
+ *   row b*C+s = kv_new[b]; with no free slot the token is host-only (lazy reuse:
+ *   the token that slot s still held leaves the tables);
  *   tok_end[b] = pos + 1.
  * A non-finite key component sets ECHO_ST_NAN and leaves that request as it
  * was.  Args: tok_off [B+1] / tok_end [B] int64 device (tok_end updated),

@@ -82,8 +82,11 @@ __global__ void __launch_bounds__(kAT)
     const int slot = (s_slot < C) ? s_slot : -1;
     if (tid == 0 && slot >= 0) {
         fb[slot >> 5] &= ~(1u << (slot & 31));
+        int32_t* const owner = slot2tok + static_cast<int64_t>(b) * C + slot;
+        const int32_t ghost = *owner;  // lazy reuse: the token the free slot still holds leaves the tables
+        if (ghost >= 0 && ghost < pos - lo) tok2slot[lo + ghost] = -1;
         tok2slot[pos] = slot;
-        slot2tok[static_cast<int64_t>(b) * C + slot] = static_cast<int32_t>(pos - lo);
+        *owner = static_cast<int32_t>(pos - lo);
         tok_end[b] = pos + 1;
     } else if (tid == 0) {
         tok_end[b] = pos + 1;

@@ -156,3 +156,33 @@ def test_a_token_listed_many_times_is_released_once_and_is_no_bad_data():
         for b in range(B):
             assert sorted(s2t[b][s2t[b] >= 0].tolist()) == sel[b, 20:].tolist()
         assert int((cache.tok2slot >= 0).sum()) == B * (C - 20)
+
+
+def test_append_to_a_lazy_cache_drops_the_token_its_slot_held():
+    n, C = 160, 64
+    host = torch.randn((n, 576), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).pin_memory()
+    cache = L.LayerCache(1, n, C, host)
+    off, end = torch.tensor([0, n], device=dev), torch.tensor([150], device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    slots = torch.empty((1, C), dtype=torch.int32, device=dev)
+    first = torch.arange(0, C, dtype=torch.int32, device=dev)[None]
+    L.cache_step(off, n, first, cache, slots, st, lazy=True, tok_end=end)
+    left = torch.full_like(first, -1)
+    left[0, :24] = first[0, 40:]
+    L.cache_step(off, n, left, cache, slots, st, lazy=True, tok_end=end)
+    k8, ks = torch.zeros((n, 128), dtype=torch.uint8, device=dev), torch.zeros(n, device=dev)
+    for i in range(5):
+        kv = torch.randn((1, 576), device=dev).to(torch.bfloat16)
+        L.append_tokens(off, end, n, torch.randn((1, 128), device=dev), kv, k8, ks, cache, st)
+        t2s, s2t = cache.tok2slot.cpu(), cache.slot2tok.cpu()
+        assert int(t2s[150 + i]) == i and int(t2s[i]) == -1
+        held = torch.nonzero(s2t >= 0)[:, 0]
+        assert torch.equal(t2s[s2t[held].long()].long(), held)                        # the tables are inverse
+        assert torch.equal(cache.dev_kv[held.to(dev)].cpu(), host[s2t[held].long()])    # and say what the rows are
+    # the dropped tokens, selected again, are recalled: their slots hold others
+    sel = torch.full_like(first, -1)
+    sel[0, :10] = torch.cat([torch.arange(5), torch.arange(150, 155)]).to(torch.int32)
+    L.cache_step(off, n, sel, cache, slots, st, lazy=True, tok_end=end)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.equal(cache.dev_kv[slots[0, :10].long()].cpu(), host[sel[0, :10].long().cpu()])
