@@ -282,9 +282,12 @@ int echo_topk_select(int B, const int64_t* tok_off, const int64_t* tok_end, int6
  * Steps 0-3 are launched as a programmatic dependent of the
  * kernel before them on `stream`: while that kernel still runs (if it lets
  * dependents start early, as echo_topk_select and echo_index_scores do) they
- * may read slot2tok and freebits, which none of this library's kernels but
- * this step writes; sel and above are read only after that kernel has
- * completed.
+ * may read tok_off, tok_end, slot2tok and freebits.  Of this library's kernels only
+ * this step (the cached top-k enters selected early tokens for its resolved form, which
+ * keeps their slots either way), echo_append_tokens and echo_cache_release write any of
+ * those, and the latter two let no dependent start before their blocks have ended, with their writes
+ * performed: a step right behind them sees the tables as they left them.  sel and above are
+ * read only after the kernel before has completed.
  */
 int echo_cache_step(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const int32_t* sel,
                     int m,

@@ -91,6 +91,8 @@ __global__ void __launch_bounds__(kAT)
     } else if (tid == 0) {
         tok_end[b] = pos + 1;
     }
+    // a cache step right behind may read these once this grid's blocks have ended, before its wait
+    if (tid == 0) __threadfence();
     // ---- the row: host pool, and the slot's device row
     const int chunks = static_cast<int>(row_bytes / 16);
     const int4* src = reinterpret_cast<const int4*>(kv_new + static_cast<int64_t>(b) * row_bytes);

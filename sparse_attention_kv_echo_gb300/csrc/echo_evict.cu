@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kRT)
     *static_cast<volatile int32_t*>(owner) = -1;
     atomicOr(word, bit);
     if (mass) mass[row] = 0.f;
+    __threadfence();  // a cache step right behind may read the tables once this grid's blocks have ended, before its wait
 }
 
 }  // namespace

@@ -1,4 +1,5 @@
 """More of the calls over a paged latent cache: workspaces on other streams, caches under lazy reuse."""
+import numpy as np
 import pytest
 import torch
 
@@ -186,3 +187,43 @@ def test_append_to_a_lazy_cache_drops_the_token_its_slot_held():
     torch.cuda.synchronize()
     assert int(st.item()) == 0
     assert torch.equal(cache.dev_kv[slots[0, :10].long()].cpu(), host[sel[0, :10].long().cpu()])
+
+
+def test_a_cache_step_right_behind_a_release_or_an_append_sees_its_tables(orc):
+    # nothing between the calls: the step's look at the tables before its wait comes after their writes
+    B, n, C, k = 4, 900, 512, 200
+    host = torch.zeros((B * n, 576), dtype=torch.bfloat16).pin_memory()
+    off = torch.arange(B + 1, device=dev) * n
+    cache = L.LayerCache(B, B * n, C, host)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    slots = torch.empty((B, k), dtype=torch.int32, device=dev)
+    k8, ks = torch.zeros((B * n, 128), dtype=torch.uint8, device=dev), torch.zeros(B * n, device=dev)
+    k_new, kv = torch.ones((B, 128), device=dev), torch.zeros((B, 576), dtype=torch.bfloat16, device=dev)
+    end = off[:-1] + 800
+    g = torch.Generator().manual_seed(6)
+    t2s = [np.full(n, -1, np.int32) for _ in range(B)]
+    s2t = [np.full(C, -1, np.int32) for _ in range(B)]
+    pick = lambda m: torch.stack([torch.randperm(800, generator=g)[:m].sort().values for _ in range(B)]).to(torch.int32)
+    for step in range(60):
+        sel, tok = pick(k), pick(400)
+        sel_d, tok_d = sel.to(dev), tok.to(dev)
+        torch.cuda.synchronize()
+        if step % 2:
+            L.cache_release(off, B * n, tok_d, cache, st)
+        else:
+            L.append_tokens(off, end, B * n, k_new, kv, k8, ks, cache, st)
+        L.cache_step(off, B * n, sel_d, cache, slots, st)
+        for b in range(B):
+            if step % 2:
+                for t in tok[b].tolist():
+                    if t2s[b][t] >= 0:
+                        s2t[b][t2s[b][t]] = -1
+                        t2s[b][t] = -1
+            else:
+                s = int(np.argmax(s2t[b] < 0))
+                t2s[b][800 + step // 2], s2t[b][s] = s, 800 + step // 2
+            want = orc.cache_step(sel[b].numpy(), t2s[b], s2t[b])[0]
+            assert np.array_equal(slots[b].cpu().numpy(), want), step
+        assert np.array_equal(cache.slot2tok.cpu().numpy(), np.concatenate(s2t))
+        assert np.array_equal(cache.tok2slot.cpu().numpy(), np.concatenate(t2s))
+    assert int(st.item()) == 0
