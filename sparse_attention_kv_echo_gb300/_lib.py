@@ -28,7 +28,7 @@ CAND_CAP = 16384             # candidate-list entries per request top-k keeps in
 EARLY_FETCH_BLOCKS = 24      # CTAs of the early-fetch and late-recall kernels
 
 EXPORTS = ("echo_above_words", "echo_append_tokens", "echo_cache_release", "echo_cache_step", "echo_cache_step_resolved",
-           "echo_debug_stall_epilogue", "echo_device_sm_count",
+           "echo_debug_stall_epilogue", "echo_debug_wait_limit", "echo_device_sm_count",
            "echo_early_fetch", "echo_evict_select", "echo_evict_select_resident", "echo_host_device_alias", "echo_index_scores", "echo_index_scores_cands", "echo_mla_chunk",
            "echo_mla_chunk_workspace_size", "echo_mla_decode", "echo_mla_mass",
            "echo_mla_mass_workspace_size", "echo_pool_above", "echo_pool_select",
@@ -158,6 +158,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         L.echo_host_device_alias.argtypes = [_vp, ctypes.POINTER(_vp)]
         L.echo_debug_stall_epilogue.restype = i32
         L.echo_debug_stall_epilogue.argtypes = [i64]
+        L.echo_debug_wait_limit.restype = i32
+        L.echo_debug_wait_limit.argtypes = [i64]
         L.echo_device_sm_count.restype = i32
         L.echo_device_sm_count.argtypes = []
         _lib = L
@@ -219,6 +221,12 @@ def debug_stall_epilogue(limit_ns: int) -> None:
     """echo_debug_stall_epilogue: >= 0, every score call first waits on a barrier nothing arrives
     on and gives up after limit_ns (tests of the timeout path); < 0 turns that off."""
     _check("echo_debug_stall_epilogue", load().echo_debug_stall_epilogue(int(limit_ns)))
+
+
+def debug_wait_limit(limit_ns: int) -> None:
+    """echo_debug_wait_limit: the limit of the waits of later mla_chunk and mla_mass calls, from the last
+    progress (< 0: the default, 2 s)."""
+    _check("echo_debug_wait_limit", load().echo_debug_wait_limit(int(limit_ns)))
 
 
 def sm_count() -> int:

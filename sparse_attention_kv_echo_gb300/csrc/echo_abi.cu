@@ -3,9 +3,15 @@
 // and small queries.
 #include <string.h>
 
+#include <atomic>
+
 #include "echo_internal.h"
 
 namespace echo {
+
+static std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 
 int sm_count() {
     int dev = 0, n = 0;
@@ -102,5 +108,11 @@ int echo_host_device_alias(const void* host_ptr, const void** device_ptr) {
 }
 
 int echo_device_sm_count(void) { return echo::sm_count(); }
+
+int echo_debug_wait_limit(int64_t limit_ns) {
+    echo::g_wait_limit_ns.store(limit_ns < 0 ? echo::kWaitLimitNs : static_cast<uint64_t>(limit_ns),
+                                std::memory_order_relaxed);
+    return ECHO_OK;
+}
 
 }  // extern "C"

@@ -379,7 +379,7 @@ struct Ctl {
     uint64_t s_free[kSBufs];                             // S of a tile has been read in both CTAs
     uint64_t drain[2];
     uint32_t tmem;
-    int abort;
+    Watch watch;
     int first;                                           // the share's first group
     float mx[2][2][64];                                  // tile maxima, or a piece's sums, by (parity, token half, row)
     // few groups: the plan, made by every CTA for itself
@@ -463,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t c = cluster_rank();
     const int ci = blockIdx.x >> 1;
-    volatile int* const abort = &ctl->abort;
+    Watch* const watch = &ctl->watch;
 
     if (tid == 0) {
         mbar_init(smem_addr(&ctl->q_full), 1);
@@ -484,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&ctl->fin_free), kSoftmax / 32);
         mbar_init(smem_addr(&ctl->o_free), 2 * kSoftmax / 32);
         for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&ctl->drain[i]), 1);
-        ctl->abort = 0;
+        watch_init(watch, a.wait_ns);
         fence_barrier_init();
         prefetch_tmap(&qmap);
     }
@@ -544,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.f;
             for (int it = p.lo; it < p.hi; ++it, ++t) {
                 const uint32_t st = t & 1u;
-                ok = ok && mbar_wait(smem_addr(&ctl->s_full[t & (kSBufs - 1)]), (t / kSBufs) & 1u, abort);
+                ok = ok && mbar_wait_watch(smem_addr(&ctl->s_full[t & (kSBufs - 1)]), (t / kSBufs) & 1u, watch);
                 tc_fence_after();
                 __syncwarp();
                 float s[32];
@@ -595,14 +595,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 l = l * corr + ((part[0] + part[1]) + (part[2] + part[3]));
                 // this P buffer is free once PV of two tiles before is done
-                if (t >= 2) ok = mbar_wait(smem_addr(&ctl->pv_done[st]), ((t >> 1) & 1u) ^ 1u, abort);
+                if (t >= 2) ok = mbar_wait_watch(smem_addr(&ctl->pv_done[st]), ((t >> 1) & 1u) ^ 1u, watch);
                 uint8_t* const prow = gP + st * kPBytes + row * 128;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     *reinterpret_cast<uint4*>(prow + (((4 * half + j) ^ (row & 7)) << 4)) =
                         make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
                 if (it > p.lo && moves) {  // O holds earlier tiles: bring it to the new reference
-                    ok = ok && mbar_wait(smem_addr(&ctl->pv_done[st ^ 1u]), ((t - 1) >> 1) & 1u, abort);
+                    ok = ok && mbar_wait_watch(smem_addr(&ctl->pv_done[st ^ 1u]), ((t - 1) >> 1) & 1u, watch);
                     tc_fence_after();
                     __syncwarp();
 #pragma unroll 1
@@ -624,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float L = 0.f;
             if (p.hi > p.lo) {
                 ctl->mx[t & 1u][half][row] = l;
-                if (pieces >= 1) ok = ok && mbar_wait(smem_addr(&ctl->fin_free), (pieces - 1) & 1u, abort);
+                if (pieces >= 1) ok = ok && mbar_wait_watch(smem_addr(&ctl->fin_free), (pieces - 1) & 1u, watch);
                 ++pieces;
                 ok = !softmax_sync_or(!ok);
                 if (!ok) break;
@@ -648,7 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 (void)softmax_sync_or(false);  // mx is read before the next tile's maxima
             }
         }
-        if (!ok) *abort = 1;
+        if (!ok) give_up(watch);
     } else if (warp < 8) {
         // ---- K of this CTA's 32 tokens.  A warp has 8 tokens and copies
         // four 128-byte row pieces per instruction (8 lanes each): with 64-byte pieces of 8 rows the
@@ -678,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     n[i] = rk < 0 ? 0u : 16u;
                     dst[i] = sK + st * kKBytes + static_cast<uint32_t>(8 * w + r) * 128u + (static_cast<uint32_t>(x ^ r) << 4);
                 }
-                if (t >= 2) ok = mbar_wait(smem_addr(&ctl->k_free[st]), ph ^ 1u, abort);
+                if (t >= 2) ok = mbar_wait_watch(smem_addr(&ctl->k_free[st]), ph ^ 1u, watch);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
 #pragma unroll
@@ -692,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_addr(&ctl->k_full[st]));
             }
         }
-        if (!ok) *abort = 1;
+        if (!ok) give_up(watch);
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < 12) {
         // ---- V: this CTA's 256 dims of the tile's 64 tokens, 16 to a warp, copied like K
@@ -717,7 +717,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     dst[i] = sV + st * kVBytes + static_cast<uint32_t>(16 * w + r) * 128u +
                              (static_cast<uint32_t>(x ^ (r & 7)) << 4);
                 }
-                if (t >= 2) ok = mbar_wait(smem_addr(&ctl->pv_done[st]), ph ^ 1u, abort);
+                if (t >= 2) ok = mbar_wait_watch(smem_addr(&ctl->pv_done[st]), ph ^ 1u, watch);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
 #pragma unroll
@@ -727,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 cp_async_arrive_noinc(smem_addr(&ctl->v_full[st]));
             }
         }
-        if (!ok) *abort = 1;
+        if (!ok) give_up(watch);
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 12 || warp == 13) {
         // ---- the MMAs of both CTAs: Q K by one thread of CTA 0, P V by another.  A look at a barrier and a
@@ -738,15 +738,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             while (ok && walk.next(&p)) {
                 if (p.hi == p.lo) continue;
-                if (qk) ok = mbar_wait_cluster(smem_addr(&ctl->q_ready), groups & 1u, abort);
-                else if (groups > 0) ok = mbar_wait_cluster(smem_addr(&ctl->o_free), (groups - 1) & 1u, abort);
+                if (qk) ok = mbar_wait_cluster(smem_addr(&ctl->q_ready), groups & 1u, watch);
+                else if (groups > 0) ok = mbar_wait_cluster(smem_addr(&ctl->o_free), (groups - 1) & 1u, watch);
                 ++groups;
                 for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
                     const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
                     if (qk) {
                         if (t >= kSBufs)
-                            ok = mbar_wait_cluster(smem_addr(&ctl->s_free[t & (kSBufs - 1)]), ((t / kSBufs) & 1u) ^ 1u, abort);
-                        ok = ok && mbar_wait_cluster(smem_addr(&ctl->k_ready[st]), ph, abort);
+                            ok = mbar_wait_cluster(smem_addr(&ctl->s_free[t & (kSBufs - 1)]), ((t / kSBufs) & 1u) ^ 1u, watch);
+                        ok = ok && mbar_wait_cluster(smem_addr(&ctl->k_ready[st]), ph, watch);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t d = tmem + kSCol + (t & (kSBufs - 1)) * 32u;
@@ -755,7 +755,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         mma2_commit_both(smem_addr(&ctl->k_free[st]));
                         mma2_commit_both(smem_addr(&ctl->s_full[t & (kSBufs - 1)]));
                     } else {  // O += P V
-                        ok = mbar_wait_cluster(smem_addr(&ctl->pv_ready[st]), ph, abort);
+                        ok = mbar_wait_cluster(smem_addr(&ctl->pv_ready[st]), ph, watch);
                         if (!ok) break;
                         tc_fence_after();
                         if (st == 0) issue_pv<0>(tmem, sP, sV, it > p.lo);
@@ -765,9 +765,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) {  // the MMAs in flight end before the CTAs' memory goes
-                *abort = 1;
+                give_up(watch);
                 mma2_commit_both(smem_addr(&ctl->drain[qk ? 0 : 1]));
-                (void)mbar_wait(smem_addr(&ctl->drain[qk ? 0 : 1]), 0, nullptr);
+                (void)mbar_wait_limit(smem_addr(&ctl->drain[qk ? 0 : 1]), 0, nullptr, kWaitNs);
             }
         }
         __syncwarp();
@@ -779,7 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (p.hi == p.lo) continue;
             // Q of the group, once the group before has no QK left.  Its (row, head) pairs are consecutive in q;
             // pairs past the group's own are another group's, or zeros, and their results are dropped
-            if (t >= 1) ok = mbar_wait(smem_addr(&ctl->k_free[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, abort);
+            if (t >= 1) ok = mbar_wait_watch(smem_addr(&ctl->k_free[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, watch);
             if (!ok) break;
             if (elect_one()) {
                 const uint32_t bar = smem_addr(&ctl->q_full);
@@ -788,16 +788,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tma_load_2d(sQ + i * kQAtom, &qmap, bar, i * 128, p.g.row0 * a.heads + static_cast<int>(c) * 64);
             }
             __syncwarp();
-            ok = mbar_wait(smem_addr(&ctl->q_full), groups & 1u, nullptr);  // always: the load lands before the CTA ends
+            // always: the load lands before the CTA ends
+            ok = mbar_wait_limit(smem_addr(&ctl->q_full), groups & 1u, nullptr, kWaitNs);
             ++groups;
             if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->q_ready), 0);
             for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
-                ok = mbar_wait(smem_addr(&ctl->k_full[t & 1u]), (t >> 1) & 1u, abort);
+                ok = mbar_wait_watch(smem_addr(&ctl->k_full[t & 1u]), (t >> 1) & 1u, watch);
                 fence_proxy_async_smem();
                 if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->k_ready[t & 1u]), 0);
             }
         }
-        if (!ok && lane == 0) *abort = 1;
+        if (!ok && lane == 0) give_up(watch);
     } else if (warp >= 16) {
         // ---- the results.  Read 16 rows x 32 columns at a time, four lanes to a row, so that stores are whole
         // sectors: a lane a row, straight to memory, took 5 us a group, through shared memory by the softmax warps 3
@@ -812,14 +813,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int64_t at = static_cast<int64_t>(p.g.row0) * a.heads + static_cast<int>(c) * 64 + r_cta;
             uint8_t* const dst = whole ? reinterpret_cast<uint8_t*>(out + at * kLatDv + half * 256) : nullptr;
             if (p.hi == p.lo) {  // nothing was seen
+                if (warp == 16 && lane == 0) watch_beat(watch);
                 for (int i = lane; i < 32 * 32; i += 32)
                     if ((i >> 5) < live) reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i >> 5) * (kLatDv * 2))[i & 31] = make_uint4(0, 0, 0, 0);
                 continue;
             }
             t += static_cast<uint32_t>(p.hi - p.lo);
             // (P of the last tile was written after PV of the one two before)
-            ok = mbar_wait(smem_addr(&ctl->fin_ready), pieces & 1u, abort) &&
-                 mbar_wait(smem_addr(&ctl->pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, abort);
+            ok = mbar_wait_watch(smem_addr(&ctl->fin_ready), pieces & 1u, watch) &&
+                 mbar_wait_watch(smem_addr(&ctl->pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, watch);
             ++pieces;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -864,7 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->o_free), 0);
         }
-        if (!ok) *abort = 1;
+        if (!ok) give_up(watch);
     } else {
         // ---- V has landed here
         if (c == 0 && ci > 0 && lane == 0) {  // first, for the join: whether this share starts the second part of a group
@@ -882,16 +884,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && walk.next(&p)) {
             for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
-                ok = mbar_wait(smem_addr(&ctl->v_full[t & 1u]), (t >> 1) & 1u, abort);
+                ok = mbar_wait_watch(smem_addr(&ctl->v_full[t & 1u]), (t >> 1) & 1u, watch);
                 fence_proxy_async_smem();
-                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->pv_ready[t & 1u]), 0);
+                if (ok && lane == 0) {
+                    mbar_arrive_remote(smem_addr(&ctl->pv_ready[t & 1u]), 0);
+                    watch_beat(watch);  // (the V stages go round with the tiles)
+                }
             }
         }
-        if (!ok && lane == 0) *abort = 1;
+        if (!ok && lane == 0) give_up(watch);
     }
     __syncthreads();
     pdl_launch_dependents();
-    if (tid == 0 && *abort) set_status(a.status, ECHO_ST_TIMEOUT);
+    if (tid == 0 && gave_up(watch)) set_status(a.status, ECHO_ST_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // no CTA leaves while the other may still signal it

@@ -10,11 +10,12 @@
 #include <stdint.h>
 
 #include "echo.h"
+#include "echo_internal.h"
 
 namespace echo {
 
 // Any wait inside a kernel gives up after this long and reports ECHO_ST_TIMEOUT.
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = kWaitLimitNs;
 
 __device__ __forceinline__ uint64_t global_ns() {
     uint64_t t;
@@ -128,6 +129,50 @@ __device__ __forceinline__ bool mbar_wait_limit(uint32_t bar, uint32_t parity, c
 // The same with the library's limit, kWaitNs.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
     return mbar_wait_limit(bar, parity, abort, kWaitNs);
+}
+
+// What the waits of a CTA watch whose work may go on for longer than any fixed limit: abort
+// ends them, and the limit runs from the last move of beat, which the warps that do the work
+// move (a warp that stores the result of a long piece, or loads what follows it, waits for
+// as long as the piece takes).  In shared memory.
+struct Watch {
+    uint64_t limit_ns;
+    int abort;
+    uint32_t beat;
+};
+
+__device__ __forceinline__ void watch_init(Watch* w, uint64_t limit_ns) {
+    w->limit_ns = limit_ns;
+    w->abort = 0;
+    w->beat = 0;
+}
+
+__device__ __forceinline__ void give_up(Watch* w) { static_cast<volatile Watch*>(w)->abort = 1; }
+__device__ __forceinline__ bool gave_up(const Watch* w) { return static_cast<const volatile Watch*>(w)->abort != 0; }
+__device__ __forceinline__ void watch_beat(Watch* w) { atomicAdd(&w->beat, 1u); }
+
+// Whether a wait that began or last saw a beat at *t0, with *seen beats, goes on.
+__device__ __forceinline__ bool watch_goes_on(const Watch* w, uint32_t* seen, uint64_t* t0) {
+    const volatile Watch* const v = w;
+    if (v->abort) return false;
+    const uint32_t beat = v->beat;
+    const uint64_t now = global_ns();
+    if (beat != *seen) {
+        *seen = beat;
+        *t0 = now;
+    }
+    return now - *t0 <= v->limit_ns;
+}
+
+// mbar_wait under a watch.
+__device__ __forceinline__ bool mbar_wait_watch(uint32_t bar, uint32_t parity, const Watch* w) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint32_t seen = static_cast<const volatile Watch*>(w)->beat;
+    uint64_t t0 = global_ns();
+    do {
+        if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    } while (watch_goes_on(w, &seen, &t0));
+    return false;
 }
 
 // ---------------------------------------------------------------- TMA

@@ -15,6 +15,11 @@ inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintp
 
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Limit of every wait inside a kernel.  The paged calls' kernels take theirs as an argument, from
+// wait_limit_ns(), which echo_debug_wait_limit changes.
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+uint64_t wait_limit_ns();
+
 // SM count of the current device.
 int sm_count();
 

@@ -207,7 +207,7 @@ struct Ctl {
     uint64_t d_full[2], d_free[2];
     uint64_t drain;
     uint32_t tmem;
-    int abort;
+    Watch watch;
     int first;
     alignas(16) float nl[2][kCols];       // -lse * log2(e) of a block's pairs
 };
@@ -257,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t c = cluster_rank();
     const int ci = blockIdx.x >> 1;
-    volatile int* const abort = &ctl->abort;
+    Watch* const watch = &ctl->watch;
     if (tid == 0) {
         for (int i = 0; i < kKSlots; ++i) {
             mbar_init(smem_addr(&ctl->k_full[i]), kLoad);
@@ -275,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&ctl->d_free[i]), 8);
         }
         mbar_init(smem_addr(&ctl->drain), 1);
-        ctl->abort = 0;
+        watch_init(watch, a.wait_ns);
         fence_barrier_init();
         if (a.n_rows > 0) prefetch_tmap(&qmap);
     }
@@ -334,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const float v = x < n ? ls[x] : -INFINITY;
                     nl[x] = v == -INFINITY ? -INFINITY : -v * 1.4426950408889634f;  // a row that sees nothing adds nothing
                 }
-                ok = ok && mbar_wait(smem_addr(&ctl->d_full[db]), (d >> 1) & 1u, abort);
+                ok = ok && mbar_wait_watch(smem_addr(&ctl->d_full[db]), (d >> 1) & 1u, watch);
                 ok = !bar_or128(1, !ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -382,13 +382,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 sum = z;
             }
             if (!ok) break;
+            if (p.hi == p.lo && tid == 0) watch_beat(watch);
             if (whole) {
                 if (in) mass_out[p.g.off + tok] = decay * old + sum;
             } else {
                 plan.part[static_cast<size_t>(2 * ci + (p.lo > 0 ? 0 : 1)) * kTok + c * 128 + tid] = sum;
             }
         }
-        if (!ok) *abort = 1;
+        if (!ok) give_up(watch);
     } else if (warp < 8 || warp >= 12) {
         // ---- K: 8 lanes per token row, 16 bytes each: a warp copies rows 4w + i + 16j, i < 4 at a time, having
         // looked up the 32 of them (lane i + 4j).  Two sets of four warps take the items in turn, so that one looks
@@ -421,8 +422,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // parity's barriers, each before the next can end
             for (int at = 0; at < kAtoms; ++at) {
                 if (item >= 1)
-                    ok = ok && mbar_wait(smem_addr(&ctl->k_free[(item - 1) & 1][at]), static_cast<uint32_t>((item - 1) >> 1) & 1u,
-                                         abort);
+                    ok = ok && mbar_wait_watch(smem_addr(&ctl->k_free[(item - 1) & 1][at]), static_cast<uint32_t>((item - 1) >> 1) & 1u,
+                                         watch);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const uint32_t dst = sK + static_cast<uint32_t>(at) * kSlot;
@@ -436,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             ++item;
         }
-        if (!ok) *abort = 1;
+        if (!ok) give_up(watch);
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 9) {
         // ---- Q: this CTA's half of a block's pairs
@@ -448,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int cb = p.g.cb0 + b, half = ((block_cols(p.g, a.heads, cb) + 31) & ~31) / 2;
                 const int32_t y = static_cast<int32_t>(p.g.col0 + static_cast<int64_t>(cb) * kCols + c * half);
                 for (int at = 0; at < kAtoms; ++at, q.step(kQSlots), ++filled) {
-                    if (filled >= kQSlots && !mbar_wait(smem_addr(&ctl->q_free[q.slot]), q.phase ^ 1u, abort)) {
+                    if (filled >= kQSlots && !mbar_wait_watch(smem_addr(&ctl->q_free[q.slot]), q.phase ^ 1u, watch)) {
                         ok = false;
                         break;
                     }
@@ -461,13 +462,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (!ok && lane == 0) *abort = 1;
+        if (!ok && lane == 0) give_up(watch);
         // the loads in flight land before the CTA's memory goes
         for (int j = 0; j < kQSlots && !ok; ++j) {
             const int back = j + 1;
             if (filled >= static_cast<uint32_t>(back)) {
                 const uint32_t f = filled - back;
-                (void)mbar_wait(smem_addr(&ctl->q_full[f % kQSlots]), (f / kQSlots) & 1u, nullptr);
+                (void)mbar_wait_limit(smem_addr(&ctl->q_full[f % kQSlots]), (f / kQSlots) & 1u, nullptr, kWaitNs);
             }
         }
     } else if (warp == 8) {
@@ -483,14 +484,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int b = p.lo; ok && b < p.hi; ++b, ++d) {
                     const int n = (block_cols(p.g, a.heads, p.g.cb0 + b) + 31) & ~31;
                     const uint32_t db = d & 1u, idesc = idesc_bf16_f32(256, static_cast<uint32_t>(n));
-                    if (d >= 2 && !mbar_wait_cluster(smem_addr(&ctl->d_free[db]), ((d >> 1) & 1u) ^ 1u, abort)) {
+                    if (d >= 2 && !mbar_wait_cluster(smem_addr(&ctl->d_free[db]), ((d >> 1) & 1u) ^ 1u, watch)) {
                         ok = false;
                         break;
                     }
                     k = k0;
                     for (int at = 0; at < kAtoms; ++at, k.step(kKSlots), q.step(kQSlots)) {
-                        if (b == p.lo) ok = mbar_wait_cluster(smem_addr(&ctl->k_ready[k.slot]), k.phase, abort);
-                        ok = ok && mbar_wait_cluster(smem_addr(&ctl->q_ready[q.slot]), q.phase, abort);
+                        if (b == p.lo) ok = mbar_wait_cluster(smem_addr(&ctl->k_ready[k.slot]), k.phase, watch);
+                        ok = ok && mbar_wait_cluster(smem_addr(&ctl->q_ready[q.slot]), q.phase, watch);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t ad = sw128_kmajor_desc(sK + static_cast<uint32_t>(k.slot) * kSlot);
@@ -506,9 +507,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) {
-                *abort = 1;
+                give_up(watch);
                 mma2_commit_both(smem_addr(&ctl->drain));
-                (void)mbar_wait(smem_addr(&ctl->drain), 0, nullptr);
+                (void)mbar_wait_limit(smem_addr(&ctl->drain), 0, nullptr, kWaitNs);
             }
         }
         __syncwarp();
@@ -519,27 +520,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (ok && walk.next(&p)) {
             if (p.hi == p.lo) continue;
             for (int at = 0; ok && at < kAtoms; ++at, k.step(kKSlots)) {
-                ok = mbar_wait(smem_addr(&ctl->k_full[k.slot]), k.phase, abort);
+                ok = mbar_wait_watch(smem_addr(&ctl->k_full[k.slot]), k.phase, watch);
                 fence_proxy_async_smem();
                 if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->k_ready[k.slot]), 0);
             }
         }
-        if (!ok && lane == 0) *abort = 1;
+        if (!ok && lane == 0) give_up(watch);
     } else {  // warp 11
         // ---- Q has landed here
         Ring q;
         bool ok = true;
         while (ok && walk.next(&p)) {
             for (int i = 0; ok && i < (p.hi - p.lo) * kAtoms; ++i, q.step(kQSlots)) {
-                ok = mbar_wait(smem_addr(&ctl->q_full[q.slot]), q.phase, abort);
-                if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->q_ready[q.slot]), 0);
+                ok = mbar_wait_watch(smem_addr(&ctl->q_full[q.slot]), q.phase, watch);
+                if (ok && lane == 0) {
+                    mbar_arrive_remote(smem_addr(&ctl->q_ready[q.slot]), 0);
+                    watch_beat(watch);  // (the Q slots go round with the MMAs)
+                }
             }
         }
-        if (!ok && lane == 0) *abort = 1;
+        if (!ok && lane == 0) give_up(watch);
     }
     __syncthreads();
     pdl_launch_dependents();
-    if (tid == 0 && *abort) set_status(a.status, ECHO_ST_TIMEOUT);
+    if (tid == 0 && gave_up(watch)) set_status(a.status, ECHO_ST_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();

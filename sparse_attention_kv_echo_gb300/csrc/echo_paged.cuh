@@ -35,6 +35,7 @@ struct ChunkArgs {
     int64_t sinks;
     const uint16_t* q;
     float scale;
+    uint64_t wait_ns;  // limit of the kernels' waits, from the last progress
     int32_t* status;
 };
 
@@ -74,6 +75,7 @@ inline ChunkArgs chunk_args(int B, const int64_t* row_off, int64_t n_rows, int h
     a.sinks = sinks;
     a.q = q;
     a.scale = scale;
+    a.wait_ns = wait_limit_ns();
     a.status = status;
     return a;
 }

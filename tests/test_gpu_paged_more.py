@@ -1,4 +1,5 @@
-"""More of the calls over a paged latent cache: workspaces on other streams, caches under lazy reuse."""
+"""More of the calls over a paged latent cache: workspaces on other streams, caches under lazy reuse, long
+pieces of work."""
 import numpy as np
 import pytest
 import torch
@@ -227,3 +228,70 @@ def test_a_cache_step_right_behind_a_release_or_an_append_sees_its_tables(orc):
         assert np.array_equal(cache.slot2tok.cpu().numpy(), np.concatenate(s2t))
         assert np.array_equal(cache.tok2slot.cpu().numpy(), np.concatenate(t2s))
     assert int(st.item()) == 0
+
+
+# ---------------------------------------------------------------- long pieces of work
+@pytest.fixture
+def short_waits():
+    # a step of the kernels takes 1 to 4 us; the pieces of these tests take 600 us and more
+    L.debug_wait_limit(200_000)
+    yield
+    L.debug_wait_limit(-1)
+
+
+def _shared_pages(n, rows, heads, page, seed):
+    """One request of n tokens, all of whose pages are one: a token's cache row is its offset in the page."""
+    bt = P.Batch([page], [1], heads, page, seed=seed, room=0)
+    g = torch.Generator().manual_seed(seed + 1)
+    bt.lens, bt.rows, bt.n = [n], [rows], rows
+    bt.q = torch.randn((rows, heads, 576), generator=g).to(torch.bfloat16)
+    bt.tok_off, bt.tok_end, bt.row_off = torch.tensor([0, n]), torch.tensor([n]), torch.tensor([0, rows])
+    bt.n_tokens, bt.tab = n, torch.zeros(-(-n // page), dtype=torch.int32)
+    return bt
+
+
+def test_a_piece_of_attention_longer_than_the_wait_limit(short_waits):
+    # 160 rows of 128 heads: every cluster has whole rows, of 60000 tokens (about 750 us) each
+    page, n, rows = 256, 60_000, 160
+    bt = _shared_pages(n, rows, 128, page, 3)
+    row_off, q, tok_off, tok_end, pages = bt.on(dev, L)
+    out = torch.empty((rows, 128, 512), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((rows, 128), device=dev)
+    ws = torch.empty(L.mla_chunk_workspace_size(rows, 128, 1), dtype=torch.uint8, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    L.mla_chunk(row_off, q, tok_off, n, pages, bt.scale, out, lse, ws, st, tok_end=tok_end)
+    assert int(st.item()) == 0
+    kv = bt.kv[:page].double()
+    for i in (0, 77, 159):
+        p = n - rows + i                                 # sees tokens 0 .. p: each cache row so many times
+        times = torch.full((page,), (p + 1) // page, dtype=torch.float64)
+        times[:(p + 1) % page] += 1
+        s = bt.scale * bt.q[i].double() @ kv.T
+        ref = torch.logsumexp(s + times.log(), -1)
+        w = torch.exp(s - ref[:, None]) * times
+        dots = bt.scale * (bt.q[i].double().abs() @ kv.abs().T).amax(-1)
+        assert torch.all((lse[i].cpu().double() - ref).abs() <= P.lse_tolerance(dots, ref, n))
+        want, absv = w @ kv[:, :512], w @ kv[:, :512].abs()
+        assert torch.all((out[i].cpu().double() - want).abs() <= P.out_tolerance(want, absv, dots, n))
+
+
+def test_an_item_of_weights_longer_than_the_wait_limit(short_waits):
+    # the first tokens, seen by all 32768 rows of 16 heads (2048 blocks of about 3.3 us for each 256 tokens); a window
+    # of 1 leaves the other tokens only their own row.  256 first tokens an item, three items a cluster
+    rows, heads, page = 32768, 16, 256
+    sinks = 3 * 256 * (L.sm_count() // 2)
+    n = sinks + rows
+    bt = _shared_pages(n, rows, heads, page, 5)
+    row_off, q, tok_off, tok_end, pages = bt.on(dev, L)
+    lse = torch.full((rows, heads), 8.0, device=dev)
+    mass = torch.zeros(n, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    L.mla_mass(row_off, q, lse, tok_off, n, pages, bt.scale, mass, mass, st, tok_end=tok_end, window=1, sinks=sinks)
+    assert int(st.item()) == 0
+    kv, qd = bt.kv[:page].to(dev).double(), q.double()
+    s = bt.scale * qd.view(-1, 576) @ kv.T - 8.0
+    want = s.exp_().view(rows, heads, page).sum((0, 1)).cpu()
+    # (a score is off by up to 2^-17 of scale * sum |q k|, about 27 +- 1: 2.2e-4 of its weight; the exponential and the
+    # sums, 64 terms long and compensated beyond, add 2e-5)
+    got = mass[:sinks].cpu().double().view(-1, page)
+    assert torch.all((got - want).abs() <= 3e-4 * want)
