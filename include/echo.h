@@ -477,10 +477,10 @@ int echo_prefill_block_static(int R, int64_t row0, int64_t n_keys, const float* 
 int echo_debug_stall_epilogue(int64_t limit_ns);
 
 /*
- * The other knob: the limit of the waits of later echo_mla_chunk and echo_mla_mass
- * calls, of the whole process (limit_ns < 0: the default, 2 s).  Their limit runs
- * from the last progress of the thread block, since one of its warps may wait for
- * a piece of work that takes longer than any fixed time.
+ * The other knob: the limit of those waits in later echo_mla_chunk and echo_mla_mass
+ * calls, of the whole process, that may lie behind a whole piece of work (limit_ns < 0:
+ * the default, 2 s).  A piece may take longer than any fixed time, so their limit
+ * runs from the last progress of the thread block.
  */
 int echo_debug_wait_limit(int64_t limit_ns);
 

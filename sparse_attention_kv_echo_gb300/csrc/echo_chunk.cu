@@ -464,6 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t c = cluster_rank();
     const int ci = blockIdx.x >> 1;
     Watch* const watch = &ctl->watch;
+    const volatile int* const abort = &watch->abort;
 
     if (tid == 0) {
         mbar_init(smem_addr(&ctl->q_full), 1);
@@ -544,7 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.f;
             for (int it = p.lo; it < p.hi; ++it, ++t) {
                 const uint32_t st = t & 1u;
-                ok = ok && mbar_wait_watch(smem_addr(&ctl->s_full[t & (kSBufs - 1)]), (t / kSBufs) & 1u, watch);
+                ok = ok && mbar_wait(smem_addr(&ctl->s_full[t & (kSBufs - 1)]), (t / kSBufs) & 1u, abort);
                 tc_fence_after();
                 __syncwarp();
                 float s[32];
@@ -595,14 +596,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 l = l * corr + ((part[0] + part[1]) + (part[2] + part[3]));
                 // this P buffer is free once PV of two tiles before is done
-                if (t >= 2) ok = mbar_wait_watch(smem_addr(&ctl->pv_done[st]), ((t >> 1) & 1u) ^ 1u, watch);
+                if (t >= 2) ok = mbar_wait(smem_addr(&ctl->pv_done[st]), ((t >> 1) & 1u) ^ 1u, abort);
                 uint8_t* const prow = gP + st * kPBytes + row * 128;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     *reinterpret_cast<uint4*>(prow + (((4 * half + j) ^ (row & 7)) << 4)) =
                         make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
                 if (it > p.lo && moves) {  // O holds earlier tiles: bring it to the new reference
-                    ok = ok && mbar_wait_watch(smem_addr(&ctl->pv_done[st ^ 1u]), ((t - 1) >> 1) & 1u, watch);
+                    ok = ok && mbar_wait(smem_addr(&ctl->pv_done[st ^ 1u]), ((t - 1) >> 1) & 1u, abort);
                     tc_fence_after();
                     __syncwarp();
 #pragma unroll 1
@@ -624,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float L = 0.f;
             if (p.hi > p.lo) {
                 ctl->mx[t & 1u][half][row] = l;
-                if (pieces >= 1) ok = ok && mbar_wait_watch(smem_addr(&ctl->fin_free), (pieces - 1) & 1u, watch);
+                if (pieces >= 1) ok = ok && mbar_wait(smem_addr(&ctl->fin_free), (pieces - 1) & 1u, abort);
                 ++pieces;
                 ok = !softmax_sync_or(!ok);
                 if (!ok) break;
@@ -678,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     n[i] = rk < 0 ? 0u : 16u;
                     dst[i] = sK + st * kKBytes + static_cast<uint32_t>(8 * w + r) * 128u + (static_cast<uint32_t>(x ^ r) << 4);
                 }
-                if (t >= 2) ok = mbar_wait_watch(smem_addr(&ctl->k_free[st]), ph ^ 1u, watch);
+                if (t >= 2) ok = mbar_wait(smem_addr(&ctl->k_free[st]), ph ^ 1u, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
 #pragma unroll
@@ -717,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     dst[i] = sV + st * kVBytes + static_cast<uint32_t>(16 * w + r) * 128u +
                              (static_cast<uint32_t>(x ^ (r & 7)) << 4);
                 }
-                if (t >= 2) ok = mbar_wait_watch(smem_addr(&ctl->pv_done[st]), ph ^ 1u, watch);
+                if (t >= 2) ok = mbar_wait(smem_addr(&ctl->pv_done[st]), ph ^ 1u, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
 #pragma unroll
@@ -738,15 +739,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             while (ok && walk.next(&p)) {
                 if (p.hi == p.lo) continue;
-                if (qk) ok = mbar_wait_cluster(smem_addr(&ctl->q_ready), groups & 1u, watch);
-                else if (groups > 0) ok = mbar_wait_cluster(smem_addr(&ctl->o_free), (groups - 1) & 1u, watch);
+                if (qk) ok = mbar_wait_cluster(smem_addr(&ctl->q_ready), groups & 1u, abort);
+                else if (groups > 0) ok = mbar_wait_cluster(smem_addr(&ctl->o_free), (groups - 1) & 1u, abort);
                 ++groups;
                 for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
                     const uint32_t st = t & 1u, ph = (t >> 1) & 1u;
                     if (qk) {
                         if (t >= kSBufs)
-                            ok = mbar_wait_cluster(smem_addr(&ctl->s_free[t & (kSBufs - 1)]), ((t / kSBufs) & 1u) ^ 1u, watch);
-                        ok = ok && mbar_wait_cluster(smem_addr(&ctl->k_ready[st]), ph, watch);
+                            ok = mbar_wait_cluster(smem_addr(&ctl->s_free[t & (kSBufs - 1)]), ((t / kSBufs) & 1u) ^ 1u, abort);
+                        ok = ok && mbar_wait_cluster(smem_addr(&ctl->k_ready[st]), ph, abort);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t d = tmem + kSCol + (t & (kSBufs - 1)) * 32u;
@@ -755,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         mma2_commit_both(smem_addr(&ctl->k_free[st]));
                         mma2_commit_both(smem_addr(&ctl->s_full[t & (kSBufs - 1)]));
                     } else {  // O += P V
-                        ok = mbar_wait_cluster(smem_addr(&ctl->pv_ready[st]), ph, watch);
+                        ok = mbar_wait_cluster(smem_addr(&ctl->pv_ready[st]), ph, abort);
                         if (!ok) break;
                         tc_fence_after();
                         if (st == 0) issue_pv<0>(tmem, sP, sV, it > p.lo);
@@ -767,7 +768,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) {  // the MMAs in flight end before the CTAs' memory goes
                 give_up(watch);
                 mma2_commit_both(smem_addr(&ctl->drain[qk ? 0 : 1]));
-                (void)mbar_wait_limit(smem_addr(&ctl->drain[qk ? 0 : 1]), 0, nullptr, kWaitNs);
+                (void)mbar_wait(smem_addr(&ctl->drain[qk ? 0 : 1]), 0, nullptr);
             }
         }
         __syncwarp();
@@ -779,7 +780,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (p.hi == p.lo) continue;
             // Q of the group, once the group before has no QK left.  Its (row, head) pairs are consecutive in q;
             // pairs past the group's own are another group's, or zeros, and their results are dropped
-            if (t >= 1) ok = mbar_wait_watch(smem_addr(&ctl->k_free[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, watch);
+            if (t >= 1) ok = mbar_wait(smem_addr(&ctl->k_free[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, abort);
             if (!ok) break;
             if (elect_one()) {
                 const uint32_t bar = smem_addr(&ctl->q_full);
@@ -789,11 +790,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             // always: the load lands before the CTA ends
-            ok = mbar_wait_limit(smem_addr(&ctl->q_full), groups & 1u, nullptr, kWaitNs);
+            ok = mbar_wait(smem_addr(&ctl->q_full), groups & 1u, nullptr);
             ++groups;
             if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->q_ready), 0);
             for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
-                ok = mbar_wait_watch(smem_addr(&ctl->k_full[t & 1u]), (t >> 1) & 1u, watch);
+                ok = mbar_wait(smem_addr(&ctl->k_full[t & 1u]), (t >> 1) & 1u, abort);
                 fence_proxy_async_smem();
                 if (ok && lane == 0) mbar_arrive_remote(smem_addr(&ctl->k_ready[t & 1u]), 0);
             }
@@ -821,7 +822,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             t += static_cast<uint32_t>(p.hi - p.lo);
             // (P of the last tile was written after PV of the one two before)
             ok = mbar_wait_watch(smem_addr(&ctl->fin_ready), pieces & 1u, watch) &&
-                 mbar_wait_watch(smem_addr(&ctl->pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, watch);
+                 mbar_wait(smem_addr(&ctl->pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, abort);
             ++pieces;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -884,7 +885,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && walk.next(&p)) {
             for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
-                ok = mbar_wait_watch(smem_addr(&ctl->v_full[t & 1u]), (t >> 1) & 1u, watch);
+                ok = mbar_wait(smem_addr(&ctl->v_full[t & 1u]), (t >> 1) & 1u, abort);
                 fence_proxy_async_smem();
                 if (ok && lane == 0) {
                     mbar_arrive_remote(smem_addr(&ctl->pv_ready[t & 1u]), 0);

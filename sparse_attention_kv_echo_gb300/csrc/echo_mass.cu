@@ -484,14 +484,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int b = p.lo; ok && b < p.hi; ++b, ++d) {
                     const int n = (block_cols(p.g, a.heads, p.g.cb0 + b) + 31) & ~31;
                     const uint32_t db = d & 1u, idesc = idesc_bf16_f32(256, static_cast<uint32_t>(n));
-                    if (d >= 2 && !mbar_wait_cluster(smem_addr(&ctl->d_free[db]), ((d >> 1) & 1u) ^ 1u, watch)) {
+                    if (d >= 2 && !mbar_wait_cluster_watch(smem_addr(&ctl->d_free[db]), ((d >> 1) & 1u) ^ 1u, watch)) {
                         ok = false;
                         break;
                     }
                     k = k0;
                     for (int at = 0; at < kAtoms; ++at, k.step(kKSlots), q.step(kQSlots)) {
-                        if (b == p.lo) ok = mbar_wait_cluster(smem_addr(&ctl->k_ready[k.slot]), k.phase, watch);
-                        ok = ok && mbar_wait_cluster(smem_addr(&ctl->q_ready[q.slot]), q.phase, watch);
+                        if (b == p.lo) ok = mbar_wait_cluster_watch(smem_addr(&ctl->k_ready[k.slot]), k.phase, watch);
+                        ok = ok && mbar_wait_cluster_watch(smem_addr(&ctl->q_ready[q.slot]), q.phase, watch);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t ad = sw128_kmajor_desc(sK + static_cast<uint32_t>(k.slot) * kSlot);

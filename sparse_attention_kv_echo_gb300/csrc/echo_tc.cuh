@@ -176,7 +176,17 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 }
 
 // mbar_wait for a barrier the other CTA arrives on (or data it wrote).
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const Watch* w) {
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    if (mbar_try_wait_cluster(bar, parity, 0u)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (mbar_try_wait_cluster(bar, parity, 20000u)) return true;
+        if (*abort) return false;
+        if (global_ns() - t0 > kWaitNs) return false;
+    }
+}
+// The same under a watch.
+__device__ __forceinline__ bool mbar_wait_cluster_watch(uint32_t bar, uint32_t parity, const Watch* w) {
     if (mbar_try_wait_cluster(bar, parity, 0u)) return true;
     uint32_t seen = static_cast<const volatile Watch*>(w)->beat;
     uint64_t t0 = global_ns();
