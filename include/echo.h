@@ -569,7 +569,9 @@ typedef struct echo_pages {
  *   A cache row that some row of the call sees must be finite; rows that none
  *   sees are not read.
  * Scores and sums are fp32; the softmax weights enter the value sum rounded to
- * bf16.  ws: echo_mla_chunk_workspace_size(n_rows, heads, B) bytes of device
+ * bf16.  The tensor cores' accumulation cuts low bits off: a score comes out up to 5e-7 of
+ * its size nearer to zero, the value sum up to 2e-4 (over any number of tokens; it is
+ * added up in fp32 every 32768 tokens).  ws: echo_mla_chunk_workspace_size(n_rows, heads, B) bytes of device
  * memory, 256-byte aligned, whose contents need not be kept between calls;
  * calls that may run at the same time need their own.
  * Errors: ECHO_EINVAL (sizes, NULL or misaligned pointers, a small workspace),

@@ -42,7 +42,8 @@
 // units [T i / n, T (i + 1) / n) of it, whatever groups those cut, so ragged
 // batches, single long requests and whole prompts load all SMs alike.  The parts
 // of a cut group go to the workspace in fp32 with their maximum and sum, and
-// chunk_join_kernel adds them in order (the same bits every time).
+// chunk_join_kernel adds them in order (the same bits every time).  A part of more than
+// kLeg tiles is walked in legs, added up in its place in the workspace.
 #include "echo_paged.cuh"
 #include "echo_tc.cuh"
 
@@ -75,8 +76,13 @@ constexpr int kMinUnits = 2;             // least units per cluster
 constexpr int kMaxClusters = 96;         // bounds the workspace (the device has 76 pairs of SMs)
 constexpr uint32_t kIdescS = idesc_bf16_f32(kM, kTok);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kM, 256) | (1u << 16);  // B (V) MN-major
+// Tiles after which O leaves the tensor memory and is added to what the legs before left, in fp32 and rounded: the
+// MMAs' accumulation cuts low bits off, so that a sum over n tiles comes out n * 3e-7 too near to zero (values of one
+// sign: 1.7e-4 after 512 tiles, 6.5e-3 after 16384 in one leg).  With 1M tokens a leg of 512 costs 0 to 2% of the time
+// (152 rows: 29.0 ms in one leg, 29.0 to 29.9 ms in legs of 256 to 2048 tiles).
+constexpr int kLeg = 512;
 constexpr size_t kPartO = static_cast<size_t>(kM) * kLatDv * 4;
-constexpr size_t kPartBytes = kPartO + 2 * kM * 4;
+constexpr size_t kPartBytes = kPartO + 3 * kM * 4;  // O, maxima, sums, factors of a leg
 
 // One group: what its rows see is v in [0, nv): token v for v < kept, else v - kept + lo
 // with lo = pos0 + rows + kept - nv (the union over its rows); with selections
@@ -281,30 +287,39 @@ __global__ void __launch_bounds__(kPT) chunk_plan_kernel(ChunkArgs a, Plan plan)
     }
 }
 
-// The part of a group that a share holds: tiles [lo, hi) of `tiles`.
+// A leg, at most kLeg tiles, of the part of a group that a share holds (a piece): tiles [lo, hi) of `tiles`.
 struct Piece {
     Group g;
     int lo, hi, tiles;
+    bool left, right;  // the piece starts behind the group's first tile, ends before its last
+    bool later, last;  // legs of the piece come before this one, none after it
 };
 
-// Walks the pieces of a share; every role of the cluster sees the same ones.
+// Walks the legs of a share's pieces; every role of the cluster sees the same ones.
 struct Walk {
     const Group* group;
     const int64_t* cum;
     int64_t u0, u1;
     int g;
+    bool on = false;  // legs of the piece are left
     // False when the share is done.  Groups that see nothing come with tiles = 0.
     __device__ __forceinline__ bool next(Piece* p) {
         for (;;) {
             if (u0 >= u1) return false;
             const int64_t c = cum[g];
             p->g = group[g];
-            ++g;
             p->tiles = tiles_of(p->g.nv);
             const int64_t a = u0 - c, b = min(u1 - c, static_cast<int64_t>(kOver + p->tiles));
-            u0 = c + kOver + p->tiles;
             p->lo = static_cast<int>(max(static_cast<int64_t>(0), a - kOver));
-            p->hi = static_cast<int>(max(static_cast<int64_t>(0), b - kOver));
+            const int to = static_cast<int>(max(static_cast<int64_t>(0), b - kOver));
+            p->hi = min(to, p->lo + kLeg);
+            p->last = p->hi == to;
+            p->later = on;
+            if (!on) p->left = p->lo > 0;
+            p->right = to < p->tiles;
+            on = !p->last;
+            u0 = c + kOver + (on ? p->hi : p->tiles);
+            g += on ? 0 : 1;
             if (p->hi > p->lo || (p->tiles == 0 && a <= 0)) return true;
         }
     }
@@ -363,6 +378,12 @@ struct Gather {
     }
 };
 
+// Where a piece's part goes.  A share's first piece may be cut on its left, its last on its right; the legs of a
+// whole piece meet in the last one's place, which is written after it.
+__device__ __forceinline__ uint8_t* part_of(const Plan& plan, int ci, const Piece& p) {
+    return plan.part + static_cast<size_t>(2 * ci + (p.left ? 0 : 1)) * kPartBytes;
+}
+
 // ---------------------------------------------------------------- attention
 constexpr int kValid = 8;
 static_assert(kValid >= kSBufs + 3, "valid flags");
@@ -411,6 +432,63 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int q) {
         if (high) w[i] = x;
         else w[i + 2] = x;
     }
+}
+
+// A warp's 32 rows x 256 dims of O, times f (a factor for each of a lane's rows), as bf16 to dst or, where that is
+// null, in fp32 to part; kLater: what the legs before left in part, by this thread, times fb is added first.
+template <bool kLater>
+__device__ __forceinline__ void store_o(uint32_t taddr, const float (&f)[4], const float (&fb)[4], uint8_t* dst, uint8_t* part,
+                                        int live) {
+    const int lane = threadIdx.x & 31, q = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll 1
+        for (uint32_t x = 0; x < 256u; x += 32u) {
+            float2 was[8];
+            if constexpr (kLater) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int r = 16 * h + 8 * g + (lane >> 2);
+                        was[4 * g + b] = make_float2(0.f, 0.f);
+                        if (r < live)
+                            was[4 * g + b] = *reinterpret_cast<const float2*>(part + static_cast<int64_t>(r) * (kLatDv * 4) + 4 * x + 32 * b + 8 * q);
+                    }
+            }
+            float o[16];
+            tmem_ld_16x256_x4(taddr + (static_cast<uint32_t>(16 * h) << 16) + x, o);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int r = 16 * h + 8 * g + (lane >> 2);
+                float ff = f[2 * h + g];
+                if constexpr (kLater) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        o[4 * b + 2 * g] = fmaf(was[4 * g + b].x, fb[2 * h + g], o[4 * b + 2 * g] * ff);
+                        o[4 * b + 2 * g + 1] = fmaf(was[4 * g + b].y, fb[2 * h + g], o[4 * b + 2 * g + 1] * ff);
+                    }
+                    ff = 1.f;
+                }
+                if (dst) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[4 * b + 2 * g] * ff, o[4 * b + 2 * g + 1] * ff);
+                        w[b] = *reinterpret_cast<const uint32_t*>(&b2);
+                    }
+                    quad_transpose(w, q);  // lane q now has columns 8q .. 8q + 7 of the 32
+                    if (r < live)
+                        *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(r) * (kLatDv * 2) + 2 * x + 16 * q) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                } else if (r < live) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        *reinterpret_cast<float2*>(part + static_cast<int64_t>(r) * (kLatDv * 4) + 4 * x + 32 * b + 8 * q) =
+                            make_float2(o[4 * b + 2 * g], o[4 * b + 2 * g + 1]);
+                }
+            }
+        }
 }
 
 // Barrier over the softmax warps; true when any thread votes so.
@@ -621,7 +699,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->pv_ready[st]), 0);
             }
             if (over) break;
-            // ---- the piece's sums: its lse, or this part's, and the factors of O for the warps that store it
+            // ---- the leg's sums, joined to those of the legs before; after the last: the row's lse, or this part's.
+            // The factors of O, and of what the legs before left, for the warps that store it
             float L = 0.f;
             if (p.hi > p.lo) {
                 ctl->mx[t & 1u][half][row] = l;
@@ -631,12 +710,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 L = l + ctl->mx[t & 1u][half ^ 1][row];
             }
-            const bool whole = p.lo == 0 && p.hi == p.tiles;
             if (half == 0) {
+                const bool whole = !p.left && !p.right;
+                float* const ml = reinterpret_cast<float*>(part_of(plan, ci, p) + kPartO);
+                float before = 0.f, mine = 1.f;
+                if (p.later) {
+                    const float m0 = ml[mi], l0 = ml[kM + mi], both = fmaxf(m0, m);
+                    before = m0 == -INFINITY ? 0.f : exp2f(m0 - both);
+                    mine = m == -INFINITY ? 0.f : exp2f(m - both);
+                    L = l0 * before + L * mine;
+                    m = both;
+                }
                 const bool any = L != 0.f;  // a NaN among the scores stays one
-                if (p.hi > p.lo) ctl->fin[row] = !whole ? 1.f : any ? 1.f / L : 0.f;
-                if (!whole) {
-                    float* const ml = reinterpret_cast<float*>(plan.part + static_cast<size_t>(2 * ci + (p.lo > 0 ? 0 : 1)) * kPartBytes + kPartO);
+                const float norm = !(whole && p.last) ? 1.f : any ? 1.f / L : 0.f;
+                if (p.hi > p.lo) ctl->fin[row] = mine * norm;
+                if (p.later) ml[2 * kM + mi] = before * norm;
+                if (!whole || !p.last) {
                     ml[mi] = m;
                     ml[kM + mi] = L;
                 } else if (lives) {
@@ -805,14 +894,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // sectors: a lane a row, straight to memory, took 5 us a group, through shared memory by the softmax warps 3
         const int half = (warp & 3) >> 1, r_cta = (warp & 1) * 32;  // dims 256 half .., rows of this CTA's 64
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int q = lane & 3;
         uint32_t pieces = 0;
         bool ok = true;
         while (ok && walk.next(&p)) {
-            const bool whole = p.lo == 0 && p.hi == p.tiles;
+            const bool direct = !p.left && !p.right && p.last;
             const int live = p.g.rows * a.heads - static_cast<int>(c) * 64 - r_cta;  // of this warp's 32 rows
             const int64_t at = static_cast<int64_t>(p.g.row0) * a.heads + static_cast<int>(c) * 64 + r_cta;
-            uint8_t* const dst = whole ? reinterpret_cast<uint8_t*>(out + at * kLatDv + half * 256) : nullptr;
+            uint8_t* const dst = direct ? reinterpret_cast<uint8_t*>(out + at * kLatDv + half * 256) : nullptr;
             if (p.hi == p.lo) {  // nothing was seen
                 if (warp == 16 && lane == 0) watch_beat(watch);
                 for (int i = lane; i < 32 * 32; i += 32)
@@ -827,42 +915,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            uint8_t* const part = plan.part + static_cast<size_t>(2 * ci + (p.lo > 0 ? 0 : 1)) * kPartBytes +
-                                  (static_cast<size_t>(static_cast<int>(c) * 64 + r_cta) * kLatDv + half * 256) * 4;
-            float f[4];
+            uint8_t* const part =
+                part_of(plan, ci, p) + (static_cast<size_t>(static_cast<int>(c) * 64 + r_cta) * kLatDv + half * 256) * 4;
+            const float* const factors = reinterpret_cast<const float*>(part_of(plan, ci, p) + kPartO) + 2 * kM + static_cast<int>(c) * 64 + r_cta;
+            float f[4], fb[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = ctl->fin[r_cta + 8 * i + (lane >> 2)];
+            if (p.later) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fb[i] = factors[8 * i + (lane >> 2)];
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&ctl->fin_free));
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll 1
-                for (uint32_t x = 0; x < 256u; x += 32u) {
-                    float o[16];
-                    tmem_ld_16x256_x4(tmem + lane_base + (static_cast<uint32_t>(16 * h) << 16) + x, o);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const int r = 16 * h + 8 * g + (lane >> 2);
-                        const float ff = f[2 * h + g];
-                        if (whole) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) {
-                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[4 * b + 2 * g] * ff, o[4 * b + 2 * g + 1] * ff);
-                                w[b] = *reinterpret_cast<const uint32_t*>(&b2);
-                            }
-                            quad_transpose(w, q);  // lane q now has columns 8q .. 8q + 7 of the 32
-                            if (r < live)
-                                *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(r) * (kLatDv * 2) + 2 * x + 16 * q) =
-                                    make_uint4(w[0], w[1], w[2], w[3]);
-                        } else if (r < live) {
-#pragma unroll
-                            for (int b = 0; b < 4; ++b)
-                                *reinterpret_cast<float2*>(part + static_cast<int64_t>(r) * (kLatDv * 4) + 4 * x + 32 * b + 8 * q) =
-                                    make_float2(o[4 * b + 2 * g], o[4 * b + 2 * g + 1]);
-                        }
-                    }
-                }
+            if (p.later) store_o<true>(tmem + lane_base, f, fb, dst, part, live);
+            else store_o<false>(tmem + lane_base, f, fb, dst, part, live);
             tc_fence_before();  // O is read: the next group's first PV may overwrite it
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->o_free), 0);

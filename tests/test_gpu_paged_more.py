@@ -295,3 +295,82 @@ def test_an_item_of_weights_longer_than_the_wait_limit(short_waits):
     # sums, 64 terms long and compensated beyond, add 2e-5)
     got = mass[:sinks].cpu().double().view(-1, page)
     assert torch.all((got - want).abs() <= 3e-4 * want)
+
+
+def _counted(bt, i, window=0, sinks=0, sel=None):
+    """Row i's (lse, out, absv, dots) in 64 bits, from how often each cache row is seen."""
+    t = bt.visible(0, i, window, sinks, sel)
+    times = torch.bincount(bt.cache_row(0, t), minlength=bt.kv.shape[0]).double()
+    there = times > 0
+    kv, times, q = bt.kv[there].double(), times[there], bt.q[i].double()
+    s = bt.scale * q @ kv.T
+    lse = torch.logsumexp(s + times.log(), -1)
+    w = torch.exp(s - lse[:, None]) * times
+    return lse, w @ kv[:, :512], w @ kv[:, :512].abs(), bt.scale * (q.abs() @ kv.abs().T).amax(-1)
+
+
+def _attend_long(bt, **kw):
+    row_off, q, tok_off, tok_end, pages = bt.on(dev, L)
+    out = torch.full((bt.n, bt.heads, 512), 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((bt.n, bt.heads), 7.0, device=dev)
+    ws = torch.full((L.mla_chunk_workspace_size(bt.n, bt.heads, 1),), 0xFF, dtype=torch.uint8, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    L.mla_chunk(row_off, q, tok_off, bt.n_tokens, pages, bt.scale, out, lse, ws, st, tok_end=tok_end, **kw)
+    assert int(st.item()) == 0
+    return out.cpu(), lse.cpu()
+
+
+def test_values_of_one_sign_over_a_million_tokens():
+    # every accumulation may cut off two of the sum's last bits (2^-22): over the 2048 of a leg, the sum growing
+    # evenly, at most 2^-12 on the mean; the roundings of weights and results have no sign
+    n, rows = 1 << 20, 160
+    bt = _shared_pages(n, rows, 128, 4096, 7)
+    bt.kv[:, :512] = bt.kv[:, :512].abs()
+    out, lse = _attend_long(bt)
+    for i in (0, 80, 159):
+        ref, want, absv, dots = _counted(bt, i)
+        assert torch.all((lse[i].double() - ref).abs() <= P.SCORE * dots + P.EXP * (1 + ref.abs()))
+        off = (out[i].double() - want) / absv
+        assert abs(float(off.mean())) <= 2.0 ** -12
+        assert torch.all(off.abs() <= 2.0 ** -8 + 2 * P.SCORE * dots[:, None] * 1.01 + 2.0 ** -8 + 2.0 ** -10)
+
+
+@pytest.mark.parametrize("heads,kind", [(128, "rising"), (128, "falling"), (128, "empty"), (16, "rising"), (40, "window"),
+                                        (128, "nan"), (128, "listed")])
+def test_pieces_of_several_legs(heads, kind):
+    # 40000 to 100000 tokens a row, more rows than clusters: pieces of several legs, whole ones and ones that are joined
+    page = 512
+    per, kw = 128 // heads, {}
+    n, rows = (100_000 if kind != "listed" else 600), 160 * per
+    bt = _shared_pages(n, rows, heads, page, 11)
+    g = torch.Generator().manual_seed(4)
+    pages = -(-n // page)
+    bt.kv = torch.randn((4 * page, 576), generator=g).to(torch.bfloat16)
+    order = torch.arange(pages) * 4 // pages                  # page 0 first, page 3 last
+    bt.tab = (order if kind != "falling" else 3 - order).to(torch.int32)
+    for i in range(4):                                        # longer keys, larger maxima
+        bt.kv[i * page:(i + 1) * page] *= 0.5 + 0.5 * i
+    if kind == "empty":                                       # a row sees nothing in its first and third quarters
+        bt.tab[(order == 0) | (order == 2)] = -1
+    if kind == "window":
+        kw = dict(window=70_000, sinks=50)
+    if kind == "nan":
+        bt.q[5, 3, 9] = float("nan")
+    sel = None
+    if kind == "listed":
+        sel = torch.randint(0, n, (rows, 40_000), generator=g, dtype=torch.int32)
+        sel[torch.rand(sel.shape, generator=g) < 0.1] = -1
+        kw = dict(sel=sel.to(dev))
+    out, lse = _attend_long(bt, **kw)
+    again = _attend_long(bt, **kw)
+    assert torch.equal(out.view(torch.int16), again[0].view(torch.int16))
+    assert torch.equal(lse.view(torch.int32), again[1].view(torch.int32))
+    for i in sorted({0, 1, 5, rows // 3, rows // 2, rows - 2, rows - 1}):
+        ref, want, absv, dots = _counted(bt, i, kw.get("window", 0), kw.get("sinks", 0), sel)
+        hurt = torch.isnan(ref)
+        assert torch.equal(hurt, torch.isnan(lse[i])) and torch.all(torch.isnan(out[i][hurt]))
+        ok = ~hurt
+        tol = P.lse_tolerance(dots, ref, 0)
+        assert torch.all((lse[i].double() - ref).abs()[ok] <= tol[ok])
+        tol = P.out_tolerance(want, absv, dots, 0) + absv * 2.0 ** -11
+        assert torch.all((out[i].double() - want).abs()[ok] <= tol[ok]), (i, float(((out[i].double() - want).abs() / tol)[ok].max()))
