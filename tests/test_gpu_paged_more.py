@@ -374,3 +374,25 @@ def test_pieces_of_several_legs(heads, kind):
         assert torch.all((lse[i].double() - ref).abs()[ok] <= tol[ok])
         tol = P.out_tolerance(want, absv, dots, 0) + absv * 2.0 ** -11
         assert torch.all((out[i].double() - want).abs()[ok] <= tol[ok]), (i, float(((out[i].double() - want).abs() / tol)[ok].max()))
+
+
+# ---------------------------------------------------------------- rows that add nothing
+@pytest.mark.parametrize("heads,rows", [(128, 5), (16, 200), (40, 33)])
+def test_a_row_without_lse_adds_no_weight_whatever_its_query_holds(heads, rows):
+    # a padded batch: rows whose lse is -inf, their queries never written
+    bt = P.Batch([600, 90], [rows, 1], heads, 16, seed=heads)
+    lse = bt.attend()[1].float()
+    out = torch.arange(rows + 1) % 3 == 1
+    lse[out] = -float("inf")
+    g = torch.Generator().manual_seed(1)
+    mass = torch.rand(bt.n_tokens, generator=g)
+    bt.q[out] = 0.0
+    call, clean, st = _weigh(bt, lse.to(dev), mass.to(dev))
+    call()
+    for junk in float("nan"), float("inf"), -float("inf"):
+        bt.q[out] = junk
+        call, got, st2 = _weigh(bt, lse.to(dev), mass.to(dev))
+        call()
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and int(st2.item()) == 0
+        assert torch.equal(got, clean) and torch.all(torch.isfinite(got))
