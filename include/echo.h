@@ -594,8 +594,10 @@ int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int heads, con
  * without a cache row, or that no row sees, only decays); other entries of
  * mass_out are left as they were.  mass and mass_out [n_tokens] f32 may be the
  * same array; decay is finite and >= 0, and with decay = 0 mass is not read.
- * A row whose lse is -inf adds nothing.  Everything is fp32 and summed in a fixed
- * order.  ws: echo_mla_mass_workspace_size(n_tokens, B) bytes, as
+ * A row whose lse is -inf adds nothing.  Sums are fp32 in a fixed order; the scores are
+ * those of echo_mla_chunk, up to 5e-7 of their size nearer to zero than the products'
+ * sum, and a weight is within 1e-5 of its value for scores up to 12 (1.5e-6 measured
+ * over 1024 rows).  ws: echo_mla_mass_workspace_size(n_tokens, B) bytes, as
  * echo_mla_chunk's.  Limits and errors as echo_mla_chunk; n_tokens >
  * ECHO_MASS_MAX_TOKENS: ECHO_EUNSUPPORTED.
  */

@@ -1,5 +1,5 @@
 """More of the calls over a paged latent cache: workspaces on other streams, caches under lazy reuse, long
-pieces of work."""
+pieces of work, rows that add nothing, and the sizes that are measured, by samples."""
 import numpy as np
 import pytest
 import torch
@@ -396,3 +396,122 @@ def test_a_row_without_lse_adds_no_weight_whatever_its_query_holds(heads, rows):
         torch.cuda.synchronize()
         assert int(st.item()) == 0 and int(st2.item()) == 0
         assert torch.equal(got, clean) and torch.all(torch.isfinite(got))
+
+
+# ---------------------------------------------------------------- at the sizes that are measured
+def _samples(bt, out, lse, rows, window=0, sinks=0, sel=None):
+    """Compares sampled rows (request, row) with their 64-bit values."""
+    for b, i in rows:
+        r = int(bt.row_off[b]) + i
+        t = bt.visible(b, i, window, sinks, sel)
+        k, q = bt.kv[bt.cache_row(b, t)].double(), bt.q[r].double()
+        s = bt.scale * q @ k.T
+        ref = torch.logsumexp(s, -1)
+        w = torch.exp(s - ref[:, None])
+        dots = bt.scale * (q.abs() @ k.abs().T).amax(-1)
+        assert torch.all((lse[r].double() - ref).abs() <= P.lse_tolerance(dots, ref, t.numel()))
+        want, absv = w @ k[:, :512], w @ k[:, :512].abs()
+        assert torch.all((out[r].double() - want).abs() <= P.out_tolerance(want, absv, dots, t.numel())), (b, i)
+
+
+def _run_attention(bt, sel=None, **kw):
+    row_off, q, tok_off, tok_end, pages = bt.on(dev, L)
+    got = []
+    for _ in range(2):
+        out = torch.full((bt.n, bt.heads, 512), 7.0, dtype=torch.bfloat16, device=dev)
+        lse = torch.full((bt.n, bt.heads), 7.0, device=dev)
+        ws = torch.full((L.mla_chunk_workspace_size(bt.n, bt.heads, len(bt.lens)),), 0xFF, dtype=torch.uint8, device=dev)
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
+        L.mla_chunk(row_off, q, tok_off, bt.n_tokens, pages, bt.scale, out, lse, ws, st, tok_end=tok_end,
+                    sel=None if sel is None else sel.to(dev), **kw)
+        assert int(st.item()) == 0
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])     # the same bits again
+    return got[0][0].cpu(), got[0][1].cpu()
+
+
+def test_a_block_of_2048_rows_over_8192_tokens():
+    bt = P.Batch([8192], [2048], 128, 64, seed=31)
+    _samples(bt, *_run_attention(bt), [(0, i) for i in (0, 1, 555, 1024, 2046, 2047)])
+    out, lse = _run_attention(bt, window=1024, sinks=16)
+    _samples(bt, out, lse, [(0, i) for i in (0, 700, 2047)], 1024, 16)
+
+
+def test_one_row_of_each_of_32_ragged_requests():
+    lens = [int(round(1024 * 16 ** (b / 31))) for b in range(32)]
+    bt = P.Batch(lens, [1] * 32, 128, 64, seed=32)
+    out, lse = _run_attention(bt)
+    _samples(bt, out, lse, [(b, 0) for b in (0, 1, 15, 16, 30, 31)])
+    out, lse = _run_attention(bt, window=4096, sinks=4)
+    _samples(bt, out, lse, [(b, 0) for b in (0, 16, 31)], 4096, 4)
+
+
+@pytest.mark.parametrize("heads", [128, 16])
+def test_1024_rows_of_2048_listed_tokens(heads):
+    bt = P.Batch([32768], [1024], heads, 1, seed=33)
+    g = torch.Generator().manual_seed(9)
+    sel = torch.randint(0, 32768 - 1024, (1024, 2048), generator=g, dtype=torch.int32)
+    out, lse = _run_attention(bt, sel=sel)
+    _samples(bt, out, lse, [(0, i) for i in (0, 3, 511, 1023)], sel=sel)
+
+
+@pytest.mark.parametrize("lens,rows,heads,absent", [([8192], [1024], 128, 0.0), ([2048, 4096, 8192], [1, 1, 1], 128, 0.25),
+                                                     ([3000, 700], [40, 1], 16, 0.0), ([1500], [1], 1, 0.0)])
+def test_weights_are_within_1e5_of_the_64_bit_ones(lens, rows, heads, absent):
+    # the header's bound.  What is in it: scores 5e-7 of their size off (|s| up to 12: 6e-6), the score and -lse in
+    # units of log2 rounded to 2^-24 of up to 24 (1.4e-6 each, times log 2), the exponential 2^-22, the sums 4e-6 at
+    # 64 terms of one sign in the worst order, their roundings of both signs in fact
+    bt = P.Batch(lens, rows, heads, 1 if absent else 64, seed=34, absent=absent)
+    out, lse = _run_attention(bt)
+    g = torch.Generator().manual_seed(3)
+    mass = torch.rand(bt.n_tokens, generator=g)
+    call, got, st = _weigh(bt, lse.to(dev), mass.to(dev))
+    call()
+    assert int(st.item()) == 0
+    got = got.cpu().double() - 0.5 * mass.double()
+    for b in range(len(lens)):
+        r0, r1, off = int(bt.row_off[b]), int(bt.row_off[b + 1]), int(bt.tok_off[b])
+        first = lens[b] - rows[b]
+        t = torch.cat([torch.arange(8), torch.randint(0, lens[b], (40,), generator=g), torch.arange(lens[b] - 8, lens[b])])
+        rows_of = bt.cache_row(b, t)
+        t, rows_of = t[rows_of >= 0], rows_of[rows_of >= 0]
+        q, k = bt.q[r0:r1].to(dev).double(), bt.kv[rows_of].to(dev).double()
+        w = torch.exp(bt.scale * (q.view(-1, 576) @ k.T).view(r1 - r0, heads, -1) - lse[r0:r1].to(dev).double()[..., None])
+        see = t.to(dev)[None, :] <= first + torch.arange(r1 - r0, device=dev)[:, None]
+        want = (w * see[:, None, :]).sum((0, 1)).cpu()
+        # (0.5 * mass is taken off again: two roundings of the sum)
+        assert torch.all((got[off + t] - want).abs() <= 1e-5 * want + 2.0 ** -23 * (want + mass[off + t].double())), b
+
+
+@pytest.mark.parametrize("lazy", [False, True])
+def test_victims_of_caches_with_more_slots_than_a_block_keeps_keys_of(lazy):
+    # 10 requests of 524288 slots: 65536 slots a block, of which it keeps 53248 keys and gathers the others again
+    B, C, length = 10, 524288, 600_000
+    g = torch.Generator(device=dev).manual_seed(8)
+    off = torch.arange(B + 1, device=dev) * length
+    s2t = torch.stack([torch.randperm(length, generator=g, device=dev)[:C] for _ in range(B)]).to(torch.int32)
+    s2t[:, ::41] = -1
+    mass = torch.rand(B * length, generator=g, device=dev)
+    mass[::3] = 0.25                                        # ties
+    mass[1::3] = (mass[1::3] * 8).floor() / 8
+    free = torch.zeros((B, C), dtype=torch.bool, device=dev)
+    bits = None
+    if lazy:
+        free = torch.rand((B, C), generator=g, device=dev) < 0.4
+        bits = (free.view(B, C // 32, 32).long() << torch.arange(32, device=dev)).sum(2)
+        bits = torch.where(bits >= 2 ** 31, bits - 2 ** 32, bits).to(torch.int32).flatten()
+    et = torch.empty((B, C), dtype=torch.int32, device=dev)
+    es, ec, st = torch.empty_like(et), torch.empty(B, dtype=torch.int32, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    for keep in (C // 8, C // 2 + 77):
+        L.evict_select(off, B * length, s2t, mass, keep, et, es, ec, st, sinks=100, recent=1000, freebits=bits)
+        assert int(st.item()) == 0
+        for b in range(B):
+            tok = torch.where(free[b], -1, s2t[b]).cpu().numpy()
+            slots = np.nonzero(tok >= 0)[0]
+            may = slots[(tok[slots] >= 100) & (tok[slots] < length - 1000)]
+            want = max(0, min(len(slots) - keep, len(may)))
+            m = mass[b * length:(b + 1) * length].cpu().numpy()[tok[may]]
+            gone = np.sort(may[np.lexsort((tok[may], m))[:want]])
+            assert int(ec[b]) == want > 0 or (want == 0 and int(ec[b]) == 0)
+            assert np.array_equal(es[b].cpu().numpy(), np.concatenate([gone, np.full(C - want, -1)]))
+            assert np.array_equal(et[b].cpu().numpy(), np.concatenate([tok[gone], np.full(C - want, -1)]))
