@@ -737,7 +737,9 @@ PAGED_METRIC = "attention of a 2048-row prompt block over a paged latent cache: 
 def run_paged(args):
     """The calls over a paged latent cache, alone: the fourth 2048-row block of the prompt over its 8192
     tokens (causal, through a 1024-token window, and over 2048 selected tokens a row), one row of each of 8
-    requests over 32768 tokens, the attention weights of both, and the victims of 8 x 4096 slots."""
+    requests over 32768 tokens, the attention weights of both (causal, with the lse of the causal attention), and
+    the victims of 8 x 4096 slots.  weights_per_row_and_head: the sum of a call's weights over its rows and heads, 1
+    when the lse are those of the rows."""
     import torch
     from sparse_attention_kv_echo_gb300 import _lib as L
     from sparse_attention_kv_echo_gb300 import workloads as wl
@@ -762,6 +764,7 @@ def run_paged(args):
         c["pages"] = L.KVPages(c["tab"], c["kv"], page)
         c["out"] = torch.empty((sum(rows), H, L.MLA_DV), dtype=torch.bfloat16, device=dev)
         c["lse"] = torch.empty((sum(rows), H), dtype=torch.float32, device=dev)
+        c["lse_causal"] = torch.empty_like(c["lse"])  # what the weights take: the calls below overwrite lse
         c["mass"] = torch.zeros(n, dtype=torch.float32, device=dev)
         c["ws"] = torch.empty(max(L.mla_chunk_workspace_size(sum(rows), H, len(rows)),
                                   L.mla_mass_workspace_size(n, len(rows))), dtype=torch.uint8, device=dev)
@@ -770,13 +773,13 @@ def run_paged(args):
     blk, dec = cache([4 * R], [R]), cache(batch.lengths, [1] * batch.B)
     sel = torch.rand((R, 3 * R), generator=g, device=dev).argsort(1)[:, :batch.k].to(torch.int32)  # before every row
 
-    def attend(c, **kw):
-        L.mla_chunk(c["row_off"], c["q"], c["off"], c["n"], c["pages"], scale, c["out"], c["lse"], c["ws"], st,
+    def attend(c, lse="lse", **kw):
+        L.mla_chunk(c["row_off"], c["q"], c["off"], c["n"], c["pages"], scale, c["out"], c[lse], c["ws"], st,
                     stream=main, **kw)
 
-    def weigh(c):
-        L.mla_mass(c["row_off"], c["q"], c["lse"], c["off"], c["n"], c["pages"], scale, c["mass"], c["mass"], st,
-                   decay=0.9375, ws=c["ws"], stream=main)
+    def weigh(c, decay=0.9375):
+        L.mla_mass(c["row_off"], c["q"], c["lse_causal"], c["off"], c["n"], c["pages"], scale, c["mass"], c["mass"], st,
+                   decay=decay, ws=c["ws"], stream=main)
 
     B, C = batch.B, batch.C
     s2t = torch.rand((B, batch.lengths[0]), generator=g, device=dev).argsort(1)[:, :C].to(torch.int32).contiguous()
@@ -790,6 +793,8 @@ def run_paged(args):
                                                  recent=256, stream=main)}
     flush = torch.empty(FLUSH_BYTES // 4, dtype=torch.float32, device=dev)
     torch.cuda.synchronize()
+    for c in (blk, dec):
+        attend(c, "lse_causal")
     us = {}
     for name, call in parts.items():
         ev = []
@@ -806,6 +811,11 @@ def run_paged(args):
             ev.append((a, b))
         torch.cuda.synchronize()
         us[name] = round(1e3 * statistics.median(a.elapsed_time(b) for a, b in ev[args.warmup:]), 2)
+    per = []
+    for c in (blk, dec):
+        weigh(c, decay=0.0)
+        main.synchronize()
+        per.append(round(float(c["mass"].double().sum()) / c["lse"].numel(), 6))
     pairs = sum(range(3 * R + 1, 4 * R + 1))
     t = us["block_causal"] * 1e-6
     print(json.dumps({
@@ -814,7 +824,7 @@ def run_paged(args):
         "dtype": "bf16 MMA, fp32 accumulate/softmax", "data": "synthetic (seeded)",
         "config": {"workload": f"{R} rows of {4 * R} tokens, 128 heads; {B} requests x {batch.lengths[0]} tokens; pages of "
                                f"{page}", "l2": "flushed by a 256 MB write before every timed call"},
-        "us": us, "tflops": round(2.0 * pairs * H * (L.MLA_DQK + L.MLA_DV) / t / 1e12, 1), "status": int(st.item()),
+        "us": us, "weights_per_row_and_head": per, "tflops": round(2.0 * pairs * H * (L.MLA_DQK + L.MLA_DV) / t / 1e12, 1), "status": int(st.item()),
     }), flush=True)
 
 

@@ -515,3 +515,17 @@ def test_victims_of_caches_with_more_slots_than_a_block_keeps_keys_of(lazy):
             assert int(ec[b]) == want > 0 or (want == 0 and int(ec[b]) == 0)
             assert np.array_equal(es[b].cpu().numpy(), np.concatenate([gone, np.full(C - want, -1)]))
             assert np.array_equal(et[b].cpu().numpy(), np.concatenate([tok[gone], np.full(C - want, -1)]))
+
+
+def test_the_bench_weighs_with_the_lse_of_its_rows():
+    import json
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "bench.py", "--part", "paged", "--steps", "2", "--warmup", "3"], cwd=root,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    line = json.loads(r.stdout.strip().splitlines()[-1])
+    assert line["status"] == 0 and len(line["weights_per_row_and_head"]) == 2
+    assert all(abs(x - 1.0) < 1e-4 for x in line["weights_per_row_and_head"])
