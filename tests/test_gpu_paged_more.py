@@ -1,5 +1,6 @@
 """More of the calls over a paged latent cache: workspaces on other streams, caches under lazy reuse, long
-pieces of work, rows that add nothing, and the sizes that are measured, by samples."""
+pieces of work, rows that add nothing, the sizes that are measured, by samples, and
+captured, empty and first calls."""
 import numpy as np
 import pytest
 import torch
@@ -529,3 +530,104 @@ def test_the_bench_weighs_with_the_lse_of_its_rows():
     line = json.loads(r.stdout.strip().splitlines()[-1])
     assert line["status"] == 0 and len(line["weights_per_row_and_head"]) == 2
     assert all(abs(x - 1.0) < 1e-4 for x in line["weights_per_row_and_head"])
+
+
+# ---------------------------------------------------------------- captured, empty, and first calls
+def test_weights_victims_and_release_in_a_replayed_graph():
+    # one graph of a step's calls, the weights' workspace taken while it is captured, replayed over growing contexts
+    B, n, C = 2, 300, 64
+    g = torch.Generator().manual_seed(4)
+    host = torch.randn((B * n, 576), generator=g).to(torch.bfloat16).pin_memory()
+    off = torch.arange(B + 1, device=dev) * n
+    q = torch.randn((B, 128, 576), generator=g).to(torch.bfloat16).to(dev)
+    row_off = torch.arange(B + 1, device=dev)
+
+    def state():
+        cache = L.LayerCache(B, B * n, C, host)
+        end = off[:-1] + 200
+        st = torch.zeros(1, dtype=torch.int32, device=dev)
+        sel = torch.stack([torch.arange(b, 2 * C, 2) for b in range(B)]).to(torch.int32).to(dev)
+        L.cache_step(off, B * n, sel, cache, torch.empty((B, C), dtype=torch.int32, device=dev), st, tok_end=end)
+        i = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)
+        return dict(cache=cache, end=end, st=st, mass=torch.zeros(B * n, device=dev), et=i(B, C), es=i(B, C), ec=i(B),
+                    lse=torch.zeros((B, 128), device=dev), out=torch.zeros((B, 128, 512), dtype=torch.bfloat16, device=dev),
+                    ws=torch.empty(L.mla_chunk_workspace_size(B, 128, B), dtype=torch.uint8, device=dev),
+                    pages=L.KVPages.of_cache(cache))
+
+    def step(s):
+        L.mla_chunk(row_off, q, off, B * n, s["pages"], 0.07, s["out"], s["lse"], s["ws"], s["st"], tok_end=s["end"])
+        L.mla_mass(row_off, q, s["lse"], off, B * n, s["pages"], 0.07, s["mass"], s["mass"], s["st"], decay=0.9, tok_end=s["end"])
+        L.evict_select(off, B * n, s["cache"].slot2tok, s["mass"], 10, s["et"], s["es"], s["ec"], s["st"], sinks=2, recent=3,
+                       tok_end=s["end"], freebits=s["cache"].freebits)
+        L.cache_release(off, B * n, s["et"], s["cache"], s["st"], mass=s["mass"], tok_end=s["end"])
+        s["end"] += 1
+    a, b = state(), state()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(b)
+    junk = [torch.full((1 << 20,), 255, dtype=torch.uint8, device=dev) for _ in range(8)]  # not in the graph's pool
+    for _ in range(3):
+        step(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in ("mass", "et", "es", "ec", "lse", "end"):
+            assert torch.equal(a[k], b[k]), k
+        assert torch.equal(a["out"], b["out"]) and torch.equal(a["cache"].slot2tok, b["cache"].slot2tok)
+        assert int(a["st"].item()) == 0 and int(b["st"].item()) == 0
+    assert int((a["cache"].slot2tok >= 0).sum()) == 2 * 10 and len(junk) == 8
+
+
+def test_calls_without_rows_or_tokens():
+    off, st = torch.tensor([0, 40, 90], device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    pages = L.KVPages(torch.arange(6, dtype=torch.int32, device=dev), torch.ones((96, 576), dtype=torch.bfloat16, device=dev), 16)
+    none = torch.zeros(3, dtype=torch.int64, device=dev)
+    q, lse = torch.empty((0, 16, 576), dtype=torch.bfloat16, device=dev), torch.empty((0, 16), device=dev)
+    mass = torch.rand(90, device=dev)
+    out = torch.full((90,), 5.0, device=dev)
+    L.mla_mass(none, q, lse, off, 90, pages, 0.1, mass, out, st, decay=0.5, tok_end=torch.tensor([30, 90], device=dev))
+    want = mass * 0.5
+    want[30:40] = 5.0
+    assert torch.equal(out, want) and int(st.item()) == 0
+    ws = torch.empty(L.mla_chunk_workspace_size(0, 16, 2), dtype=torch.uint8, device=dev)
+    L.mla_chunk(none, q, off, 90, pages, 0.1, torch.empty((0, 16, 512), dtype=torch.bfloat16, device=dev), lse, ws, st)
+    # requests without tokens: nothing to weigh or to evict
+    zero, empty = torch.zeros(3, dtype=torch.int64, device=dev), torch.empty(0, device=dev)
+    L.mla_mass(none, q, lse, zero, 0, L.KVPages(torch.empty(0, dtype=torch.int32, device=dev), pages.kv, 16), 0.1, empty, empty, st)
+    i = torch.full((2, 32), 3, dtype=torch.int32, device=dev)
+    cnt = torch.full((2,), 3, dtype=torch.int32, device=dev)
+    L.evict_select(zero, 0, torch.full_like(i, -1), empty, 0, i, i.clone(), cnt, st)
+    assert torch.all(i == -1) and torch.all(cnt == 0) and int(st.item()) == 0
+
+
+def test_a_process_may_capture_its_first_call():
+    import subprocess
+    import sys
+    code = """
+import torch
+from sparse_attention_kv_echo_gb300 import _lib as L
+dev = "cuda"
+L.load()
+off, rows = torch.tensor([0, 500], device=dev), torch.tensor([0, 40], device=dev)
+q = torch.randn((40, 128, 576), device=dev).to(torch.bfloat16)
+pages = L.KVPages(torch.arange(32, dtype=torch.int32, device=dev), torch.randn((512, 576), device=dev).to(torch.bfloat16), 16)
+out, lse = torch.zeros((40, 128, 512), dtype=torch.bfloat16, device=dev), torch.zeros((40, 128), device=dev)
+ws = torch.zeros(L.mla_chunk_workspace_size(40, 128, 1), dtype=torch.uint8, device=dev)
+mass, st = torch.zeros(500, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+s2t = torch.arange(64, dtype=torch.int32, device=dev)[None].contiguous()
+et, es, ec = torch.zeros_like(s2t), torch.zeros_like(s2t), torch.zeros(1, dtype=torch.int32, device=dev)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    L.mla_chunk(rows, q, off, 500, pages, 0.07, out, lse, ws, st)
+    L.mla_mass(rows, q, lse, off, 500, pages, 0.07, mass, mass, st, decay=0.0)
+    L.evict_select(off, 500, s2t, mass, 10, et, es, ec, st)
+g.replay()
+torch.cuda.synchronize()
+assert int(st.item()) == 0 and int(ec.item()) == 54 and abs(float(mass.sum()) - 40 * 128) < 1, (st, ec, mass.sum())
+print("captured")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-1500:]
