@@ -401,8 +401,8 @@ class KVPages:
     there.  Keeps the tensors alive; the table may change between calls, in place."""
 
     def __init__(self, page_tab: torch.Tensor, kv: torch.Tensor, page: int, req_rows: int = 0):
-        if page < 1 or req_rows < 0:
-            raise ValueError("KVPages: page >= 1 and req_rows >= 0")
+        if not 1 <= page < 2 ** 31 or not 0 <= req_rows < 2 ** 63:  # what the struct's fields hold
+            raise ValueError("KVPages: 1 <= page < 2^31 and 0 <= req_rows < 2^63")
         _expect("KVPages", torch.cuda.current_device(), ("page_tab", page_tab, torch.int32, (page_tab.numel(),)),
                 ("kv", kv, torch.bfloat16, (kv.shape[0], MLA_DQK)))
         self.page_tab, self.kv, self.page, self.req_rows = page_tab, kv, int(page), int(req_rows)
@@ -414,7 +414,8 @@ class KVPages:
 
     @classmethod
     def of_cache(cls, cache: "LayerCache") -> "KVPages":
-        """The slots of a LayerCache as pages of one row (a token that is not resident has no row)."""
+        """The slots of a LayerCache as pages of one row (a token that is not resident has no row; under lazy
+        reuse one that was freed has its row until its slot is handed out)."""
         return cls(cache.tok2slot, cache.dev_kv, 1, cache.C)
 
 
@@ -489,7 +490,7 @@ def evict_select(tok_off, n_tokens, slot2tok, mass, keep, evict_tok, evict_slot,
     freebits: the cache's free bits (a LayerCache's, or a slice of them); a cache under lazy reuse needs them, as
     its free slots keep their tokens."""
     B = tok_off.shape[0] - 1
-    C = slot2tok.numel() // B
+    C = slot2tok.numel() // max(B, 1)
     dev = torch.cuda.current_device()
     _expect("evict_select", dev, ("tok_off", tok_off, torch.int64, (B + 1,)),
             ("slot2tok", slot2tok, torch.int32, (B * C,) if slot2tok.dim() == 1 else (B, C)),

@@ -104,3 +104,17 @@ def test_victims_refuse_free_bits_of_another_size(host, words):
     with pytest.raises(ValueError):
         L.evict_select(torch.tensor([0, 10]), 10, i, torch.zeros(10), 1, i, i, i[0, :1], i[0, :1],
                        freebits=torch.zeros(words, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("page,req_rows", [(0, 0), (-1, 0), (2 ** 31, 0), (2 ** 32 + 16, 0), (16, -1), (16, 2 ** 64 + 1)])
+def test_pages_refuse_sizes_the_struct_does_not_hold(host, page, req_rows):
+    tab, kv = torch.zeros(1, dtype=torch.int32), torch.zeros((16, 576), dtype=torch.bfloat16)
+    L.KVPages(tab, kv, 2 ** 31 - 1, 0)
+    with pytest.raises(ValueError):
+        L.KVPages(tab, kv, page, req_rows)
+
+
+def test_victims_of_no_requests_are_refused_by_the_library(host):
+    i = torch.zeros((0, 64), dtype=torch.int32)
+    with pytest.raises(ValueError):      # (no ZeroDivisionError: the tables fit no request)
+        L.evict_select(torch.tensor([0]), 10, torch.zeros(64, dtype=torch.int32), torch.zeros(10), 1, i, i, i[:, 0], i[:, 0])
