@@ -639,6 +639,173 @@ int echo_evict_select(int B, const int64_t* tok_off, const int64_t* tok_end, int
                       echo_stream_t stream);
 
 /*
+ * Speculative decoding over a paged cache.  A request's new rows are the nodes of a
+ * tree of drafted tokens: node 0 is the last committed token, parent [n_rows] int32
+ * gives each node's parent, 0 <= parent < the node's own index within its request
+ * (-1: none, as node 0).  The nodes' cache rows are the last of the context, node i at
+ * token len_b - n_b + i whatever its depth.  A step: echo_tree_masks, echo_mla_tree in
+ * every layer, echo_draft_verify, echo_rows_keep, echo_pages_free, and echo_pages_reserve
+ * for the next tree.
+ *
+ * echo_tree_masks: bit j % 32 of word j / 32 of mask [n_rows,words] u32 (device) is set
+ * for row i of a request when node j is node i or one of its ancestors; depth [n_rows]
+ * int32 (may be NULL) counts the ancestors, so node i stands at position len_b - n_b +
+ * depth.  A parent out of range counts as none and sets ECHO_ST_BADDATA; so does a
+ * request of more than 32 * words rows, whose masks and depths are zero.  1 <= words <=
+ * ECHO_TREE_MAX_WORDS.  Rows outside every request are left as they were.
+ * Errors: ECHO_EINVAL, ECHO_EUNSUPPORTED (B, n_rows or words too large), ECHO_ECUDA.
+ */
+#define ECHO_TREE_MAX_WORDS 32               /* 1024 nodes a tree */
+#define ECHO_TREE_MAX_NODES (32 * ECHO_TREE_MAX_WORDS)
+int echo_tree_masks(int B, const int64_t* row_off, int64_t n_rows, const int32_t* parent, int words, uint32_t* mask,
+                    int32_t* depth, int32_t* status, echo_stream_t stream);
+
+/*
+ * Attention of trees: echo_mla_chunk where row i of request b, at token p = len_b - n_b +
+ * i, sees the tokens t < len_b - n_b (the context before the tree) and, of the tree's own
+ * tokens len_b - n_b + j, those with j <= i whose bit j is set in the row's mask (any
+ * bits, not ancestors alone: a row without its own bit does not see itself).  Tokens
+ * without a cache row are not seen; a row that sees nothing has out = 0 and lse = -inf.
+ * mask [n_rows,words] u32, device.  The rows of a request with more than 32 * words see
+ * nothing and set ECHO_ST_BADDATA.  The other arguments, the workspace (echo_mla_chunk_workspace_size)
+ * and the errors as echo_mla_chunk; words < 1 or no mask: ECHO_EINVAL, words >
+ * ECHO_TREE_MAX_WORDS: ECHO_EUNSUPPORTED.
+ */
+int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q, const uint32_t* mask,
+                  int words, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_pages* pages,
+                  float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes, int32_t* status,
+                  echo_stream_t stream);
+
+/*
+ * Verification of drafted tokens.  token [n_rows] int32 is each node's token; row i of
+ * target [n_rows,vocab] holds the target's probabilities of the token behind node i, row
+ * i of draft those that node i's children were drawn from, independently of each other.
+ * The walk starts at node 0.  At node v, with left = target[v] and R = 1, its children c
+ * are tried in the order of their indices: with x = token[c] and d = draft[v] (draft NULL:
+ * d[x] = 1, else 0: a draft that is not drawn),
+ *   u_node[c] * d[x] * R < left[x]: c is accepted, the walk goes on at c;
+ *   else left becomes max(0, left - R * d) and R its sum (unless that is 0: both stay).
+ * When no child is left, the token behind the path is the first y with
+ *   left[0] + .. + left[y] > u_pick[b] * (left[0] + .. + left[vocab - 1]).
+ * With u_node [n_rows] and u_pick [B] independent and uniform in [0, 1) the accepted tokens
+ * and the one behind them are distributed as the target's own.  u_node and u_pick
+ * NULL: greedy; target may then hold logits, draft is not read, a child is accepted
+ * when its token is the first of target[v]'s largest, and that is the token behind the path.
+ *   path [n_rows] int32: the accepted nodes of request b in order from row_off[b] on
+ *     (node 0 first), -1 behind; count [B] int32: how many (>= 1 with rows, else 0);
+ *     next [B] int32: the token behind the path (-1 without rows).
+ *   dtype ECHO_F32 or ECHO_BF16, of target and draft both (16-byte aligned).
+ * The sums are exact to 2^-60 a value (64-bit integers), so equal inputs give equal
+ * results on any launch, and a test falls on the right side of its border unless it is
+ * within 2^-48 of it.  Probabilities are to be in [0, 1] with a sum of at most 8: NaN and
+ * values outside [0, 2] count as 0 and 2 and set ECHO_ST_NAN; a row that is 0 throughout
+ * gives token 0 and ECHO_ST_BADDATA; uniform numbers outside [0, 1) (or NaN) count as the
+ * nearest in it.  Greedy: NaN is below every number and sets ECHO_ST_NAN.  A node
+ * whose token is not in [0, vocab) is not accepted and changes nothing (when it is tried:
+ * ECHO_ST_BADDATA); a request of more than ECHO_TREE_MAX_NODES rows or with inconsistent row
+ * bounds has count 0 and next -1, and sets ECHO_ST_BADDATA.  Nodes whose parent is out of range are never
+ * reached.  Which rows of target and draft are read whole: those of nodes with a rejection,
+ * and of the last.
+ * Errors: ECHO_EINVAL (sizes, NULL or misaligned pointers, one of u_node and u_pick),
+ * ECHO_EUNSUPPORTED (B, n_rows, vocab > ECHO_MAX_VOCAB, dtype), ECHO_ECUDA.
+ */
+#define ECHO_F32 0
+#define ECHO_BF16 1
+#define ECHO_MAX_VOCAB (1 << 24)
+int echo_draft_verify(int B, const int64_t* row_off, int64_t n_rows, const int32_t* parent, const int32_t* token,
+                      int64_t vocab, int dtype, const void* target, const void* draft, const float* u_node,
+                      const float* u_pick, int32_t* path, int32_t* count, int32_t* next, int32_t* status,
+                      echo_stream_t stream);
+
+/*
+ * The pages of a paged cache while requests come, branch, grow and go.  refs
+ * [n_pages] int32 counts, for each page, the table entries that name it; 0: free.
+ * Layer l's rows are kv + l * layer_bytes, n_pages * page rows of row_bytes each (a
+ * multiple of 16); every layer shares the table, so a page is one of each layer.
+ * An empty pool: page_tab all -1, refs all 0.  kv with kv_rows = n_pages * page,
+ * page_tab, page and req_rows = 0 are the echo_pages of a layer.
+ * Here tok_off[b] must be a multiple of page, so that each entry belongs to one
+ * request (else, or with inconsistent bounds, the request is left as it was and
+ * ECHO_ST_BADDATA set); tok_end [B] is required where it is an argument.  Table entries that name no page of the
+ * pool, and counts that would fall below 0, set ECHO_ST_BADDATA.
+ * All of them: one call at a time on a pool (the calls read and write its table and
+ * counts); equal inputs give equal tables, whatever the launch.  ws:
+ * echo_pages_workspace_size(B, n_pages) bytes, 256-byte aligned, B being the requests or pairs of the call; contents need not be kept.
+ * Errors: ECHO_EINVAL (sizes, NULL or misaligned pointers, a small workspace),
+ * ECHO_EUNSUPPORTED (B > ECHO_MAX_REQUESTS, n_pages > ECHO_POOL_MAX_PAGES), ECHO_ECUDA.
+ */
+typedef struct echo_page_pool {
+    int32_t* page_tab;
+    int32_t* refs;
+    void* kv;
+    int64_t n_pages;
+    int64_t row_bytes;
+    int64_t layer_bytes;
+    int32_t layers;
+    int32_t page;
+} echo_page_pool;
+
+#define ECHO_POOL_MAX_PAGES (1 << 24)
+size_t echo_pages_workspace_size(int B, int64_t n_pages);
+
+/*
+ * Pages for the tokens [tok_end[b], want[b]) of every request, to be written by the
+ * caller: entries of those tokens without a page take the lowest free pages, in the order of
+ * requests and entries.  A page of theirs that other entries name too is
+ * replaced by a free one (copy on write; the rows before tok_end[b] are copied to it).  A
+ * request is served whole or not at all: when the free pages do not reach, it and
+ * those after it that need any are left as they were, and ECHO_ST_FULL is set.  room [B] int64 (may be
+ * NULL): want[b] when served, else tok_end[b].  tok_end[b] <= want[b] <=
+ * tok_off[b+1], and a request whose last page is partly used must have that page (else ECHO_ST_BADDATA; not served).
+ * The caller sets tok_end when it has the rows.
+ */
+int echo_pages_reserve(int B, const int64_t* tok_off, const int64_t* tok_end, const int64_t* want, int64_t n_tokens,
+                       const echo_page_pool* pool, int64_t* room, void* ws, size_t ws_bytes, int32_t* status,
+                       echo_stream_t stream);
+
+/*
+ * Gives up the pages behind every request's end: entries whose first token is at or past
+ * tok_end[b] become -1, and their pages' counts fall (tok_end[b] = tok_off[b]: the request's
+ * all).  The bytes stay.
+ */
+int echo_pages_free(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_page_pool* pool,
+                    int32_t* status, echo_stream_t stream);
+
+/*
+ * Forks: for each pair i < n, request dst[i] gives up what it holds and gets the context of
+ * request src[i] (requests of the B that tok_off and tok_end describe): its full pages shared,
+ * the rows of a partly used last page copied to the lowest free one (in the order of the
+ * pairs), and tok_end[dst[i]] set to its length.  No page for the last rows: the context ends with its
+ * last full page, and ECHO_ST_FULL is set.  Several pairs may have one src.  A pair with
+ * src or dst out of range or equal, a dst that an earlier pair has, that is some pair's src, or whose
+ * region is shorter than the context is left out and sets ECHO_ST_BADDATA.  n <= ECHO_MAX_REQUESTS; ws for n.
+ */
+int echo_pages_fork(int n, const int32_t* src, const int32_t* dst, int B, const int64_t* tok_off, int64_t* tok_end,
+                    int64_t n_tokens, const echo_page_pool* pool, void* ws, size_t ws_bytes, int32_t* status,
+                    echo_stream_t stream);
+
+/*
+ * Closes the pool up: with U pages in use, those at or behind place U move, ascending, to the
+ * free ones before it, ascending; rows of every layer, counts and the entries of
+ * page_tab [ceil(n_tokens / page)] follow.  used [1] int32 = U.  ws for B = 1.
+ */
+int echo_pages_compact(int64_t n_tokens, const echo_page_pool* pool, int32_t* used, void* ws, size_t ws_bytes,
+                       int32_t* status, echo_stream_t stream);
+
+/*
+ * Keeps the accepted path of each request's tree: with base = tok_end[b] - n_b (n_b its rows,
+ * row_off), the cache rows of the tokens base + path[row_off[b] + i] move to the
+ * tokens base + i, i < count[b], in every layer, and new_end[b] = base + count[b]
+ * (new_end [B] int64, another array than tok_end).  path and count as echo_draft_verify writes them: ascending.
+ * Enqueue echo_pages_free with new_end for the pages of the rejected rows.  A path
+ * that does not ascend or leaves the tree, a count beyond n_b, more rows than tokens, a token without a page or one
+ * whose page others name too: the request is left as it was, new_end[b] = tok_end[b], ECHO_ST_BADDATA.
+ */
+int echo_rows_keep(int B, const int64_t* row_off, int64_t n_rows, const int32_t* path, const int32_t* count,
+                   const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_page_pool* pool,
+                   int64_t* new_end, int32_t* status, echo_stream_t stream);
+
+/*
  * Releases tokens from the cache: for each entry of tok [B,m] int32 (request-local,
  * -1 padding; evict_tok with m = C is such a list) that is resident, its two
  * table entries become -1, its slot's free bit is set and, with mass (may be

@@ -25,16 +25,21 @@ HEADS, DIM, MAX_REQUESTS = 64, 128, 4096
 CACHE_HOLD_EARLY, CACHE_LAZY = 1, 2   # echo_cache_step flags
 TOPK_CACHED_MAX_SLOTS = 32768  # C limit of echo_topk_select_cached and of the cached form of echo_topk_select_cands
 CAND_CAP = 16384             # candidate-list entries per request top-k keeps in shared memory
+TREE_MAX_WORDS, TREE_MAX_NODES = 32, 1024   # words of a tree's masks, its nodes
+DTYPE_F32, DTYPE_BF16, MAX_VOCAB = 0, 1, 1 << 24   # echo_draft_verify
+POOL_MAX_PAGES = 1 << 24
 EARLY_FETCH_BLOCKS = 24      # CTAs of the early-fetch and late-recall kernels
 
 EXPORTS = ("echo_above_words", "echo_append_tokens", "echo_cache_release", "echo_cache_step", "echo_cache_step_resolved",
-           "echo_debug_stall_epilogue", "echo_debug_wait_limit", "echo_device_sm_count",
+           "echo_debug_stall_epilogue", "echo_debug_wait_limit", "echo_device_sm_count", "echo_draft_verify",
            "echo_early_fetch", "echo_evict_select", "echo_evict_select_resident", "echo_host_device_alias", "echo_index_scores", "echo_index_scores_cands", "echo_mla_chunk",
            "echo_mla_chunk_workspace_size", "echo_mla_decode", "echo_mla_mass",
-           "echo_mla_mass_workspace_size", "echo_pool_above", "echo_pool_select",
+           "echo_mla_mass_workspace_size", "echo_mla_tree", "echo_pages_compact", "echo_pages_fork", "echo_pages_free",
+           "echo_pages_reserve", "echo_pages_workspace_size", "echo_pool_above", "echo_pool_select", "echo_rows_keep",
            "echo_pool_slots", "echo_prefill_block",
            "echo_prefill_block_static", "echo_prefill_scores", "echo_prefill_workspace_size", "echo_quantize_q", "echo_seed_early",
-           "echo_topk_select", "echo_topk_select_cached", "echo_topk_select_cands")
+           "echo_topk_select", "echo_topk_select_cached", "echo_topk_select_cands",
+           "echo_tree_masks")
 
 _vp = ctypes.c_void_p
 
@@ -54,6 +59,11 @@ class EchoCandsStruct(ctypes.Structure):
 class EchoPagesStruct(ctypes.Structure):
     _fields_ = [("page_tab", _vp), ("kv", _vp), ("kv_rows", ctypes.c_int64), ("req_rows", ctypes.c_int64),
                 ("page", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class EchoPagePoolStruct(ctypes.Structure):
+    _fields_ = [("page_tab", _vp), ("refs", _vp), ("kv", _vp), ("n_pages", ctypes.c_int64), ("row_bytes", ctypes.c_int64),
+                ("layer_bytes", ctypes.c_int64), ("layers", ctypes.c_int32), ("page", ctypes.c_int32)]
 
 
 class EchoError(RuntimeError):
@@ -118,6 +128,26 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                                     _vp, ctypes.c_size_t, _vp, _vp]
         L.echo_mla_mass_workspace_size.restype = ctypes.c_size_t
         L.echo_mla_mass_workspace_size.argtypes = [i64, i32]
+        L.echo_tree_masks.restype = i32
+        L.echo_tree_masks.argtypes = [i32, _vp, i64, _vp, i32, _vp, _vp, _vp, _vp]
+        L.echo_mla_tree.restype = i32
+        L.echo_mla_tree.argtypes = [i32, _vp, i64, i32, _vp, _vp, i32, _vp, _vp, i64, pages, f32, _vp, _vp, _vp,
+                                    ctypes.c_size_t, _vp, _vp]
+        L.echo_draft_verify.restype = i32
+        L.echo_draft_verify.argtypes = [i32, _vp, i64, _vp, _vp, i64, i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+        pool = ctypes.POINTER(EchoPagePoolStruct)
+        L.echo_pages_workspace_size.restype = ctypes.c_size_t
+        L.echo_pages_workspace_size.argtypes = [i32, i64]
+        L.echo_pages_reserve.restype = i32
+        L.echo_pages_reserve.argtypes = [i32, _vp, _vp, _vp, i64, pool, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+        L.echo_pages_free.restype = i32
+        L.echo_pages_free.argtypes = [i32, _vp, _vp, i64, pool, _vp, _vp]
+        L.echo_pages_fork.restype = i32
+        L.echo_pages_fork.argtypes = [i32, _vp, _vp, i32, _vp, _vp, i64, pool, _vp, ctypes.c_size_t, _vp, _vp]
+        L.echo_pages_compact.restype = i32
+        L.echo_pages_compact.argtypes = [i64, pool, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+        L.echo_rows_keep.restype = i32
+        L.echo_rows_keep.argtypes = [i32, _vp, i64, _vp, _vp, _vp, _vp, i64, pool, _vp, _vp, _vp]
         L.echo_evict_select.restype = i32
         L.echo_evict_select.argtypes = [i32, _vp, _vp, i64, _vp, i32, _vp, i64, i64, i64, _vp, _vp, _vp, _vp, _vp]
         L.echo_evict_select_resident.restype = i32
@@ -480,6 +510,155 @@ def mla_mass(row_off, q, lse, tok_off, n_tokens, pages, scale, mass, mass_out, s
         B, _ptr(row_off), n, heads, _ptr(q), _ptr(lse), _ptr(tok_off), _ptr(tok_end), int(n_tokens),
         ctypes.byref(pages.struct), int(window), int(sinks), float(scale), _ptr(mass), _ptr(mass_out), float(decay),
         _ptr(ws), ws.numel(), _ptr(status), _stream(stream)))
+
+
+def tree_masks(row_off, parent, mask, status, depth=None, stream=None):
+    """echo_tree_masks: the ancestors of every node of the requests' draft trees.  parent [n] int32 (request-local,
+    -1: none) -> mask [n,words] int32, a bit for each node of the request, depth [n] int32 (or None)."""
+    B, n, words = row_off.shape[0] - 1, parent.shape[0], mask.shape[-1]
+    dev = torch.cuda.current_device()
+    _expect("tree_masks", dev, ("row_off", row_off, torch.int64, (B + 1,)), ("parent", parent, torch.int32, (n,)),
+            ("mask", mask, torch.int32, (n, words)), ("status", status, torch.int32, (1,)))
+    if depth is not None:
+        _expect("tree_masks", dev, ("depth", depth, torch.int32, (n,)))
+    _check("echo_tree_masks", load().echo_tree_masks(B, _ptr(row_off), n, _ptr(parent), words, _ptr(mask), _ptr(depth),
+                                                     _ptr(status), _stream(stream)))
+
+
+def mla_tree(row_off, q, mask, tok_off, n_tokens, pages, scale, out, lse, ws, status, tok_end=None, stream=None):
+    """echo_mla_tree: mla_chunk where a request's new rows are the nodes of a draft tree: each sees the whole context
+    before the tree and, of the tree, the nodes up to itself whose bit its row of mask [n,words] int32 has
+    (tree_masks).  ws as mla_chunk's."""
+    words = mask.shape[-1]
+    B, n, heads = _check_chunk("mla_tree", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end,
+                               ("out", out, torch.bfloat16, (q.shape[0], q.shape[1], MLA_DV)),
+                               ("mask", mask, torch.int32, (q.shape[0], words)), ("ws", ws, torch.uint8, (ws.numel(),)))
+    _check("echo_mla_tree", load().echo_mla_tree(
+        B, _ptr(row_off), n, heads, _ptr(q), _ptr(mask), words, _ptr(tok_off), _ptr(tok_end), int(n_tokens),
+        ctypes.byref(pages.struct), float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _ptr(status),
+        _stream(stream)))
+
+
+def draft_verify(row_off, parent, token, target, path, count, next_tok, status, draft=None, u_node=None, u_pick=None,
+                 stream=None):
+    """echo_draft_verify: the path of each request's draft tree that the target accepts, and the token behind it.
+    parent, token [n] int32; target [n,vocab] f32 or bf16: the target's probabilities behind each node; draft [n,vocab]
+    of the same type: those its children were drawn from (None: drafts without probabilities); u_node [n] and u_pick [B]
+    f32: uniform numbers in [0, 1) (both None: greedy, target may hold logits) -> path [n] int32 (accepted nodes from
+    row_off[b] on, -1 behind), count [B] int32, next_tok [B] int32."""
+    B, (n, vocab), dev = row_off.shape[0] - 1, target.shape, torch.cuda.current_device()
+    if target.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"draft_verify: target must be float32 or bfloat16, not {target.dtype}")
+    _expect("draft_verify", dev, ("row_off", row_off, torch.int64, (B + 1,)), ("parent", parent, torch.int32, (n,)),
+            ("token", token, torch.int32, (n,)), ("target", target, target.dtype, (n, vocab)),
+            ("path", path, torch.int32, (n,)), ("count", count, torch.int32, (B,)),
+            ("next_tok", next_tok, torch.int32, (B,)), ("status", status, torch.int32, (1,)))
+    if draft is not None:
+        _expect("draft_verify", dev, ("draft", draft, target.dtype, (n, vocab)))
+    if (u_node is None) != (u_pick is None):
+        raise ValueError("draft_verify: u_node and u_pick go together")
+    if u_node is not None:
+        _expect("draft_verify", dev, ("u_node", u_node, torch.float32, (n,)), ("u_pick", u_pick, torch.float32, (B,)))
+    _check("echo_draft_verify", load().echo_draft_verify(
+        B, _ptr(row_off), n, _ptr(parent), _ptr(token), vocab, DTYPE_F32 if target.dtype is torch.float32 else DTYPE_BF16,
+        _ptr(target), _ptr(draft), _ptr(u_node), _ptr(u_pick), _ptr(path), _ptr(count), _ptr(next_tok), _ptr(status),
+        _stream(stream)))
+
+
+class PagePool:
+    """The pages of a paged cache with the counts of who holds them (an echo_page_pool): page_tab [entries] int32 (as
+    KVPages'; -1: no page), refs [n_pages] int32 (0: free), kv [n_pages * page, 576] bf16, or [layers, n_pages * page, 576]
+    with one table for every layer.  An empty pool has page_tab all -1 and refs all 0.  Keeps the tensors alive."""
+
+    def __init__(self, page_tab: torch.Tensor, refs: torch.Tensor, kv: torch.Tensor, page: int):
+        if not 1 <= page < 2 ** 31:
+            raise ValueError("PagePool: 1 <= page < 2^31")
+        n = refs.numel()
+        shape = (n * page, MLA_DQK) if kv.dim() == 2 else (kv.shape[0], n * page, MLA_DQK)
+        _expect("PagePool", torch.cuda.current_device(), ("page_tab", page_tab, torch.int32, (page_tab.numel(),)),
+                ("refs", refs, torch.int32, (n,)), ("kv", kv, torch.bfloat16, shape))
+        self.page_tab, self.refs, self.kv, self.page, self.n_pages = page_tab, refs, kv, int(page), n
+        self.layers = 1 if kv.dim() == 2 else kv.shape[0]
+        self.tokens = page_tab.numel() * self.page
+        s = EchoPagePoolStruct()
+        s.page_tab, s.refs, s.kv, s.n_pages = _ptr(page_tab), _ptr(refs), _ptr(kv), n
+        s.row_bytes, s.layer_bytes, s.layers, s.page = 2 * MLA_DQK, 2 * MLA_DQK * n * self.page, self.layers, self.page
+        self.struct = s
+
+    def of_layer(self, layer: int = 0) -> "KVPages":
+        """The pages of a layer, for mla_chunk, mla_mass and mla_tree."""
+        return KVPages(self.page_tab, self.kv if self.kv.dim() == 2 else self.kv[layer], self.page)
+
+
+def pages_workspace_size(B: int, n_pages: int) -> int:
+    return int(load().echo_pages_workspace_size(int(B), int(n_pages)))
+
+
+def _check_pool(call, tok_off, n_tokens, pool, status, *more):
+    B, dev = tok_off.shape[0] - 1, torch.cuda.current_device()
+    _expect(call, dev, ("tok_off", tok_off, torch.int64, (B + 1,)), ("status", status, torch.int32, (1,)), *more)
+    if pool.tokens < n_tokens or pool.refs.get_device() != dev:
+        raise ValueError(f"{call}: the page table covers {pool.tokens} token rows, not {n_tokens}, or lies on another device")
+    return B
+
+
+def pages_reserve(tok_off, tok_end, want, n_tokens, pool, room, ws, status, stream=None):
+    """echo_pages_reserve: pages for the tokens [tok_end[b], want[b]) of every request (want [B] int64, token rows),
+    the lowest free ones; a page others hold too is replaced.  room [B] int64 (or None): want[b] where served, else
+    tok_end[b].  ws: uint8, pages_workspace_size(B, n_pages)."""
+    B = _check_pool("pages_reserve", tok_off, n_tokens, pool, status, ("ws", ws, torch.uint8, (ws.numel(),)))
+    per = [("tok_end", tok_end), ("want", want)] + ([("room", room)] if room is not None else [])
+    _expect("pages_reserve", torch.cuda.current_device(), *((name, t, torch.int64, (B,)) for name, t in per))
+    _check("echo_pages_reserve", load().echo_pages_reserve(
+        B, _ptr(tok_off), _ptr(tok_end), _ptr(want), int(n_tokens), ctypes.byref(pool.struct), _ptr(room), _ptr(ws),
+        ws.numel(), _ptr(status), _stream(stream)))
+
+
+def pages_free(tok_off, tok_end, n_tokens, pool, status, stream=None):
+    """echo_pages_free: gives up the pages behind every request's end (tok_end[b] = tok_off[b]: all of them)."""
+    B = _check_pool("pages_free", tok_off, n_tokens, pool, status)
+    _expect("pages_free", torch.cuda.current_device(), ("tok_end", tok_end, torch.int64, (B,)))
+    _check("echo_pages_free", load().echo_pages_free(B, _ptr(tok_off), _ptr(tok_end), int(n_tokens),
+                                                     ctypes.byref(pool.struct), _ptr(status), _stream(stream)))
+
+
+def pages_fork(src, dst, tok_off, tok_end, n_tokens, pool, ws, status, stream=None):
+    """echo_pages_fork: request dst[i] gives up its pages and gets the context of request src[i] (src, dst [m] int32):
+    full pages shared, the rows of a partly used last page copied, tok_end[dst[i]] set.  ws: uint8,
+    pages_workspace_size(m, n_pages)."""
+    m = src.numel()
+    B = _check_pool("pages_fork", tok_off, n_tokens, pool, status, ("src", src, torch.int32, (m,)),
+                    ("dst", dst, torch.int32, (m,)), ("ws", ws, torch.uint8, (ws.numel(),)))
+    _expect("pages_fork", torch.cuda.current_device(), ("tok_end", tok_end, torch.int64, (B,)))
+    _check("echo_pages_fork", load().echo_pages_fork(
+        m, _ptr(src), _ptr(dst), B, _ptr(tok_off), _ptr(tok_end), int(n_tokens), ctypes.byref(pool.struct), _ptr(ws),
+        ws.numel(), _ptr(status), _stream(stream)))
+
+
+def pages_compact(n_tokens, pool, used, ws, status, stream=None):
+    """echo_pages_compact: the pages in use move to the first places of the pool, their rows, counts and table entries
+    with them; used [1] int32: how many there are.  ws: uint8, pages_workspace_size(1, n_pages)."""
+    dev = torch.cuda.current_device()
+    _expect("pages_compact", dev, ("used", used, torch.int32, (1,)), ("ws", ws, torch.uint8, (ws.numel(),)),
+            ("status", status, torch.int32, (1,)))
+    if pool.tokens < n_tokens or pool.refs.get_device() != dev:
+        raise ValueError(f"pages_compact: the page table covers {pool.tokens} token rows, not {n_tokens}, or lies on "
+                         "another device")
+    _check("echo_pages_compact", load().echo_pages_compact(int(n_tokens), ctypes.byref(pool.struct), _ptr(used), _ptr(ws),
+                                                           ws.numel(), _ptr(status), _stream(stream)))
+
+
+def rows_keep(row_off, path, count, tok_off, tok_end, n_tokens, pool, new_end, status, stream=None):
+    """echo_rows_keep: the cache rows of the accepted nodes of each request's draft tree (path, count of
+    draft_verify) move together behind the context, in every layer; new_end [B] int64: where the contexts then end
+    (not tok_end itself).  pages_free(new_end) gives up the pages behind."""
+    B = _check_pool("rows_keep", tok_off, n_tokens, pool, status)
+    _expect("rows_keep", torch.cuda.current_device(), ("row_off", row_off, torch.int64, (B + 1,)),
+            ("path", path, torch.int32, (path.numel(),)), ("count", count, torch.int32, (B,)),
+            ("tok_end", tok_end, torch.int64, (B,)), ("new_end", new_end, torch.int64, (B,)))
+    _check("echo_rows_keep", load().echo_rows_keep(
+        B, _ptr(row_off), path.numel(), _ptr(path), _ptr(count), _ptr(tok_off), _ptr(tok_end), int(n_tokens),
+        ctypes.byref(pool.struct), _ptr(new_end), _ptr(status), _stream(stream)))
 
 
 def evict_select(tok_off, n_tokens, slot2tok, mass, keep, evict_tok, evict_slot, evict_cnt, status, sinks=0, recent=0,

@@ -33,6 +33,8 @@ struct ChunkArgs {
     int k;
     int64_t window;
     int64_t sinks;
+    const uint32_t* mask;  // [n_rows, words] the tree nodes each row sees (echo_mla_tree), null: no trees
+    int words;
     const uint16_t* q;
     float scale;
     uint64_t wait_ns;  // limit of the kernels' waits, from the last progress
@@ -73,6 +75,8 @@ inline ChunkArgs chunk_args(int B, const int64_t* row_off, int64_t n_rows, int h
     a.k = sel ? k : 0;
     a.window = window < kMaxLen ? window : kMaxLen;  // no context is longer: positions + window stay in 64 bits
     a.sinks = sinks;
+    a.mask = nullptr;
+    a.words = 0;
     a.q = q;
     a.scale = scale;
     a.wait_ns = wait_limit_ns();
@@ -82,7 +86,8 @@ inline ChunkArgs chunk_args(int B, const int64_t* row_off, int64_t n_rows, int h
 
 // Rows [r0, r0 + n) of request b, its token rows from off on and its length.
 // False: the row bounds are inconsistent (n = 0).  Inconsistent token bounds,
-// more rows than tokens, or more than kMaxLen tokens leave len = 0.
+// more rows than tokens or than the masks of trees have bits, or more than kMaxLen
+// tokens leave len = 0.
 __device__ __forceinline__ bool chunk_request(const ChunkArgs& a, int b, int64_t* r0, int64_t* n, int64_t* off,
                                               int64_t* len) {
     const int64_t lo = a.row_off[b], hi = a.row_off[b + 1];
@@ -98,7 +103,7 @@ __device__ __forceinline__ bool chunk_request(const ChunkArgs& a, int b, int64_t
         set_status(a.status, ECHO_ST_BADDATA);
         return false;
     }
-    if (hi > lo && (!ok || *len < *n || *len > kMaxLen)) {
+    if (hi > lo && (!ok || *len < *n || *len > kMaxLen || (a.mask && *n > 32ll * a.words))) {
         set_status(a.status, ECHO_ST_BADDATA);
         *len = 0;
     }

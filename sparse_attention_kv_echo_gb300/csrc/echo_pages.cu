@@ -1,0 +1,615 @@
+// echo_pages.cu -- the pages of a paged cache while requests come, branch, grow and go
+// (echo.h, echo_page_pool): reserve, free, fork, compact and the rows of an accepted path.
+//
+// The table and the counts are small and every order in which pages are handed out is
+// fixed, so one block plans (scans over requests, then over the counts) and names the rows
+// to move in a list; a grid moves them through all layers.  What bounds the plans is
+// latency, the moves the memory.
+#include "echo_common.cuh"
+#include "echo_paged.cuh"
+
+namespace echo {
+namespace {
+
+struct PoolArgs {
+    int32_t* tab;
+    int32_t* refs;
+    uint8_t* kv;
+    int64_t n_pages;
+    int64_t row_bytes;
+    int64_t layer_bytes;
+    int layers;
+    int page;
+    int64_t entries;  // of the table
+};
+
+// Rows [src, src + rows) of every layer go to dst.
+struct __align__(16) Move {
+    int64_t src;
+    int64_t dst;
+    int64_t rows;
+    int64_t reserved;
+};
+
+// The workspace: how many moves, the moves, and a list of pages.
+struct Work {
+    int32_t* moves;   // [1]
+    Move* move;       // [requests of the call]
+    int32_t* list;    // [n_pages]
+    int32_t* map;     // [n_pages]
+};
+
+struct WorkLayout {
+    size_t move, list, map, total;
+};
+inline WorkLayout work_layout(int B, int64_t n_pages) {
+    WorkLayout l;
+    l.move = 256;
+    l.list = round_up(l.move + static_cast<size_t>(B) * sizeof(Move), 256);
+    l.map = round_up(l.list + static_cast<size_t>(n_pages) * 4, 256);
+    l.total = round_up(l.map + static_cast<size_t>(n_pages) * 4, 256);
+    return l;
+}
+inline Work work_of(void* ws, int B, int64_t n_pages) {
+    const WorkLayout l = work_layout(B, n_pages);
+    uint8_t* const w = static_cast<uint8_t*>(ws);
+    return Work{reinterpret_cast<int32_t*>(w), reinterpret_cast<Move*>(w + l.move), reinterpret_cast<int32_t*>(w + l.list),
+                reinterpret_cast<int32_t*>(w + l.map)};
+}
+
+// Request b's token rows [off, end) of its region [off, last).  False: inconsistent, or not on a page's border.
+struct Region {
+    int64_t off, end, last;
+};
+__device__ __forceinline__ bool region_of(const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, int page, int b, Region* r) {
+    r->off = tok_off[b];
+    r->last = tok_off[b + 1];
+    r->end = tok_end[b];
+    return r->off >= 0 && r->last >= r->off && r->last <= n_tokens && r->end >= r->off && r->end <= r->last && r->off % page == 0;
+}
+__device__ __forceinline__ int64_t pages_to(int64_t tok, int page) { return (tok + page - 1) / page; }
+
+__device__ __forceinline__ bool in_pool(const PoolArgs& a, int32_t p) { return p >= 0 && p < a.n_pages; }
+
+// One entry less names page p.
+__device__ __forceinline__ void drop_ref(const PoolArgs& a, int32_t p, int32_t* status) {
+    if (!in_pool(a, p)) {
+        set_status(status, ECHO_ST_BADDATA);
+        return;
+    }
+    if (atomicSub(a.refs + p, 1) <= 0) {
+        atomicAdd(a.refs + p, 1);
+        set_status(status, ECHO_ST_BADDATA);
+    }
+}
+
+// ---------------------------------------------------------------- free
+constexpr int kFT = 256;
+
+__global__ void __launch_bounds__(kFT)
+    pages_free_kernel(PoolArgs a, const int64_t* __restrict__ tok_off, const int64_t* __restrict__ tok_end, int64_t n_tokens, int32_t* status) {
+    Region r;
+    if (!region_of(tok_off, tok_end, n_tokens, a.page, blockIdx.x, &r)) {
+        if (threadIdx.x == 0 && blockIdx.y == 0) set_status(status, ECHO_ST_BADDATA);
+        return;
+    }
+    const int64_t e1 = pages_to(r.last, a.page);
+    for (int64_t e = pages_to(r.end, a.page) + static_cast<int64_t>(blockIdx.y) * kFT + threadIdx.x; e < e1; e += static_cast<int64_t>(gridDim.y) * kFT) {
+        const int32_t p = a.tab[e];
+        if (p == -1) continue;
+        a.tab[e] = -1;
+        drop_ref(a, p, status);
+    }
+}
+
+// ---------------------------------------------------------------- the block that plans
+constexpr int kPlanT = 1024;
+
+// Lists the first `most` free pages, ascending; returns how many there are up to `most`.  A block together.
+__device__ __forceinline__ int64_t list_free(const PoolArgs& a, int64_t most, int32_t* list, uint32_t* scratch) {
+    int64_t found = 0;
+    for (int64_t p0 = 0; p0 < a.n_pages && found < most; p0 += 4 * kPlanT) {
+        const int64_t p = p0 + 4 * threadIdx.x;
+        bool is[4];
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            is[i] = p + i < a.n_pages && a.refs[p + i] == 0;
+            n += is[i];
+        }
+        uint32_t total;
+        int64_t at = found + block_exclusive_scan<kPlanT>(n, scratch, &total);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (is[i]) {
+                if (at < most) list[at] = static_cast<int32_t>(p + i);
+                ++at;
+            }
+        found += total;
+    }
+    __syncthreads();
+    return min(found, most);
+}
+
+// Whether entry e of a request that grows needs a page, and the page it has.
+__device__ __forceinline__ bool needs_page(const PoolArgs& a, int64_t e, bool* bad, int32_t* page) {
+    const int32_t p = a.tab[e];
+    *page = p;
+    if (p < 0) return true;
+    if (!in_pool(a, p)) {
+        *bad = true;
+        return false;
+    }
+    const int32_t r = a.refs[p];
+    *bad |= r < 1;  // named, but counted free
+    return r > 1;
+}
+
+__global__ void __launch_bounds__(kPlanT)
+    pages_reserve_kernel(PoolArgs a, int B, const int64_t* __restrict__ tok_off, const int64_t* __restrict__ tok_end,
+                         const int64_t* __restrict__ want, int64_t n_tokens, int64_t* __restrict__ room, Work w, int32_t* status) {
+    __shared__ int64_t scratch64[kPlanT / 32];
+    __shared__ uint32_t scratch[kPlanT / 32 + 1];
+    __shared__ int32_t need[ECHO_MAX_REQUESTS];
+    __shared__ int s_moves, s_given;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) s_moves = s_given = 0;
+    // ---- how many pages every request needs, a warp to each; -1: none, it is inconsistent
+    for (int b = warp; b < B; b += kPlanT / 32) {
+        Region r;
+        const int64_t to = want[b];
+        bool ok = region_of(tok_off, tok_end, n_tokens, a.page, b, &r) && to >= r.end && to <= r.last;
+        int64_t n = 0;
+        if (ok && to > r.end) {
+            const int64_t e0 = r.end / a.page, e1 = pages_to(to, a.page);
+            bool bad = false;
+            for (int64_t base = e0; base < e1; base += 32) {
+                const int64_t e = base + lane;
+                int32_t p;
+                const bool it = e < e1 && needs_page(a, e, &bad, &p);
+                if (it && p < 0 && e == e0 && r.end % a.page) bad = true;  // its rows are nowhere
+                n += __popc(__ballot_sync(0xffffffffu, it));
+            }
+            ok = !__any_sync(0xffffffffu, bad);
+        }
+        if (lane == 0) {
+            need[b] = ok ? static_cast<int32_t>(min(n, static_cast<int64_t>(0x7FFFFFFF))) : -1;
+            if (!ok) set_status(status, ECHO_ST_BADDATA);
+        }
+    }
+    __syncthreads();
+    // ---- the free pages
+    int64_t mine = 0;
+    for (int b = tid; b < B; b += kPlanT) mine += max(need[b], 0);
+    int64_t total;
+    (void)block_scan64<kPlanT>(mine, scratch64, &total);
+    const int64_t most = min(total, a.n_pages);
+    const int64_t have = list_free(a, most, w.list, scratch);
+    // ---- where each request's begin, or that it goes without
+    int64_t base = 0;
+    bool full = false;
+    for (int b0 = 0; b0 < B; b0 += kPlanT) {
+        const int b = b0 + tid;
+        const int64_t n = b < B ? max(need[b], 0) : 0;
+        int64_t sum;
+        __syncthreads();
+        const int64_t at = base + block_scan64<kPlanT>(n, scratch64, &sum);
+        base += sum;
+        if (b < B) {
+            const bool served = need[b] >= 0 && (n == 0 || at + n <= have);
+            full |= need[b] >= 0 && !served;
+            if (room) room[b] = served ? want[b] : tok_end[b];
+            need[b] = served && n > 0 ? static_cast<int32_t>(at) : -1;
+            if (served && n > 0) atomicMax(&s_given, static_cast<int>(at + n));
+        }
+    }
+    if (full) set_status(status, ECHO_ST_FULL);
+    __syncthreads();
+    // ---- handed out; the counts of the pages replaced fall when all have been, since two requests may replace the same one
+    for (int b = warp; b < B; b += kPlanT / 32) {
+        int64_t at = need[b];
+        if (at < 0) continue;
+        Region r;
+        (void)region_of(tok_off, tok_end, n_tokens, a.page, b, &r);
+        const int64_t e0 = r.end / a.page, e1 = pages_to(want[b], a.page);
+        for (int64_t first = e0; first < e1; first += 32) {
+            const int64_t e = first + lane;
+            int32_t p = -1;
+            bool bad = false;
+            const bool it = e < e1 && needs_page(a, e, &bad, &p);
+            const uint32_t m = __ballot_sync(0xffffffffu, it);
+            if (it) {
+                const int64_t k = at + __popc(m & ((1u << lane) - 1u));
+                const int32_t to = w.list[k];
+                a.tab[e] = to;
+                a.refs[to] = 1;
+                w.map[k] = p;
+                if (p >= 0 && e == e0 && r.end % a.page)
+                    w.move[atomicAdd(&s_moves, 1)] = Move{static_cast<int64_t>(p) * a.page, static_cast<int64_t>(to) * a.page, r.end % a.page, 0};
+            }
+            at += __popc(m);
+        }
+    }
+    __syncthreads();
+    for (int k = tid; k < s_given; k += kPlanT)
+        if (w.map[k] >= 0) drop_ref(a, w.map[k], status);
+    if (tid == 0) *w.moves = s_moves;
+}
+
+// ---------------------------------------------------------------- fork
+struct ForkArgs {
+    int n;
+    const int32_t* src;
+    const int32_t* dst;
+    int B;
+    const int64_t* tok_off;
+    int64_t* tok_end;
+    int64_t n_tokens;
+};
+
+// Whether pair i may be forked; a block together.
+__device__ __forceinline__ bool fork_pair(const ForkArgs& f, int page, int i, Region* from, Region* to) {
+    const int s = f.src[i], d = f.dst[i];
+    bool ok = s >= 0 && s < f.B && d >= 0 && d < f.B;
+    bool clash = false;
+    for (int k = threadIdx.x; k < f.n; k += blockDim.x) clash |= (k < i && f.dst[k] == d) || f.src[k] == d;
+    clash = __syncthreads_or(clash);
+    if (!ok || clash) return false;
+    ok = region_of(f.tok_off, f.tok_end, f.n_tokens, page, s, from);
+    // (the end of dst is replaced, whatever it is)
+    to->off = f.tok_off[d];
+    to->last = f.tok_off[d + 1];
+    to->end = to->off;
+    return ok && to->off >= 0 && to->last >= to->off && to->last <= f.n_tokens && to->off % page == 0 && to->last - to->off >= from->end - from->off;
+}
+
+__global__ void __launch_bounds__(kFT) pages_share_kernel(PoolArgs a, ForkArgs f, Work w, int32_t* status) {
+    const int i = blockIdx.x;
+    Region from, to;
+    const bool ok = fork_pair(f, a.page, i, &from, &to);
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
+        w.map[i] = ok;
+        if (!ok) set_status(status, ECHO_ST_BADDATA);
+    }
+    if (!ok) return;
+    const int64_t full = (from.end - from.off) / a.page, entries = pages_to(to.last, a.page) - to.off / a.page;
+    const int32_t* const s = a.tab + from.off / a.page;
+    int32_t* const d = a.tab + to.off / a.page;
+    for (int64_t e = static_cast<int64_t>(blockIdx.y) * kFT + threadIdx.x; e < entries; e += static_cast<int64_t>(gridDim.y) * kFT) {
+        const int32_t old = d[e];
+        int32_t p = e < full ? s[e] : -1;
+        if (p >= 0 && !in_pool(a, p)) {
+            set_status(status, ECHO_ST_BADDATA);
+            p = -1;
+        }
+        if (old == p) continue;
+        if (p >= 0) atomicAdd(a.refs + p, 1);
+        if (old != -1) drop_ref(a, old, status);
+        d[e] = p < 0 ? -1 : p;
+    }
+}
+
+__global__ void __launch_bounds__(kPlanT) pages_tails_kernel(PoolArgs a, ForkArgs f, Work w, int32_t* status) {
+    __shared__ uint32_t scratch[kPlanT / 32 + 1];
+    const int tid = threadIdx.x;
+    pdl_wait();
+    uint32_t total = 0;
+    for (int i0 = 0; i0 < f.n; i0 += kPlanT) {
+        const int i = i0 + tid;
+        bool it = false;
+        if (i < f.n && w.map[i]) {
+            const int64_t off = f.tok_off[f.src[i]], n = f.tok_end[f.src[i]] - off;
+            it = n % a.page && in_pool(a, a.tab[off / a.page + n / a.page]);
+        }
+        uint32_t sum;
+        (void)block_exclusive_scan<kPlanT>(it, scratch, &sum);
+        total += sum;
+    }
+    const int64_t have = list_free(a, min(static_cast<int64_t>(total), a.n_pages), w.list, scratch);
+    uint32_t base = 0;
+    bool full = false, bad = false;
+    for (int i0 = 0; i0 < f.n; i0 += kPlanT) {
+        const int i = i0 + tid;
+        int64_t n = 0, rest = 0, off = 0, to_off = 0;
+        int32_t p = -1;
+        const bool ok = i < f.n && w.map[i];
+        if (ok) {
+            off = f.tok_off[f.src[i]];
+            n = f.tok_end[f.src[i]] - off;
+            rest = n % a.page;
+            to_off = f.tok_off[f.dst[i]];
+            if (rest) {
+                p = a.tab[off / a.page + n / a.page];
+                bad |= p >= 0 && !in_pool(a, p);
+            }
+        }
+        const bool it = in_pool(a, p);
+        uint32_t sum;
+        const uint32_t at = base + block_exclusive_scan<kPlanT>(it, scratch, &sum);
+        if (it) {
+            if (at < have) {
+                const int32_t to = w.list[at];
+                a.tab[to_off / a.page + n / a.page] = to;
+                a.refs[to] = 1;
+                w.move[at] = Move{static_cast<int64_t>(p) * a.page, static_cast<int64_t>(to) * a.page, rest, 0};
+            } else {
+                full = true;
+                n -= rest;
+            }
+        }
+        if (ok) f.tok_end[f.dst[i]] = to_off + n;
+        base += sum;
+    }
+    if (full) set_status(status, ECHO_ST_FULL);
+    if (bad) set_status(status, ECHO_ST_BADDATA);
+    if (tid == 0) *w.moves = static_cast<int32_t>(have);
+}
+
+// ---------------------------------------------------------------- compact
+// list[k]: the k-th free place before U; map[p]: where page p >= U goes (-1: it is free).
+__global__ void __launch_bounds__(kPlanT) pages_compact_kernel(PoolArgs a, int32_t* __restrict__ used, Work w) {
+    __shared__ uint32_t scratch[kPlanT / 32 + 1];
+    const int tid = threadIdx.x;
+    uint32_t mine = 0;
+    for (int64_t p = tid; p < a.n_pages; p += kPlanT) mine += a.refs[p] > 0;
+    uint32_t U;
+    (void)block_exclusive_scan<kPlanT>(mine, scratch, &U);
+    uint32_t holes = 0, far = 0;
+    for (int64_t p0 = 0; p0 < U; p0 += kPlanT) {
+        const int64_t p = p0 + tid;
+        const bool is = p < U && a.refs[p] <= 0;
+        uint32_t total;
+        const uint32_t at = holes + block_exclusive_scan<kPlanT>(is, scratch, &total);
+        if (is) w.list[at] = static_cast<int32_t>(p);
+        holes += total;
+    }
+    __syncthreads();
+    for (int64_t p0 = U; p0 < a.n_pages; p0 += kPlanT) {
+        const int64_t p = p0 + tid;
+        const int32_t r = p < a.n_pages ? a.refs[p] : 0;
+        uint32_t total;
+        const uint32_t at = far + block_exclusive_scan<kPlanT>(r > 0, scratch, &total);
+        if (p < a.n_pages) {
+            const int32_t to = r > 0 ? w.list[at] : -1;
+            w.map[p] = to;
+            if (r > 0) {
+                a.refs[to] = r;
+                a.refs[p] = 0;
+            }
+        }
+        far += total;
+    }
+    if (tid == 0) *used = static_cast<int32_t>(U);
+}
+
+constexpr int kMT = 256;
+
+__device__ __forceinline__ void move_bytes(const uint8_t* src, uint8_t* dst, int64_t bytes) {
+    for (int64_t i = threadIdx.x * 16ll; i < bytes; i += kMT * 16ll)
+        *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(src + i);
+}
+
+__global__ void __launch_bounds__(kMT) pages_place_kernel(PoolArgs a, const int32_t* __restrict__ used, Work w, int32_t* status) {
+    pdl_wait();
+    const int32_t U = *used;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * kMT + threadIdx.x; e < a.entries; e += static_cast<int64_t>(gridDim.x) * kMT) {
+        const int32_t p = a.tab[e];
+        if (p < U) continue;
+        const int32_t to = p < a.n_pages ? w.map[p] : -1;
+        if (to < 0) set_status(status, ECHO_ST_BADDATA);
+        else a.tab[e] = to;
+    }
+    const int64_t bytes = a.page * a.row_bytes, pages = a.n_pages - U;
+    for (int64_t u = blockIdx.x; u < pages * a.layers; u += gridDim.x) {
+        const int64_t l = u / pages, p = U + u % pages;
+        const int32_t to = w.map[p];
+        if (to < 0) continue;
+        uint8_t* const kv = a.kv + l * a.layer_bytes;
+        move_bytes(kv + p * bytes, kv + to * bytes, bytes);
+    }
+}
+
+// ---------------------------------------------------------------- moves
+__global__ void __launch_bounds__(kMT) pages_move_kernel(PoolArgs a, Work w) {
+    pdl_wait();
+    const int64_t n = *w.moves;
+    for (int64_t u = blockIdx.x; u < n * a.layers; u += gridDim.x) {
+        const Move m = w.move[u % n];
+        uint8_t* const kv = a.kv + u / n * a.layer_bytes;
+        move_bytes(kv + m.src * a.row_bytes, kv + m.dst * a.row_bytes, m.rows * a.row_bytes);
+    }
+}
+
+// ---------------------------------------------------------------- the rows of an accepted path
+constexpr int kKT = 288;
+constexpr int kBatch = 64;
+
+// A thread has one 16-byte column of some layers and takes the path's rows in order: the path ascends, so
+// a row is read before a later one is written over it.
+__global__ void __launch_bounds__(kKT)
+    rows_keep_kernel(PoolArgs a, const int64_t* __restrict__ row_off, int64_t n_rows, const int32_t* __restrict__ path,
+                     const int32_t* __restrict__ count, const int64_t* __restrict__ tok_off, const int64_t* __restrict__ tok_end,
+                     int64_t n_tokens, int64_t* __restrict__ new_end, int32_t* status) {
+    __shared__ int64_t from[kBatch], to[kBatch];
+    const int b = blockIdx.x, tid = threadIdx.x;
+    const int64_t r0 = row_off[b], r1 = row_off[b + 1];
+    const int64_t c = count[b];
+    Region r;
+    bool ok = region_of(tok_off, tok_end, n_tokens, a.page, b, &r) && r0 >= 0 && r1 >= r0 && r1 <= n_rows && r1 - r0 <= r.end - r.off &&
+              c >= 0 && c <= r1 - r0;
+    const int64_t n = r1 - r0, base = r.end - n;
+    const auto row_of = [&](int64_t tok, bool* bad, bool whole) {
+        const int32_t p = a.tab[tok / a.page];
+        if (!in_pool(a, p) || (whole && a.refs[p] != 1)) {
+            *bad = true;
+            return static_cast<int64_t>(0);
+        }
+        return static_cast<int64_t>(p) * a.page + tok % a.page;
+    };
+    if (ok) {
+        bool bad = false;
+        for (int64_t i = tid; i < c; i += kKT) {
+            const int64_t x = path[r0 + i], before = i > 0 ? path[r0 + i - 1] : -1;
+            if (x <= before || x >= n) {
+                bad = true;
+            } else if (x != i) {
+                (void)row_of(base + x, &bad, false);
+                (void)row_of(base + i, &bad, true);
+            }
+        }
+        ok = !__syncthreads_or(bad);
+    }
+    if (tid == 0 && blockIdx.y == 0) {
+        if (!ok) set_status(status, ECHO_ST_BADDATA);
+        new_end[b] = ok ? base + c : tok_end[b];
+    }
+    if (!ok) return;
+    const int64_t cols = a.row_bytes / 16;
+    for (int64_t i0 = 0; i0 < c; i0 += kBatch) {
+        __syncthreads();
+        if (tid < kBatch && i0 + tid < c) {
+            const int64_t x = path[r0 + i0 + tid];
+            bool bad = false;
+            from[tid] = row_of(base + x, &bad, false) * a.row_bytes;
+            to[tid] = row_of(base + i0 + tid, &bad, false) * a.row_bytes;
+        }
+        __syncthreads();
+        const int m = static_cast<int>(min(static_cast<int64_t>(kBatch), c - i0));
+        for (int64_t k = static_cast<int64_t>(blockIdx.y) * kKT + tid; k < cols * a.layers; k += static_cast<int64_t>(gridDim.y) * kKT) {
+            uint8_t* const kv = a.kv + k / cols * a.layer_bytes + k % cols * 16;
+            for (int i = 0; i < m; ++i)
+                if (from[i] != to[i]) *reinterpret_cast<uint4*>(kv + to[i]) = *reinterpret_cast<const uint4*>(kv + from[i]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+int check_pool(const echo_page_pool* p, int64_t n_tokens) {
+    if (!p || n_tokens < 0 || !p->refs || !p->kv || (n_tokens > 0 && !p->page_tab)) return ECHO_EINVAL;
+    if (p->n_pages < 1 || p->page < 1 || p->layers < 1 || p->row_bytes < 16 || p->row_bytes % 16) return ECHO_EINVAL;
+    if (p->n_pages > ECHO_POOL_MAX_PAGES) return ECHO_EUNSUPPORTED;
+    if (!is_aligned(p->kv, 16) || p->layer_bytes % 16) return ECHO_EINVAL;
+    const int64_t rows = p->n_pages * p->page;  // below 2^55
+    if (p->row_bytes > (1ll << 62) / rows) return ECHO_EINVAL;
+    if (p->layers > 1 && p->layer_bytes < rows * p->row_bytes) return ECHO_EINVAL;
+    return ECHO_OK;
+}
+
+PoolArgs pool_args(const echo_page_pool* p, int64_t n_tokens) {
+    PoolArgs a;
+    a.tab = p->page_tab;
+    a.refs = p->refs;
+    a.kv = static_cast<uint8_t*>(p->kv);
+    a.n_pages = p->n_pages;
+    a.row_bytes = p->row_bytes;
+    a.layer_bytes = p->layer_bytes;
+    a.layers = p->layers;
+    a.page = p->page;
+    a.entries = n_tokens / p->page + (n_tokens % p->page != 0);
+    return a;
+}
+
+int check_work(const void* ws, size_t ws_bytes, int B, int64_t n_pages) {
+    return ws && is_aligned(ws, 256) && ws_bytes >= echo_pages_workspace_size(B, n_pages) ? ECHO_OK : ECHO_EINVAL;
+}
+
+// Blocks over a request's entries when the regions are alike.
+unsigned entry_blocks(const PoolArgs& a, int B) {
+    const int64_t n = (a.entries / B + kFT - 1) / kFT;
+    return static_cast<unsigned>(n < 1 ? 1 : n > 64 ? 64 : n);
+}
+
+}  // namespace
+}  // namespace echo
+
+extern "C" size_t echo_pages_workspace_size(int B, int64_t n_pages) {
+    if (B <= 0 || B > ECHO_MAX_REQUESTS || n_pages <= 0 || n_pages > ECHO_POOL_MAX_PAGES) return 0;
+    return echo::work_layout(B, n_pages > B ? n_pages : B).total;
+}
+
+extern "C" int echo_pages_free(int B, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_page_pool* pool,
+                               int32_t* status, echo_stream_t stream) {
+    using namespace echo;
+    if (B <= 0 || !tok_off || !tok_end || !status) return ECHO_EINVAL;
+    if (B > ECHO_MAX_REQUESTS) return ECHO_EUNSUPPORTED;
+    const int rc = check_pool(pool, n_tokens);
+    if (rc) return rc;
+    if (n_tokens == 0) return ECHO_OK;
+    const PoolArgs a = pool_args(pool, n_tokens);
+    pages_free_kernel<<<dim3(B, entry_blocks(a, B)), kFT, 0, static_cast<cudaStream_t>(stream)>>>(a, tok_off, tok_end, n_tokens, status);
+    ECHO_CUDA_OK(cudaGetLastError());
+    return ECHO_OK;
+}
+
+extern "C" int echo_pages_reserve(int B, const int64_t* tok_off, const int64_t* tok_end, const int64_t* want, int64_t n_tokens,
+                                  const echo_page_pool* pool, int64_t* room, void* ws, size_t ws_bytes, int32_t* status,
+                                  echo_stream_t stream) {
+    using namespace echo;
+    if (B <= 0 || !tok_off || !tok_end || !want || !status) return ECHO_EINVAL;
+    if (B > ECHO_MAX_REQUESTS) return ECHO_EUNSUPPORTED;
+    int rc = check_pool(pool, n_tokens);
+    if (rc) return rc;
+    if ((rc = check_work(ws, ws_bytes, B, pool->n_pages))) return rc;
+    const PoolArgs a = pool_args(pool, n_tokens);
+    const Work w = work_of(ws, B, pool->n_pages > B ? pool->n_pages : B);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    pages_reserve_kernel<<<1, kPlanT, 0, s>>>(a, B, tok_off, tok_end, want, n_tokens, room, w, status);
+    ECHO_CUDA_OK(cudaGetLastError());
+    ECHO_CUDA_OK(launch_after(false, pages_move_kernel, dim3(static_cast<unsigned>(2 * sm_count())), kMT, 0, s, a, w));
+    return ECHO_OK;
+}
+
+extern "C" int echo_pages_fork(int n, const int32_t* src, const int32_t* dst, int B, const int64_t* tok_off, int64_t* tok_end,
+                               int64_t n_tokens, const echo_page_pool* pool, void* ws, size_t ws_bytes, int32_t* status,
+                               echo_stream_t stream) {
+    using namespace echo;
+    if (n < 0 || B <= 0 || !tok_off || !tok_end || !status) return ECHO_EINVAL;
+    if (n > ECHO_MAX_REQUESTS || B > ECHO_MAX_REQUESTS) return ECHO_EUNSUPPORTED;
+    int rc = check_pool(pool, n_tokens);
+    if (rc) return rc;
+    if (n == 0) return ECHO_OK;
+    if (!src || !dst || (rc = check_work(ws, ws_bytes, n, pool->n_pages))) return ECHO_EINVAL;
+    const PoolArgs a = pool_args(pool, n_tokens);
+    const ForkArgs f = {n, src, dst, B, tok_off, tok_end, n_tokens};
+    const Work w = work_of(ws, n, pool->n_pages > n ? pool->n_pages : n);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    pages_share_kernel<<<dim3(n, entry_blocks(a, B)), kFT, 0, s>>>(a, f, w, status);
+    ECHO_CUDA_OK(cudaGetLastError());
+    ECHO_CUDA_OK(launch_after(false, pages_tails_kernel, dim3(1), kPlanT, 0, s, a, f, w, status));
+    ECHO_CUDA_OK(launch_after(false, pages_move_kernel, dim3(static_cast<unsigned>(2 * sm_count())), kMT, 0, s, a, w));
+    return ECHO_OK;
+}
+
+extern "C" int echo_pages_compact(int64_t n_tokens, const echo_page_pool* pool, int32_t* used, void* ws, size_t ws_bytes,
+                                  int32_t* status, echo_stream_t stream) {
+    using namespace echo;
+    if (!used || !status) return ECHO_EINVAL;
+    int rc = check_pool(pool, n_tokens);
+    if (rc) return rc;
+    if ((rc = check_work(ws, ws_bytes, 1, pool->n_pages))) return rc;
+    const PoolArgs a = pool_args(pool, n_tokens);
+    const Work w = work_of(ws, 1, pool->n_pages);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    pages_compact_kernel<<<1, kPlanT, 0, s>>>(a, used, w);
+    ECHO_CUDA_OK(cudaGetLastError());
+    ECHO_CUDA_OK(launch_after(false, pages_place_kernel, dim3(static_cast<unsigned>(8 * sm_count())), kMT, 0, s, a, const_cast<const int32_t*>(used), w, status));
+    return ECHO_OK;
+}
+
+extern "C" int echo_rows_keep(int B, const int64_t* row_off, int64_t n_rows, const int32_t* path, const int32_t* count,
+                              const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_page_pool* pool,
+                              int64_t* new_end, int32_t* status, echo_stream_t stream) {
+    using namespace echo;
+    if (B <= 0 || n_rows < 0 || !row_off || !count || !tok_off || !tok_end || !new_end || !status) return ECHO_EINVAL;
+    if (B > ECHO_MAX_REQUESTS || n_rows > ECHO_CHUNK_MAX_ROWS) return ECHO_EUNSUPPORTED;
+    if (n_rows > 0 && !path) return ECHO_EINVAL;
+    if (new_end < tok_end + B && tok_end < new_end + B) return ECHO_EINVAL;
+    const int rc = check_pool(pool, n_tokens);
+    if (rc) return rc;
+    const PoolArgs a = pool_args(pool, n_tokens);
+    const int64_t blocks = (a.row_bytes / 16 * a.layers + kKT - 1) / kKT;
+    rows_keep_kernel<<<dim3(B, static_cast<unsigned>(blocks < 64 ? blocks : 64)), kKT, 0, static_cast<cudaStream_t>(stream)>>>(
+        a, row_off, n_rows, path, count, tok_off, tok_end, n_tokens, new_end, status);
+    ECHO_CUDA_OK(cudaGetLastError());
+    return ECHO_OK;
+}
