@@ -83,6 +83,8 @@ def lib_path() -> str:
 def load(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load libecho.so (raises when it is missing and not built)."""
     global _lib
+    if _lib is not None:  # (set once, when it is complete)
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -205,12 +207,18 @@ def _ptr(t):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _device():
+    # torch.cuda.current_device() without its look at the initialisation (0.6 us a call)
+    return torch.cuda.current_device() if _raw_stream is None or _raw_device is None else _raw_device()
 
 
 def _stream(s):
     if s is None:
         if _raw_stream is not None:  # the same handle as below, without making a Stream object (3 us a call)
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -454,7 +462,7 @@ def mla_chunk_workspace_size(n_rows: int, heads: int, B: int) -> int:
 
 
 def _check_chunk(call, row_off, q, tok_off, n_tokens, pages, lse, status, tok_end, *more):
-    B, n, heads, dev = tok_off.shape[0] - 1, q.shape[0], q.shape[1], torch.cuda.current_device()
+    (n, heads, _), B, dev = q.shape, tok_off.shape[0] - 1, _device()
     _expect(call, dev, ("row_off", row_off, torch.int64, (B + 1,)), ("tok_off", tok_off, torch.int64, (B + 1,)),
             ("q", q, torch.bfloat16, (n, heads, MLA_DQK)), ("lse", lse, torch.float32, (n, heads)),
             ("status", status, torch.int32, (1,)), *more)
@@ -516,13 +524,11 @@ def tree_masks(row_off, parent, mask, status, depth=None, stream=None):
     """echo_tree_masks: the ancestors of every node of the requests' draft trees.  parent [n] int32 (request-local,
     -1: none) -> mask [n,words] int32, a bit for each node of the request, depth [n] int32 (or None)."""
     B, n, words = row_off.shape[0] - 1, parent.shape[0], mask.shape[-1]
-    dev = torch.cuda.current_device()
-    _expect("tree_masks", dev, ("row_off", row_off, torch.int64, (B + 1,)), ("parent", parent, torch.int32, (n,)),
-            ("mask", mask, torch.int32, (n, words)), ("status", status, torch.int32, (1,)))
-    if depth is not None:
-        _expect("tree_masks", dev, ("depth", depth, torch.int32, (n,)))
-    _check("echo_tree_masks", load().echo_tree_masks(B, _ptr(row_off), n, _ptr(parent), words, _ptr(mask), _ptr(depth),
-                                                     _ptr(status), _stream(stream)))
+    _expect("tree_masks", _device(), ("row_off", row_off, torch.int64, (B + 1,)), ("parent", parent, torch.int32, (n,)),
+            ("mask", mask, torch.int32, (n, words)), ("status", status, torch.int32, (1,)),
+            *([] if depth is None else [("depth", depth, torch.int32, (n,))]))
+    _check("echo_tree_masks", load().echo_tree_masks(B, row_off.data_ptr(), n, parent.data_ptr(), words, mask.data_ptr(),
+                                                     _ptr(depth), status.data_ptr(), _stream(stream)))
 
 
 def mla_tree(row_off, q, mask, tok_off, n_tokens, pages, scale, out, lse, ws, status, tok_end=None, stream=None):
@@ -534,9 +540,9 @@ def mla_tree(row_off, q, mask, tok_off, n_tokens, pages, scale, out, lse, ws, st
                                ("out", out, torch.bfloat16, (q.shape[0], q.shape[1], MLA_DV)),
                                ("mask", mask, torch.int32, (q.shape[0], words)), ("ws", ws, torch.uint8, (ws.numel(),)))
     _check("echo_mla_tree", load().echo_mla_tree(
-        B, _ptr(row_off), n, heads, _ptr(q), _ptr(mask), words, _ptr(tok_off), _ptr(tok_end), int(n_tokens),
-        ctypes.byref(pages.struct), float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _ptr(status),
-        _stream(stream)))
+        B, row_off.data_ptr(), n, heads, q.data_ptr(), mask.data_ptr(), words, tok_off.data_ptr(), _ptr(tok_end),
+        int(n_tokens), pages.struct, float(scale), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
+        status.data_ptr(), _stream(stream)))
 
 
 def draft_verify(row_off, parent, token, target, path, count, next_tok, status, draft=None, u_node=None, u_pick=None,
@@ -546,23 +552,20 @@ def draft_verify(row_off, parent, token, target, path, count, next_tok, status, 
     of the same type: those its children were drawn from (None: drafts without probabilities); u_node [n] and u_pick [B]
     f32: uniform numbers in [0, 1) (both None: greedy, target may hold logits) -> path [n] int32 (accepted nodes from
     row_off[b] on, -1 behind), count [B] int32, next_tok [B] int32."""
-    B, (n, vocab), dev = row_off.shape[0] - 1, target.shape, torch.cuda.current_device()
-    if target.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"draft_verify: target must be float32 or bfloat16, not {target.dtype}")
-    _expect("draft_verify", dev, ("row_off", row_off, torch.int64, (B + 1,)), ("parent", parent, torch.int32, (n,)),
-            ("token", token, torch.int32, (n,)), ("target", target, target.dtype, (n, vocab)),
-            ("path", path, torch.int32, (n,)), ("count", count, torch.int32, (B,)),
-            ("next_tok", next_tok, torch.int32, (B,)), ("status", status, torch.int32, (1,)))
-    if draft is not None:
-        _expect("draft_verify", dev, ("draft", draft, target.dtype, (n, vocab)))
+    B, (n, vocab), dtype = row_off.shape[0] - 1, target.shape, target.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"draft_verify: target must be float32 or bfloat16, not {dtype}")
     if (u_node is None) != (u_pick is None):
         raise ValueError("draft_verify: u_node and u_pick go together")
-    if u_node is not None:
-        _expect("draft_verify", dev, ("u_node", u_node, torch.float32, (n,)), ("u_pick", u_pick, torch.float32, (B,)))
+    _expect("draft_verify", _device(), ("row_off", row_off, torch.int64, (B + 1,)), ("parent", parent, torch.int32, (n,)),
+            ("token", token, torch.int32, (n,)), ("target", target, dtype, (n, vocab)), ("path", path, torch.int32, (n,)),
+            ("count", count, torch.int32, (B,)), ("next_tok", next_tok, torch.int32, (B,)),
+            ("status", status, torch.int32, (1,)), *([] if draft is None else [("draft", draft, dtype, (n, vocab))]),
+            *([] if u_node is None else [("u_node", u_node, torch.float32, (n,)), ("u_pick", u_pick, torch.float32, (B,))]))
     _check("echo_draft_verify", load().echo_draft_verify(
-        B, _ptr(row_off), n, _ptr(parent), _ptr(token), vocab, DTYPE_F32 if target.dtype is torch.float32 else DTYPE_BF16,
-        _ptr(target), _ptr(draft), _ptr(u_node), _ptr(u_pick), _ptr(path), _ptr(count), _ptr(next_tok), _ptr(status),
-        _stream(stream)))
+        B, row_off.data_ptr(), n, parent.data_ptr(), token.data_ptr(), vocab,
+        DTYPE_F32 if dtype is torch.float32 else DTYPE_BF16, target.data_ptr(), _ptr(draft), _ptr(u_node), _ptr(u_pick),
+        path.data_ptr(), count.data_ptr(), next_tok.data_ptr(), status.data_ptr(), _stream(stream)))
 
 
 class PagePool:
@@ -575,11 +578,11 @@ class PagePool:
             raise ValueError("PagePool: 1 <= page < 2^31")
         n = refs.numel()
         shape = (n * page, MLA_DQK) if kv.dim() == 2 else (kv.shape[0], n * page, MLA_DQK)
-        _expect("PagePool", torch.cuda.current_device(), ("page_tab", page_tab, torch.int32, (page_tab.numel(),)),
+        _expect("PagePool", _device(), ("page_tab", page_tab, torch.int32, (page_tab.numel(),)),
                 ("refs", refs, torch.int32, (n,)), ("kv", kv, torch.bfloat16, shape))
         self.page_tab, self.refs, self.kv, self.page, self.n_pages = page_tab, refs, kv, int(page), n
         self.layers = 1 if kv.dim() == 2 else kv.shape[0]
-        self.tokens = page_tab.numel() * self.page
+        self.tokens, self.device = page_tab.numel() * self.page, kv.get_device()
         s = EchoPagePoolStruct()
         s.page_tab, s.refs, s.kv, s.n_pages = _ptr(page_tab), _ptr(refs), _ptr(kv), n
         s.row_bytes, s.layer_bytes, s.layers, s.page = 2 * MLA_DQK, 2 * MLA_DQK * n * self.page, self.layers, self.page
@@ -594,32 +597,39 @@ def pages_workspace_size(B: int, n_pages: int) -> int:
     return int(load().echo_pages_workspace_size(int(B), int(n_pages)))
 
 
-def _check_pool(call, tok_off, n_tokens, pool, status, *more):
-    B, dev = tok_off.shape[0] - 1, torch.cuda.current_device()
-    _expect(call, dev, ("tok_off", tok_off, torch.int64, (B + 1,)), ("status", status, torch.int32, (1,)), *more)
-    if pool.tokens < n_tokens or pool.refs.get_device() != dev:
-        raise ValueError(f"{call}: the page table covers {pool.tokens} token rows, not {n_tokens}, or lies on another device")
+def _check_pool(call, tok_off, n_tokens, pool, status, per_request, *more):
+    # per_request: tensors with an int64 for each request
+    B = tok_off.shape[0] - 1
+    dev = _device()
+    _expect(call, dev, ("tok_off", tok_off, torch.int64, (B + 1,)), ("status", status, torch.int32, (1,)),
+            *[(name, t, torch.int64, (B,)) for name, t in per_request], *more)
+    _check_table(call, n_tokens, pool, dev)
     return B
+
+
+def _check_table(call, n_tokens, pool, dev):
+    if pool.tokens < n_tokens or pool.device != dev:
+        raise ValueError(f"{call}: the page table covers {pool.tokens} token rows, not {n_tokens}, or lies on another device")
 
 
 def pages_reserve(tok_off, tok_end, want, n_tokens, pool, room, ws, status, stream=None):
     """echo_pages_reserve: pages for the tokens [tok_end[b], want[b]) of every request (want [B] int64, token rows),
     the lowest free ones; a page others hold too is replaced.  room [B] int64 (or None): want[b] where served, else
     tok_end[b].  ws: uint8, pages_workspace_size(B, n_pages)."""
-    B = _check_pool("pages_reserve", tok_off, n_tokens, pool, status, ("ws", ws, torch.uint8, (ws.numel(),)))
-    per = [("tok_end", tok_end), ("want", want)] + ([("room", room)] if room is not None else [])
-    _expect("pages_reserve", torch.cuda.current_device(), *((name, t, torch.int64, (B,)) for name, t in per))
+    per = [("tok_end", tok_end), ("want", want)]
+    if room is not None:
+        per.append(("room", room))
+    B = _check_pool("pages_reserve", tok_off, n_tokens, pool, status, per, ("ws", ws, torch.uint8, (ws.numel(),)))
     _check("echo_pages_reserve", load().echo_pages_reserve(
-        B, _ptr(tok_off), _ptr(tok_end), _ptr(want), int(n_tokens), ctypes.byref(pool.struct), _ptr(room), _ptr(ws),
-        ws.numel(), _ptr(status), _stream(stream)))
+        B, tok_off.data_ptr(), tok_end.data_ptr(), want.data_ptr(), int(n_tokens), pool.struct, _ptr(room), ws.data_ptr(),
+        ws.numel(), status.data_ptr(), _stream(stream)))
 
 
 def pages_free(tok_off, tok_end, n_tokens, pool, status, stream=None):
     """echo_pages_free: gives up the pages behind every request's end (tok_end[b] = tok_off[b]: all of them)."""
-    B = _check_pool("pages_free", tok_off, n_tokens, pool, status)
-    _expect("pages_free", torch.cuda.current_device(), ("tok_end", tok_end, torch.int64, (B,)))
-    _check("echo_pages_free", load().echo_pages_free(B, _ptr(tok_off), _ptr(tok_end), int(n_tokens),
-                                                     ctypes.byref(pool.struct), _ptr(status), _stream(stream)))
+    B = _check_pool("pages_free", tok_off, n_tokens, pool, status, [("tok_end", tok_end)])
+    _check("echo_pages_free", load().echo_pages_free(B, tok_off.data_ptr(), tok_end.data_ptr(), int(n_tokens), pool.struct,
+                                                     status.data_ptr(), _stream(stream)))
 
 
 def pages_fork(src, dst, tok_off, tok_end, n_tokens, pool, ws, status, stream=None):
@@ -627,38 +637,35 @@ def pages_fork(src, dst, tok_off, tok_end, n_tokens, pool, ws, status, stream=No
     full pages shared, the rows of a partly used last page copied, tok_end[dst[i]] set.  ws: uint8,
     pages_workspace_size(m, n_pages)."""
     m = src.numel()
-    B = _check_pool("pages_fork", tok_off, n_tokens, pool, status, ("src", src, torch.int32, (m,)),
+    B = _check_pool("pages_fork", tok_off, n_tokens, pool, status, [("tok_end", tok_end)], ("src", src, torch.int32, (m,)),
                     ("dst", dst, torch.int32, (m,)), ("ws", ws, torch.uint8, (ws.numel(),)))
-    _expect("pages_fork", torch.cuda.current_device(), ("tok_end", tok_end, torch.int64, (B,)))
     _check("echo_pages_fork", load().echo_pages_fork(
-        m, _ptr(src), _ptr(dst), B, _ptr(tok_off), _ptr(tok_end), int(n_tokens), ctypes.byref(pool.struct), _ptr(ws),
-        ws.numel(), _ptr(status), _stream(stream)))
+        m, src.data_ptr(), dst.data_ptr(), B, tok_off.data_ptr(), tok_end.data_ptr(), int(n_tokens), pool.struct,
+        ws.data_ptr(), ws.numel(), status.data_ptr(), _stream(stream)))
 
 
 def pages_compact(n_tokens, pool, used, ws, status, stream=None):
     """echo_pages_compact: the pages in use move to the first places of the pool, their rows, counts and table entries
     with them; used [1] int32: how many there are.  ws: uint8, pages_workspace_size(1, n_pages)."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     _expect("pages_compact", dev, ("used", used, torch.int32, (1,)), ("ws", ws, torch.uint8, (ws.numel(),)),
             ("status", status, torch.int32, (1,)))
-    if pool.tokens < n_tokens or pool.refs.get_device() != dev:
-        raise ValueError(f"pages_compact: the page table covers {pool.tokens} token rows, not {n_tokens}, or lies on "
-                         "another device")
-    _check("echo_pages_compact", load().echo_pages_compact(int(n_tokens), ctypes.byref(pool.struct), _ptr(used), _ptr(ws),
-                                                           ws.numel(), _ptr(status), _stream(stream)))
+    _check_table("pages_compact", n_tokens, pool, dev)
+    _check("echo_pages_compact", load().echo_pages_compact(int(n_tokens), pool.struct, used.data_ptr(), ws.data_ptr(),
+                                                           ws.numel(), status.data_ptr(), _stream(stream)))
 
 
 def rows_keep(row_off, path, count, tok_off, tok_end, n_tokens, pool, new_end, status, stream=None):
     """echo_rows_keep: the cache rows of the accepted nodes of each request's draft tree (path, count of
     draft_verify) move together behind the context, in every layer; new_end [B] int64: where the contexts then end
     (not tok_end itself).  pages_free(new_end) gives up the pages behind."""
-    B = _check_pool("rows_keep", tok_off, n_tokens, pool, status)
-    _expect("rows_keep", torch.cuda.current_device(), ("row_off", row_off, torch.int64, (B + 1,)),
-            ("path", path, torch.int32, (path.numel(),)), ("count", count, torch.int32, (B,)),
-            ("tok_end", tok_end, torch.int64, (B,)), ("new_end", new_end, torch.int64, (B,)))
+    B, n = tok_off.shape[0] - 1, path.numel()
+    _check_pool("rows_keep", tok_off, n_tokens, pool, status, [("tok_end", tok_end), ("new_end", new_end)],
+                ("row_off", row_off, torch.int64, (B + 1,)), ("path", path, torch.int32, (n,)),
+                ("count", count, torch.int32, (B,)))
     _check("echo_rows_keep", load().echo_rows_keep(
-        B, _ptr(row_off), path.numel(), _ptr(path), _ptr(count), _ptr(tok_off), _ptr(tok_end), int(n_tokens),
-        ctypes.byref(pool.struct), _ptr(new_end), _ptr(status), _stream(stream)))
+        B, row_off.data_ptr(), n, path.data_ptr(), count.data_ptr(), tok_off.data_ptr(), tok_end.data_ptr(), int(n_tokens),
+        pool.struct, new_end.data_ptr(), status.data_ptr(), _stream(stream)))
 
 
 def evict_select(tok_off, n_tokens, slot2tok, mass, keep, evict_tok, evict_slot, evict_cnt, status, sinks=0, recent=0,

@@ -7,6 +7,7 @@
 // latency, the moves the memory.
 #include "echo_common.cuh"
 #include "echo_paged.cuh"
+#include "echo_tc.cuh"
 
 namespace echo {
 namespace {
@@ -21,6 +22,7 @@ struct PoolArgs {
     int layers;
     int page;
     int64_t entries;  // of the table
+    bool wide;        // refs on a 16-byte boundary
 };
 
 // Rows [src, src + rows) of every layer go to dst.
@@ -37,25 +39,31 @@ struct Work {
     Move* move;       // [requests of the call]
     int32_t* list;    // [n_pages]
     int32_t* map;     // [n_pages]
+    int32_t* far;     // [n_pages]
 };
 
 struct WorkLayout {
-    size_t move, list, map, total;
+    size_t move, list, map, far, total;
 };
 inline WorkLayout work_layout(int B, int64_t n_pages) {
     WorkLayout l;
     l.move = 256;
     l.list = round_up(l.move + static_cast<size_t>(B) * sizeof(Move), 256);
     l.map = round_up(l.list + static_cast<size_t>(n_pages) * 4, 256);
-    l.total = round_up(l.map + static_cast<size_t>(n_pages) * 4, 256);
+    l.far = round_up(l.map + static_cast<size_t>(n_pages) * 4, 256);
+    l.total = round_up(l.far + static_cast<size_t>(n_pages) * 4, 256);
     return l;
 }
 inline Work work_of(void* ws, int B, int64_t n_pages) {
     const WorkLayout l = work_layout(B, n_pages);
     uint8_t* const w = static_cast<uint8_t*>(ws);
     return Work{reinterpret_cast<int32_t*>(w), reinterpret_cast<Move*>(w + l.move), reinterpret_cast<int32_t*>(w + l.list),
-                reinterpret_cast<int32_t*>(w + l.map)};
+                reinterpret_cast<int32_t*>(w + l.map), reinterpret_cast<int32_t*>(w + l.far)};
 }
+
+// x / d and x % d for an x >= 0, by a 32-bit division where that does (the 64-bit one takes some 100 instructions).
+__device__ __forceinline__ int64_t quot(int64_t x, int d) { return x >> 32 ? x / d : static_cast<uint32_t>(x) / static_cast<uint32_t>(d); }
+__device__ __forceinline__ int rest(int64_t x, int d) { return static_cast<int>(x - quot(x, d) * d); }
 
 // Request b's token rows [off, end) of its region [off, last).  False: inconsistent, or not on a page's border.
 struct Region {
@@ -65,9 +73,9 @@ __device__ __forceinline__ bool region_of(const int64_t* tok_off, const int64_t*
     r->off = tok_off[b];
     r->last = tok_off[b + 1];
     r->end = tok_end[b];
-    return r->off >= 0 && r->last >= r->off && r->last <= n_tokens && r->end >= r->off && r->end <= r->last && r->off % page == 0;
+    return r->off >= 0 && r->last >= r->off && r->last <= n_tokens && r->end >= r->off && r->end <= r->last && rest(r->off, page) == 0;
 }
-__device__ __forceinline__ int64_t pages_to(int64_t tok, int page) { return (tok + page - 1) / page; }
+__device__ __forceinline__ int64_t pages_to(int64_t tok, int page) { return quot(tok + page - 1, page); }
 
 __device__ __forceinline__ bool in_pool(const PoolArgs& a, int32_t p) { return p >= 0 && p < a.n_pages; }
 
@@ -81,6 +89,46 @@ __device__ __forceinline__ void drop_ref(const PoolArgs& a, int32_t p, int32_t* 
         atomicAdd(a.refs + p, 1);
         set_status(status, ECHO_ST_BADDATA);
     }
+}
+
+// ---------------------------------------------------------------- moves
+// Rows move 64 bytes a thread at a time, four 16-byte pieces in flight: a piece of NT * 64 bytes by a block of NT.
+constexpr int kMT = 256;
+
+template <int NT>
+__device__ __forceinline__ void move_piece(const uint8_t* src, uint8_t* dst, int64_t bytes) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = (i * NT + threadIdx.x) * 16;
+        if (at < bytes) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + at));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = (i * NT + threadIdx.x) * 16;
+        if (at < bytes) __stcs(reinterpret_cast<uint4*>(dst + at), v[i]);
+    }
+}
+
+// The n listed moves, each of at most a page's rows, shared by `blocks` blocks along x and `rows` along the layers.
+template <int NT>
+__device__ __forceinline__ void move_all(const PoolArgs& a, const Move* move, uint32_t n, uint32_t block, uint32_t blocks, int row, int rows) {
+    constexpr int kPiece = NT * 64;
+    const uint32_t pieces = static_cast<uint32_t>((a.page * a.row_bytes + kPiece - 1) / kPiece);
+    for (uint32_t u = block; u < n * pieces; u += blocks) {
+        const Move m = move[u / pieces];
+        const int64_t at = static_cast<int64_t>(u % pieces) * kPiece, bytes = m.rows * a.row_bytes - at;
+        if (bytes <= 0) continue;
+        for (int l = row; l < a.layers; l += rows) {
+            uint8_t* const kv = a.kv + l * a.layer_bytes + at;
+            move_piece<NT>(kv + m.src * a.row_bytes, kv + m.dst * a.row_bytes, bytes);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kMT) pages_move_kernel(PoolArgs a, Work w) {
+    pdl_wait();
+    move_all<kMT>(a, w.move, static_cast<uint32_t>(*w.moves), blockIdx.x, gridDim.x, blockIdx.y, gridDim.y);
 }
 
 // ---------------------------------------------------------------- free
@@ -105,23 +153,31 @@ __global__ void __launch_bounds__(kFT)
 // ---------------------------------------------------------------- the block that plans
 constexpr int kPlanT = 1024;
 
+// The counts of 16 pages from p on (1 behind the last).
+__device__ __forceinline__ void counts_of(const PoolArgs& a, int64_t p, int32_t (&r)[16]) {
+    if (p + 16 <= a.n_pages && a.wide) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<int4*>(r + 4 * i) = reinterpret_cast<const int4*>(a.refs + p)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = p + i < a.n_pages ? a.refs[p + i] : 1;
+    }
+}
+
 // Lists the first `most` free pages, ascending; returns how many there are up to `most`.  A block together.
 __device__ __forceinline__ int64_t list_free(const PoolArgs& a, int64_t most, int32_t* list, uint32_t* scratch) {
     int64_t found = 0;
-    for (int64_t p0 = 0; p0 < a.n_pages && found < most; p0 += 4 * kPlanT) {
-        const int64_t p = p0 + 4 * threadIdx.x;
-        bool is[4];
-        uint32_t n = 0;
+    for (int64_t p0 = 0; p0 < a.n_pages && found < most; p0 += 16 * kPlanT) {
+        const int64_t p = p0 + 16 * threadIdx.x;
+        int32_t r[16];
+        counts_of(a, p, r);
+        uint32_t n = 0, total;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            is[i] = p + i < a.n_pages && a.refs[p + i] == 0;
-            n += is[i];
-        }
-        uint32_t total;
+        for (int i = 0; i < 16; ++i) n += r[i] == 0;
         int64_t at = found + block_exclusive_scan<kPlanT>(n, scratch, &total);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (is[i]) {
+        for (int i = 0; i < 16; ++i)
+            if (r[i] == 0) {
                 if (at < most) list[at] = static_cast<int32_t>(p + i);
                 ++at;
             }
@@ -145,7 +201,9 @@ __device__ __forceinline__ bool needs_page(const PoolArgs& a, int64_t e, bool* b
     return r > 1;
 }
 
-__global__ void __launch_bounds__(kPlanT)
+// A cluster: its first CTA plans, all of it copies what a copy on write has to (one launch; most calls copy nothing).
+constexpr int kReserveCtas = 8;
+__global__ void __cluster_dims__(kReserveCtas, 1, 1) __launch_bounds__(kPlanT)
     pages_reserve_kernel(PoolArgs a, int B, const int64_t* __restrict__ tok_off, const int64_t* __restrict__ tok_end,
                          const int64_t* __restrict__ want, int64_t n_tokens, int64_t* __restrict__ room, Work w, int32_t* status) {
     __shared__ int64_t scratch64[kPlanT / 32];
@@ -153,87 +211,93 @@ __global__ void __launch_bounds__(kPlanT)
     __shared__ int32_t need[ECHO_MAX_REQUESTS];
     __shared__ int s_moves, s_given;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) s_moves = s_given = 0;
-    // ---- how many pages every request needs, a warp to each; -1: none, it is inconsistent
-    for (int b = warp; b < B; b += kPlanT / 32) {
-        Region r;
-        const int64_t to = want[b];
-        bool ok = region_of(tok_off, tok_end, n_tokens, a.page, b, &r) && to >= r.end && to <= r.last;
-        int64_t n = 0;
-        if (ok && to > r.end) {
-            const int64_t e0 = r.end / a.page, e1 = pages_to(to, a.page);
-            bool bad = false;
-            for (int64_t base = e0; base < e1; base += 32) {
-                const int64_t e = base + lane;
-                int32_t p;
-                const bool it = e < e1 && needs_page(a, e, &bad, &p);
-                if (it && p < 0 && e == e0 && r.end % a.page) bad = true;  // its rows are nowhere
-                n += __popc(__ballot_sync(0xffffffffu, it));
+    if (blockIdx.x == 0) {
+        if (tid == 0) s_moves = s_given = 0;
+        // ---- how many pages every request needs, a warp to each; -1: none, it is inconsistent
+        for (int b = warp; b < B; b += kPlanT / 32) {
+            Region r;
+            const int64_t to = want[b];
+            bool ok = region_of(tok_off, tok_end, n_tokens, a.page, b, &r) && to >= r.end && to <= r.last;
+            int64_t n = 0;
+            if (ok && to > r.end) {
+                const int64_t e0 = quot(r.end, a.page), e1 = pages_to(to, a.page);
+                const bool part = rest(r.end, a.page) > 0;
+                bool bad = false;
+                for (int64_t base = e0; base < e1; base += 32) {
+                    const int64_t e = base + lane;
+                    int32_t p;
+                    const bool it = e < e1 && needs_page(a, e, &bad, &p);
+                    if (it && p < 0 && e == e0 && part) bad = true;  // its rows are nowhere
+                    n += __popc(__ballot_sync(0xffffffffu, it));
+                }
+                ok = !__any_sync(0xffffffffu, bad);
             }
-            ok = !__any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+                need[b] = ok ? static_cast<int32_t>(min(n, static_cast<int64_t>(0x7FFFFFFF))) : -1;
+                if (!ok) set_status(status, ECHO_ST_BADDATA);
+            }
         }
-        if (lane == 0) {
-            need[b] = ok ? static_cast<int32_t>(min(n, static_cast<int64_t>(0x7FFFFFFF))) : -1;
-            if (!ok) set_status(status, ECHO_ST_BADDATA);
-        }
-    }
-    __syncthreads();
-    // ---- the free pages
-    int64_t mine = 0;
-    for (int b = tid; b < B; b += kPlanT) mine += max(need[b], 0);
-    int64_t total;
-    (void)block_scan64<kPlanT>(mine, scratch64, &total);
-    const int64_t most = min(total, a.n_pages);
-    const int64_t have = list_free(a, most, w.list, scratch);
-    // ---- where each request's begin, or that it goes without
-    int64_t base = 0;
-    bool full = false;
-    for (int b0 = 0; b0 < B; b0 += kPlanT) {
-        const int b = b0 + tid;
-        const int64_t n = b < B ? max(need[b], 0) : 0;
-        int64_t sum;
         __syncthreads();
-        const int64_t at = base + block_scan64<kPlanT>(n, scratch64, &sum);
-        base += sum;
-        if (b < B) {
-            const bool served = need[b] >= 0 && (n == 0 || at + n <= have);
-            full |= need[b] >= 0 && !served;
-            if (room) room[b] = served ? want[b] : tok_end[b];
-            need[b] = served && n > 0 ? static_cast<int32_t>(at) : -1;
-            if (served && n > 0) atomicMax(&s_given, static_cast<int>(at + n));
-        }
-    }
-    if (full) set_status(status, ECHO_ST_FULL);
-    __syncthreads();
-    // ---- handed out; the counts of the pages replaced fall when all have been, since two requests may replace the same one
-    for (int b = warp; b < B; b += kPlanT / 32) {
-        int64_t at = need[b];
-        if (at < 0) continue;
-        Region r;
-        (void)region_of(tok_off, tok_end, n_tokens, a.page, b, &r);
-        const int64_t e0 = r.end / a.page, e1 = pages_to(want[b], a.page);
-        for (int64_t first = e0; first < e1; first += 32) {
-            const int64_t e = first + lane;
-            int32_t p = -1;
-            bool bad = false;
-            const bool it = e < e1 && needs_page(a, e, &bad, &p);
-            const uint32_t m = __ballot_sync(0xffffffffu, it);
-            if (it) {
-                const int64_t k = at + __popc(m & ((1u << lane) - 1u));
-                const int32_t to = w.list[k];
-                a.tab[e] = to;
-                a.refs[to] = 1;
-                w.map[k] = p;
-                if (p >= 0 && e == e0 && r.end % a.page)
-                    w.move[atomicAdd(&s_moves, 1)] = Move{static_cast<int64_t>(p) * a.page, static_cast<int64_t>(to) * a.page, r.end % a.page, 0};
+        // ---- the free pages
+        int64_t mine = 0;
+        for (int b = tid; b < B; b += kPlanT) mine += max(need[b], 0);
+        int64_t total;
+        (void)block_scan64<kPlanT>(mine, scratch64, &total);
+        const int64_t most = min(total, a.n_pages);
+        const int64_t have = list_free(a, most, w.list, scratch);
+        // ---- where each request's begin, or that it goes without
+        int64_t base = 0;
+        bool full = false;
+        for (int b0 = 0; b0 < B; b0 += kPlanT) {
+            const int b = b0 + tid;
+            const int64_t n = b < B ? max(need[b], 0) : 0;
+            int64_t sum;
+            __syncthreads();
+            const int64_t at = base + block_scan64<kPlanT>(n, scratch64, &sum);
+            base += sum;
+            if (b < B) {
+                const bool served = need[b] >= 0 && (n == 0 || at + n <= have);
+                full |= need[b] >= 0 && !served;
+                if (room) room[b] = served ? want[b] : tok_end[b];
+                need[b] = served && n > 0 ? static_cast<int32_t>(at) : -1;
+                if (served && n > 0) atomicMax(&s_given, static_cast<int>(at + n));
             }
-            at += __popc(m);
         }
+        if (full) set_status(status, ECHO_ST_FULL);
+        __syncthreads();
+        // ---- handed out; the counts of the pages replaced fall when all have been, since two requests may replace the same one
+        for (int b = warp; b < B; b += kPlanT / 32) {
+            int64_t at = need[b];
+            if (at < 0) continue;
+            Region r;
+            (void)region_of(tok_off, tok_end, n_tokens, a.page, b, &r);
+            const int64_t e0 = quot(r.end, a.page), e1 = pages_to(want[b], a.page);
+            const int part = rest(r.end, a.page);
+            for (int64_t first = e0; first < e1; first += 32) {
+                const int64_t e = first + lane;
+                int32_t p = -1;
+                bool bad = false;
+                const bool it = e < e1 && needs_page(a, e, &bad, &p);
+                const uint32_t m = __ballot_sync(0xffffffffu, it);
+                if (it) {
+                    const int64_t k = at + __popc(m & ((1u << lane) - 1u));
+                    const int32_t to = w.list[k];
+                    a.tab[e] = to;
+                    a.refs[to] = 1;
+                    w.map[k] = p;
+                    if (p >= 0 && e == e0 && part)
+                        w.move[atomicAdd(&s_moves, 1)] = Move{static_cast<int64_t>(p) * a.page, static_cast<int64_t>(to) * a.page, part, 0};
+                }
+                at += __popc(m);
+            }
+        }
+        __syncthreads();
+        for (int k = tid; k < s_given; k += kPlanT)
+            if (w.map[k] >= 0) drop_ref(a, w.map[k], status);
+        if (tid == 0) *w.moves = s_moves;
     }
-    __syncthreads();
-    for (int k = tid; k < s_given; k += kPlanT)
-        if (w.map[k] >= 0) drop_ref(a, w.map[k], status);
-    if (tid == 0) *w.moves = s_moves;
+    cluster_sync_all();
+    move_all<kPlanT>(a, w.move, static_cast<uint32_t>(*w.moves), blockIdx.x, kReserveCtas, 0, 1);
 }
 
 // ---------------------------------------------------------------- fork
@@ -260,7 +324,7 @@ __device__ __forceinline__ bool fork_pair(const ForkArgs& f, int page, int i, Re
     to->off = f.tok_off[d];
     to->last = f.tok_off[d + 1];
     to->end = to->off;
-    return ok && to->off >= 0 && to->last >= to->off && to->last <= f.n_tokens && to->off % page == 0 && to->last - to->off >= from->end - from->off;
+    return ok && to->off >= 0 && to->last >= to->off && to->last <= f.n_tokens && rest(to->off, page) == 0 && to->last - to->off >= from->end - from->off;
 }
 
 __global__ void __launch_bounds__(kFT) pages_share_kernel(PoolArgs a, ForkArgs f, Work w, int32_t* status) {
@@ -272,9 +336,9 @@ __global__ void __launch_bounds__(kFT) pages_share_kernel(PoolArgs a, ForkArgs f
         if (!ok) set_status(status, ECHO_ST_BADDATA);
     }
     if (!ok) return;
-    const int64_t full = (from.end - from.off) / a.page, entries = pages_to(to.last, a.page) - to.off / a.page;
-    const int32_t* const s = a.tab + from.off / a.page;
-    int32_t* const d = a.tab + to.off / a.page;
+    const int64_t full = quot(from.end - from.off, a.page), entries = pages_to(to.last, a.page) - quot(to.off, a.page);
+    const int32_t* const s = a.tab + quot(from.off, a.page);
+    int32_t* const d = a.tab + quot(to.off, a.page);
     for (int64_t e = static_cast<int64_t>(blockIdx.y) * kFT + threadIdx.x; e < entries; e += static_cast<int64_t>(gridDim.y) * kFT) {
         const int32_t old = d[e];
         int32_t p = e < full ? s[e] : -1;
@@ -299,7 +363,7 @@ __global__ void __launch_bounds__(kPlanT) pages_tails_kernel(PoolArgs a, ForkArg
         bool it = false;
         if (i < f.n && w.map[i]) {
             const int64_t off = f.tok_off[f.src[i]], n = f.tok_end[f.src[i]] - off;
-            it = n % a.page && in_pool(a, a.tab[off / a.page + n / a.page]);
+            it = rest(n, a.page) && in_pool(a, a.tab[quot(off, a.page) + quot(n, a.page)]);
         }
         uint32_t sum;
         (void)block_exclusive_scan<kPlanT>(it, scratch, &sum);
@@ -310,16 +374,16 @@ __global__ void __launch_bounds__(kPlanT) pages_tails_kernel(PoolArgs a, ForkArg
     bool full = false, bad = false;
     for (int i0 = 0; i0 < f.n; i0 += kPlanT) {
         const int i = i0 + tid;
-        int64_t n = 0, rest = 0, off = 0, to_off = 0;
+        int64_t n = 0, over = 0, off = 0, to_off = 0;
         int32_t p = -1;
         const bool ok = i < f.n && w.map[i];
         if (ok) {
             off = f.tok_off[f.src[i]];
             n = f.tok_end[f.src[i]] - off;
-            rest = n % a.page;
+            over = rest(n, a.page);
             to_off = f.tok_off[f.dst[i]];
-            if (rest) {
-                p = a.tab[off / a.page + n / a.page];
+            if (over) {
+                p = a.tab[quot(off, a.page) + quot(n, a.page)];
                 bad |= p >= 0 && !in_pool(a, p);
             }
         }
@@ -329,12 +393,12 @@ __global__ void __launch_bounds__(kPlanT) pages_tails_kernel(PoolArgs a, ForkArg
         if (it) {
             if (at < have) {
                 const int32_t to = w.list[at];
-                a.tab[to_off / a.page + n / a.page] = to;
+                a.tab[quot(to_off, a.page) + quot(n, a.page)] = to;
                 a.refs[to] = 1;
-                w.move[at] = Move{static_cast<int64_t>(p) * a.page, static_cast<int64_t>(to) * a.page, rest, 0};
+                w.move[at] = Move{static_cast<int64_t>(p) * a.page, static_cast<int64_t>(to) * a.page, over, 0};
             } else {
                 full = true;
-                n -= rest;
+                n -= over;
             }
         }
         if (ok) f.tok_end[f.dst[i]] = to_off + n;
@@ -346,77 +410,81 @@ __global__ void __launch_bounds__(kPlanT) pages_tails_kernel(PoolArgs a, ForkArg
 }
 
 // ---------------------------------------------------------------- compact
-// list[k]: the k-th free place before U; map[p]: where page p >= U goes (-1: it is free).
+// list[k]: the k-th free place before U, far[k]: the k-th page in use from U on, which goes there; map[p]: where page p >= U
+// goes (-1: it is free).
 __global__ void __launch_bounds__(kPlanT) pages_compact_kernel(PoolArgs a, int32_t* __restrict__ used, Work w) {
     __shared__ uint32_t scratch[kPlanT / 32 + 1];
     const int tid = threadIdx.x;
-    uint32_t mine = 0;
-    for (int64_t p = tid; p < a.n_pages; p += kPlanT) mine += a.refs[p] > 0;
-    uint32_t U;
+    uint32_t mine = 0, U;
+    int32_t r[16];
+    for (int64_t p0 = 0; p0 < a.n_pages; p0 += 16 * kPlanT) {
+        counts_of(a, p0 + 16 * tid, r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mine += r[i] > 0 && p0 + 16 * tid + i < a.n_pages;
+    }
     (void)block_exclusive_scan<kPlanT>(mine, scratch, &U);
     uint32_t holes = 0, far = 0;
-    for (int64_t p0 = 0; p0 < U; p0 += kPlanT) {
-        const int64_t p = p0 + tid;
-        const bool is = p < U && a.refs[p] <= 0;
-        uint32_t total;
-        const uint32_t at = holes + block_exclusive_scan<kPlanT>(is, scratch, &total);
-        if (is) w.list[at] = static_cast<int32_t>(p);
+    for (int64_t p0 = 0; p0 < U; p0 += 16 * kPlanT) {
+        const int64_t p = p0 + 16 * tid;
+        counts_of(a, p, r);
+        uint32_t n = 0, total;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) n += r[i] <= 0 && p + i < U;
+        uint32_t at = holes + block_exclusive_scan<kPlanT>(n, scratch, &total);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (r[i] <= 0 && p + i < U) w.list[at++] = static_cast<int32_t>(p + i);
         holes += total;
     }
     __syncthreads();
-    for (int64_t p0 = U; p0 < a.n_pages; p0 += kPlanT) {
-        const int64_t p = p0 + tid;
-        const int32_t r = p < a.n_pages ? a.refs[p] : 0;
-        uint32_t total;
-        const uint32_t at = far + block_exclusive_scan<kPlanT>(r > 0, scratch, &total);
-        if (p < a.n_pages) {
-            const int32_t to = r > 0 ? w.list[at] : -1;
-            w.map[p] = to;
-            if (r > 0) {
-                a.refs[to] = r;
-                a.refs[p] = 0;
+    for (int64_t p0 = U & ~15u; p0 < a.n_pages; p0 += 16 * kPlanT) {
+        const int64_t p = p0 + 16 * tid;
+        counts_of(a, p, r);
+        uint32_t n = 0, total;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) n += r[i] > 0 && p + i >= U && p + i < a.n_pages;
+        uint32_t at = far + block_exclusive_scan<kPlanT>(n, scratch, &total);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (p + i < U || p + i >= a.n_pages) continue;
+            int32_t to = -1;
+            if (r[i] > 0) {
+                to = w.list[at];
+                w.far[at++] = static_cast<int32_t>(p + i);
+                a.refs[to] = r[i];
+                a.refs[p + i] = 0;
             }
+            w.map[p + i] = to;
         }
         far += total;
     }
-    if (tid == 0) *used = static_cast<int32_t>(U);
-}
-
-constexpr int kMT = 256;
-
-__device__ __forceinline__ void move_bytes(const uint8_t* src, uint8_t* dst, int64_t bytes) {
-    for (int64_t i = threadIdx.x * 16ll; i < bytes; i += kMT * 16ll)
-        *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(src + i);
+    if (tid == 0) {
+        *used = static_cast<int32_t>(U);
+        *w.moves = static_cast<int32_t>(far);
+    }
 }
 
 __global__ void __launch_bounds__(kMT) pages_place_kernel(PoolArgs a, const int32_t* __restrict__ used, Work w, int32_t* status) {
     pdl_wait();
     const int32_t U = *used;
-    for (int64_t e = static_cast<int64_t>(blockIdx.x) * kMT + threadIdx.x; e < a.entries; e += static_cast<int64_t>(gridDim.x) * kMT) {
-        const int32_t p = a.tab[e];
-        if (p < U) continue;
-        const int32_t to = p < a.n_pages ? w.map[p] : -1;
-        if (to < 0) set_status(status, ECHO_ST_BADDATA);
-        else a.tab[e] = to;
-    }
-    const int64_t bytes = a.page * a.row_bytes, pages = a.n_pages - U;
-    for (int64_t u = blockIdx.x; u < pages * a.layers; u += gridDim.x) {
-        const int64_t l = u / pages, p = U + u % pages;
-        const int32_t to = w.map[p];
-        if (to < 0) continue;
-        uint8_t* const kv = a.kv + l * a.layer_bytes;
-        move_bytes(kv + p * bytes, kv + to * bytes, bytes);
-    }
-}
-
-// ---------------------------------------------------------------- moves
-__global__ void __launch_bounds__(kMT) pages_move_kernel(PoolArgs a, Work w) {
-    pdl_wait();
-    const int64_t n = *w.moves;
-    for (int64_t u = blockIdx.x; u < n * a.layers; u += gridDim.x) {
-        const Move m = w.move[u % n];
-        uint8_t* const kv = a.kv + u / n * a.layer_bytes;
-        move_bytes(kv + m.src * a.row_bytes, kv + m.dst * a.row_bytes, m.rows * a.row_bytes);
+    if (blockIdx.y == 0)
+        for (int64_t e = static_cast<int64_t>(blockIdx.x) * kMT + threadIdx.x; e < a.entries; e += static_cast<int64_t>(gridDim.x) * kMT) {
+            const int32_t p = a.tab[e];
+            if (p < U) continue;
+            const int32_t to = p < a.n_pages ? w.map[p] : -1;
+            if (to < 0) set_status(status, ECHO_ST_BADDATA);
+            else a.tab[e] = to;
+        }
+    const int64_t bytes = a.page * a.row_bytes;
+    constexpr int kPiece = kMT * 64;
+    const uint32_t pieces = static_cast<uint32_t>((bytes + kPiece - 1) / kPiece), n = static_cast<uint32_t>(*w.moves) * pieces;
+    for (uint32_t u = blockIdx.x; u < n; u += gridDim.x) {
+        const uint32_t k = u / pieces;
+        const int64_t at = static_cast<int64_t>(u % pieces) * kPiece, src = w.far[k] * bytes + at, dst = w.list[k] * bytes + at;
+        for (int l = blockIdx.y; l < a.layers; l += gridDim.y) {
+            uint8_t* const kv = a.kv + l * a.layer_bytes;
+            move_piece<kMT>(kv + src, kv + dst, bytes - at);
+        }
     }
 }
 
@@ -424,8 +492,10 @@ __global__ void __launch_bounds__(kMT) pages_move_kernel(PoolArgs a, Work w) {
 constexpr int kKT = 288;
 constexpr int kBatch = 64;
 
-// A thread has one 16-byte column of some layers and takes the path's rows in order: the path ascends, so
-// a row is read before a later one is written over it.
+constexpr int kHeld = 8;  // rows a thread reads before it writes them
+
+// A thread has one 16-byte column of some layers and takes the path's rows in order, eight at a time: the path
+// ascends, so no row is written before it has been read.
 __global__ void __launch_bounds__(kKT)
     rows_keep_kernel(PoolArgs a, const int64_t* __restrict__ row_off, int64_t n_rows, const int32_t* __restrict__ path,
                      const int32_t* __restrict__ count, const int64_t* __restrict__ tok_off, const int64_t* __restrict__ tok_end,
@@ -438,23 +508,30 @@ __global__ void __launch_bounds__(kKT)
     bool ok = region_of(tok_off, tok_end, n_tokens, a.page, b, &r) && r0 >= 0 && r1 >= r0 && r1 <= n_rows && r1 - r0 <= r.end - r.off &&
               c >= 0 && c <= r1 - r0;
     const int64_t n = r1 - r0, base = r.end - n;
-    const auto row_of = [&](int64_t tok, bool* bad, bool whole) {
-        const int32_t p = a.tab[tok / a.page];
-        if (!in_pool(a, p) || (whole && a.refs[p] != 1)) {
+    // bytes from the pool's first row; alone: the page has to be this request's alone
+    const auto row_of = [&](int64_t tok, bool* bad, bool alone) {
+        const int64_t e = quot(tok, a.page);
+        const int32_t p = a.tab[e];
+        if (!in_pool(a, p) || (alone && a.refs[p] != 1)) {
             *bad = true;
             return static_cast<int64_t>(0);
         }
-        return static_cast<int64_t>(p) * a.page + tok % a.page;
+        return (static_cast<int64_t>(p) * a.page + (tok - e * a.page)) * a.row_bytes;
     };
     if (ok) {
         bool bad = false;
         for (int64_t i = tid; i < c; i += kKT) {
             const int64_t x = path[r0 + i], before = i > 0 ? path[r0 + i - 1] : -1;
+            int64_t src = 0, dst = 0;
             if (x <= before || x >= n) {
                 bad = true;
             } else if (x != i) {
-                (void)row_of(base + x, &bad, false);
-                (void)row_of(base + i, &bad, true);
+                src = row_of(base + x, &bad, false);
+                dst = row_of(base + i, &bad, true);
+            }
+            if (i < kBatch) {
+                from[i] = src;
+                to[i] = dst;
             }
         }
         ok = !__syncthreads_or(bad);
@@ -464,21 +541,31 @@ __global__ void __launch_bounds__(kKT)
         new_end[b] = ok ? base + c : tok_end[b];
     }
     if (!ok) return;
-    const int64_t cols = a.row_bytes / 16;
+    const int cols = static_cast<int>(a.row_bytes / 16);
     for (int64_t i0 = 0; i0 < c; i0 += kBatch) {
-        __syncthreads();
-        if (tid < kBatch && i0 + tid < c) {
-            const int64_t x = path[r0 + i0 + tid];
-            bool bad = false;
-            from[tid] = row_of(base + x, &bad, false) * a.row_bytes;
-            to[tid] = row_of(base + i0 + tid, &bad, false) * a.row_bytes;
+        if (i0 > 0) {
+            __syncthreads();
+            if (tid < kBatch && i0 + tid < c) {
+                const int64_t i = i0 + tid, x = path[r0 + i];
+                bool bad = false;
+                from[tid] = x != i ? row_of(base + x, &bad, false) : 0;
+                to[tid] = x != i ? row_of(base + i, &bad, false) : 0;
+            }
+            __syncthreads();
         }
-        __syncthreads();
         const int m = static_cast<int>(min(static_cast<int64_t>(kBatch), c - i0));
-        for (int64_t k = static_cast<int64_t>(blockIdx.y) * kKT + tid; k < cols * a.layers; k += static_cast<int64_t>(gridDim.y) * kKT) {
-            uint8_t* const kv = a.kv + k / cols * a.layer_bytes + k % cols * 16;
-            for (int i = 0; i < m; ++i)
-                if (from[i] != to[i]) *reinterpret_cast<uint4*>(kv + to[i]) = *reinterpret_cast<const uint4*>(kv + from[i]);
+        for (int64_t k = static_cast<int64_t>(blockIdx.y) * kKT + tid; k < static_cast<int64_t>(cols) * a.layers; k += static_cast<int64_t>(gridDim.y) * kKT) {
+            const int64_t l = quot(k, cols);
+            uint8_t* const kv = a.kv + l * a.layer_bytes + (k - l * cols) * 16;
+            for (int i = 0; i < m; i += kHeld) {
+                uint4 v[kHeld];
+#pragma unroll
+                for (int h = 0; h < kHeld; ++h)
+                    if (i + h < m && from[i + h] != to[i + h]) v[h] = *reinterpret_cast<const uint4*>(kv + from[i + h]);
+#pragma unroll
+                for (int h = 0; h < kHeld; ++h)
+                    if (i + h < m && from[i + h] != to[i + h]) *reinterpret_cast<uint4*>(kv + to[i + h]) = v[h];
+            }
         }
     }
 }
@@ -506,6 +593,7 @@ PoolArgs pool_args(const echo_page_pool* p, int64_t n_tokens) {
     a.layers = p->layers;
     a.page = p->page;
     a.entries = n_tokens / p->page + (n_tokens % p->page != 0);
+    a.wide = is_aligned(p->refs, 16);
     return a;
 }
 
@@ -518,6 +606,8 @@ unsigned entry_blocks(const PoolArgs& a, int B) {
     const int64_t n = (a.entries / B + kFT - 1) / kFT;
     return static_cast<unsigned>(n < 1 ? 1 : n > 64 ? 64 : n);
 }
+
+unsigned layer_blocks(const PoolArgs& a) { return static_cast<unsigned>(a.layers < 8 ? a.layers : 8); }
 
 }  // namespace
 }  // namespace echo
@@ -553,9 +643,8 @@ extern "C" int echo_pages_reserve(int B, const int64_t* tok_off, const int64_t* 
     const PoolArgs a = pool_args(pool, n_tokens);
     const Work w = work_of(ws, B, pool->n_pages > B ? pool->n_pages : B);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    pages_reserve_kernel<<<1, kPlanT, 0, s>>>(a, B, tok_off, tok_end, want, n_tokens, room, w, status);
+    pages_reserve_kernel<<<kReserveCtas, kPlanT, 0, s>>>(a, B, tok_off, tok_end, want, n_tokens, room, w, status);
     ECHO_CUDA_OK(cudaGetLastError());
-    ECHO_CUDA_OK(launch_after(false, pages_move_kernel, dim3(static_cast<unsigned>(2 * sm_count())), kMT, 0, s, a, w));
     return ECHO_OK;
 }
 
@@ -576,7 +665,7 @@ extern "C" int echo_pages_fork(int n, const int32_t* src, const int32_t* dst, in
     pages_share_kernel<<<dim3(n, entry_blocks(a, B)), kFT, 0, s>>>(a, f, w, status);
     ECHO_CUDA_OK(cudaGetLastError());
     ECHO_CUDA_OK(launch_after(false, pages_tails_kernel, dim3(1), kPlanT, 0, s, a, f, w, status));
-    ECHO_CUDA_OK(launch_after(false, pages_move_kernel, dim3(static_cast<unsigned>(2 * sm_count())), kMT, 0, s, a, w));
+    ECHO_CUDA_OK(launch_after(false, pages_move_kernel, dim3(static_cast<unsigned>(sm_count()), layer_blocks(a)), kMT, 0, s, a, w));
     return ECHO_OK;
 }
 
@@ -592,7 +681,7 @@ extern "C" int echo_pages_compact(int64_t n_tokens, const echo_page_pool* pool, 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     pages_compact_kernel<<<1, kPlanT, 0, s>>>(a, used, w);
     ECHO_CUDA_OK(cudaGetLastError());
-    ECHO_CUDA_OK(launch_after(false, pages_place_kernel, dim3(static_cast<unsigned>(8 * sm_count())), kMT, 0, s, a, const_cast<const int32_t*>(used), w, status));
+    ECHO_CUDA_OK(launch_after(false, pages_place_kernel, dim3(static_cast<unsigned>((8 * sm_count() + layer_blocks(a) - 1) / layer_blocks(a)), layer_blocks(a)), kMT, 0, s, a, const_cast<const int32_t*>(used), w, status));
     return ECHO_OK;
 }
 
