@@ -40,10 +40,21 @@ struct Work {
     int32_t* list;    // [n_pages]
     int32_t* map;     // [n_pages]
     int32_t* far;     // [n_pages]
+    struct Tail* tail;  // [requests of the call]
+};
+
+// What a pair of a fork has behind the shared pages.
+struct __align__(32) Tail {
+    int64_t entry;    // dst's entry of the partly used page
+    int64_t end;      // dst's end without its rows
+    int32_t dst;      // -1: the pair is left out
+    int32_t page;     // src's page of them, -1: none
+    int32_t rows;
+    int32_t reserved;
 };
 
 struct WorkLayout {
-    size_t move, list, map, far, total;
+    size_t move, list, map, far, tail, total;
 };
 inline WorkLayout work_layout(int B, int64_t n_pages) {
     WorkLayout l;
@@ -51,14 +62,16 @@ inline WorkLayout work_layout(int B, int64_t n_pages) {
     l.list = round_up(l.move + static_cast<size_t>(B) * sizeof(Move), 256);
     l.map = round_up(l.list + static_cast<size_t>(n_pages) * 4, 256);
     l.far = round_up(l.map + static_cast<size_t>(n_pages) * 4, 256);
-    l.total = round_up(l.far + static_cast<size_t>(n_pages) * 4, 256);
+    l.tail = round_up(l.far + static_cast<size_t>(n_pages) * 4, 256);
+    l.total = round_up(l.tail + static_cast<size_t>(B) * sizeof(Tail), 256);
     return l;
 }
 inline Work work_of(void* ws, int B, int64_t n_pages) {
     const WorkLayout l = work_layout(B, n_pages);
     uint8_t* const w = static_cast<uint8_t*>(ws);
     return Work{reinterpret_cast<int32_t*>(w), reinterpret_cast<Move*>(w + l.move), reinterpret_cast<int32_t*>(w + l.list),
-                reinterpret_cast<int32_t*>(w + l.map), reinterpret_cast<int32_t*>(w + l.far)};
+                reinterpret_cast<int32_t*>(w + l.map), reinterpret_cast<int32_t*>(w + l.far),
+                reinterpret_cast<Tail*>(w + l.tail)};
 }
 
 // x / d and x % d for an x >= 0, by a 32-bit division where that does (the 64-bit one takes some 100 instructions).
@@ -153,30 +166,31 @@ __global__ void __launch_bounds__(kFT)
 // ---------------------------------------------------------------- the block that plans
 constexpr int kPlanT = 1024;
 
-// The counts of 16 pages from p on (1 behind the last).
-__device__ __forceinline__ void counts_of(const PoolArgs& a, int64_t p, int32_t (&r)[16]) {
-    if (p + 16 <= a.n_pages && a.wide) {
+constexpr int kRun = 4;   // (16 made the plans 2 to 4 us slower on pools of 3000 to 8500 pages: more code to fetch, fewer threads at work)
+// The counts of kRun pages from p on (1 behind the last).
+__device__ __forceinline__ void counts_of(const PoolArgs& a, int64_t p, int32_t (&r)[kRun]) {
+    if (p + kRun <= a.n_pages && a.wide) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<int4*>(r + 4 * i) = reinterpret_cast<const int4*>(a.refs + p)[i];
+        for (int i = 0; i < kRun / 4; ++i) *reinterpret_cast<int4*>(r + 4 * i) = reinterpret_cast<const int4*>(a.refs + p)[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = p + i < a.n_pages ? a.refs[p + i] : 1;
+        for (int i = 0; i < kRun; ++i) r[i] = p + i < a.n_pages ? a.refs[p + i] : 1;
     }
 }
 
 // Lists the first `most` free pages, ascending; returns how many there are up to `most`.  A block together.
 __device__ __forceinline__ int64_t list_free(const PoolArgs& a, int64_t most, int32_t* list, uint32_t* scratch) {
     int64_t found = 0;
-    for (int64_t p0 = 0; p0 < a.n_pages && found < most; p0 += 16 * kPlanT) {
-        const int64_t p = p0 + 16 * threadIdx.x;
-        int32_t r[16];
+    for (int64_t p0 = 0; p0 < a.n_pages && found < most; p0 += kRun * kPlanT) {
+        const int64_t p = p0 + kRun * threadIdx.x;
+        int32_t r[kRun];
         counts_of(a, p, r);
         uint32_t n = 0, total;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) n += r[i] == 0;
+        for (int i = 0; i < kRun; ++i) n += r[i] == 0;
         int64_t at = found + block_exclusive_scan<kPlanT>(n, scratch, &total);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < kRun; ++i)
             if (r[i] == 0) {
                 if (at < most) list[at] = static_cast<int32_t>(p + i);
                 ++at;
@@ -201,100 +215,150 @@ __device__ __forceinline__ bool needs_page(const PoolArgs& a, int64_t e, bool* b
     return r > 1;
 }
 
-// A cluster: its first CTA plans, all of it copies what a copy on write has to (one launch; most calls copy nothing).
+// A cluster: its first CTA plans, 1024 requests at a time, all of it copies what a copy on write has to (one launch; most calls
+// copy nothing).  kWidth lanes look through a request's entries, eight when no request grows over more.
 constexpr int kReserveCtas = 8;
+
+struct ReserveSmem {
+    int64_t scratch64[kPlanT / 32];
+    uint32_t scratch[kPlanT / 32 + 1];
+    int64_t first[kPlanT];   // a request's entries that new tokens fall in: the first, how many, and rows in it already
+    int32_t entries[kPlanT];
+    int32_t part[kPlanT];
+    int32_t need[kPlanT];    // pages it needs, -1: inconsistent; then where its pages begin, -1: none
+    uint32_t mask[kPlanT];   // of its first 32 entries, those that need one
+    int moves;
+};
+
+// Which of a request's entries [at, at + kWidth) need a page, a bit each in its lanes (of request i of the batch; -1: none).
+template <int kWidth>
+__device__ __forceinline__ uint32_t entries_in_need(const PoolArgs& a, const ReserveSmem& sm, int i, int at, int32_t* page, bool* bad) {
+    const int lane = threadIdx.x & 31, sub = lane % kWidth;
+    bool it = false;
+    if (i >= 0 && at + sub < sm.entries[i]) {
+        it = needs_page(a, sm.first[i] + at + sub, bad, page);
+        if (it && *page < 0 && at + sub == 0 && sm.part[i] > 0) *bad = true;  // its rows are nowhere
+    }
+    return (__ballot_sync(0xffffffffu, it) >> (lane - sub)) & (kWidth == 32 ? 0xFFFFFFFFu : (1u << kWidth) - 1u);
+}
+
+template <int kWidth>
+__device__ __forceinline__ void count_needs(const PoolArgs& a, ReserveSmem& sm, int requests) {
+    const int lane = threadIdx.x & 31, sub = lane % kWidth;
+    for (int i0 = (threadIdx.x >> 5) * (32 / kWidth); i0 < requests; i0 += kPlanT / kWidth) {
+        const int i = i0 + lane / kWidth < requests ? i0 + lane / kWidth : -1;
+        int most = i >= 0 ? sm.entries[i] : 0, n = 0;
+#pragma unroll
+        for (int o = kWidth; o < 32; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        bool bad = false;
+        for (int at = 0; at < most; at += kWidth) {
+            int32_t p;
+            const uint32_t m = entries_in_need<kWidth>(a, sm, i, at, &p, &bad);
+            if (at == 0 && sub == 0 && i >= 0) sm.mask[i] = m;
+            n += __popc(m);
+        }
+#pragma unroll
+        for (int o = 1; o < kWidth; o <<= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o) != 0;
+        if (i >= 0 && sub == 0 && sm.need[i] >= 0) sm.need[i] = bad ? -1 : n;
+    }
+}
+
+template <int kWidth>
+__device__ __forceinline__ void hand_out(const PoolArgs& a, ReserveSmem& sm, const Work& w, int64_t given, int requests) {
+    const int lane = threadIdx.x & 31, sub = lane % kWidth;
+    for (int i0 = (threadIdx.x >> 5) * (32 / kWidth); i0 < requests; i0 += kPlanT / kWidth) {
+        const int i = i0 + lane / kWidth < requests && sm.need[i0 + lane / kWidth] >= 0 ? i0 + lane / kWidth : -1;
+        const int len = i >= 0 ? sm.entries[i] : 0;
+        int64_t k0 = i >= 0 ? sm.need[i] : 0;
+        int most = len;
+#pragma unroll
+        for (int o = kWidth; o < 32; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        for (int at = 0; at < most; at += kWidth) {
+            int32_t p = -1;
+            bool bad = false;
+            uint32_t m;
+            if (kWidth == 8 || most <= 32) {  // known from the count
+                m = at < len ? sm.mask[i] : 0u;
+                if ((m >> sub) & 1u) p = a.tab[sm.first[i] + sub];
+            } else {
+                m = entries_in_need<kWidth>(a, sm, i, at, &p, &bad);
+            }
+            if ((m >> sub) & 1u) {
+                const int64_t e = sm.first[i] + at + sub, k = k0 + __popc(m & ((1u << sub) - 1u));
+                const int32_t to = w.list[k];
+                a.tab[e] = to;
+                a.refs[to] = 1;
+                w.map[given + k] = p;
+                if (p >= 0 && at + sub == 0 && sm.part[i] > 0)
+                    w.move[atomicAdd(&sm.moves, 1)] =
+                        Move{static_cast<int64_t>(p) * a.page, static_cast<int64_t>(to) * a.page, sm.part[i], 0};
+            }
+            k0 += __popc(m);
+        }
+    }
+}
+
 __global__ void __cluster_dims__(kReserveCtas, 1, 1) __launch_bounds__(kPlanT)
     pages_reserve_kernel(PoolArgs a, int B, const int64_t* __restrict__ tok_off, const int64_t* __restrict__ tok_end,
                          const int64_t* __restrict__ want, int64_t n_tokens, int64_t* __restrict__ room, Work w, int32_t* status) {
-    __shared__ int64_t scratch64[kPlanT / 32];
-    __shared__ uint32_t scratch[kPlanT / 32 + 1];
-    __shared__ int32_t need[ECHO_MAX_REQUESTS];
-    __shared__ int s_moves, s_given;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ ReserveSmem sm;
+    const int tid = threadIdx.x;
     if (blockIdx.x == 0) {
-        if (tid == 0) s_moves = s_given = 0;
-        // ---- how many pages every request needs, a warp to each; -1: none, it is inconsistent
-        for (int b = warp; b < B; b += kPlanT / 32) {
-            Region r;
-            const int64_t to = want[b];
-            bool ok = region_of(tok_off, tok_end, n_tokens, a.page, b, &r) && to >= r.end && to <= r.last;
-            int64_t n = 0;
-            if (ok && to > r.end) {
-                const int64_t e0 = quot(r.end, a.page), e1 = pages_to(to, a.page);
-                const bool part = rest(r.end, a.page) > 0;
-                bool bad = false;
-                for (int64_t base = e0; base < e1; base += 32) {
-                    const int64_t e = base + lane;
-                    int32_t p;
-                    const bool it = e < e1 && needs_page(a, e, &bad, &p);
-                    if (it && p < 0 && e == e0 && part) bad = true;  // its rows are nowhere
-                    n += __popc(__ballot_sync(0xffffffffu, it));
-                }
-                ok = !__any_sync(0xffffffffu, bad);
-            }
-            if (lane == 0) {
-                need[b] = ok ? static_cast<int32_t>(min(n, static_cast<int64_t>(0x7FFFFFFF))) : -1;
-                if (!ok) set_status(status, ECHO_ST_BADDATA);
-            }
-        }
-        __syncthreads();
-        // ---- the free pages
-        int64_t mine = 0;
-        for (int b = tid; b < B; b += kPlanT) mine += max(need[b], 0);
-        int64_t total;
-        (void)block_scan64<kPlanT>(mine, scratch64, &total);
-        const int64_t most = min(total, a.n_pages);
-        const int64_t have = list_free(a, most, w.list, scratch);
-        // ---- where each request's begin, or that it goes without
-        int64_t base = 0;
+        if (tid == 0) sm.moves = 0;
+        int64_t given = 0;  // pages handed out
         bool full = false;
         for (int b0 = 0; b0 < B; b0 += kPlanT) {
-            const int b = b0 + tid;
-            const int64_t n = b < B ? max(need[b], 0) : 0;
-            int64_t sum;
-            __syncthreads();
-            const int64_t at = base + block_scan64<kPlanT>(n, scratch64, &sum);
-            base += sum;
+            const int b = b0 + tid, requests = min(B - b0, kPlanT);
+            // ---- the entries every request grows over
+            int64_t end = 0, to = 0;
+            bool ok = false, many = false;
             if (b < B) {
-                const bool served = need[b] >= 0 && (n == 0 || at + n <= have);
-                full |= need[b] >= 0 && !served;
-                if (room) room[b] = served ? want[b] : tok_end[b];
-                need[b] = served && n > 0 ? static_cast<int32_t>(at) : -1;
-                if (served && n > 0) atomicMax(&s_given, static_cast<int>(at + n));
+                Region r;
+                to = want[b];
+                ok = region_of(tok_off, tok_end, n_tokens, a.page, b, &r) && to >= r.end && to <= r.last;
+                end = r.end;
+                int64_t first = 0, n = 0;
+                if (ok && to > end) {
+                    first = quot(end, a.page);
+                    n = pages_to(to, a.page) - first;
+                }
+                many = n > 8;
+                sm.first[tid] = first;
+                sm.entries[tid] = static_cast<int32_t>(min(n, static_cast<int64_t>(0x7FFFFFC0)));
+                sm.part[tid] = static_cast<int32_t>(end - first * a.page);
+                sm.need[tid] = ok ? 0 : -1;
             }
+            many = __syncthreads_or(many);
+            if (many) count_needs<32>(a, sm, requests);
+            else count_needs<8>(a, sm, requests);
+            __syncthreads();
+            // ---- the free pages, and where each request's begin
+            const int32_t mine = b < B ? sm.need[tid] : -1;
+            if (b < B && mine < 0) set_status(status, ECHO_ST_BADDATA);
+            int64_t total;
+            const int64_t at = block_scan64<kPlanT>(max(mine, 0), sm.scratch64, &total);
+            const bool before = __syncthreads_or(full);  // an earlier batch's request went without
+            const int64_t have = before ? 0 : list_free(a, min(total, a.n_pages), w.list, sm.scratch);
+            bool served = false;
+            if (b < B) {
+                served = mine == 0 || (mine > 0 && at + mine <= have);
+                full |= mine > 0 && !served;
+                if (room) room[b] = served ? to : end;
+                sm.need[tid] = served && mine > 0 ? static_cast<int32_t>(at) : -1;
+            }
+            // the requests served are the first of those in need: their pages are the first of the list
+            int64_t here;
+            (void)block_scan64<kPlanT>(served ? max(mine, 0) : 0, sm.scratch64, &here);
+            // ---- handed out; the counts of the pages replaced fall when all have been, since two requests may replace the same one
+            if (many) hand_out<32>(a, sm, w, given, requests);
+            else hand_out<8>(a, sm, w, given, requests);
+            given += here;
+            __syncthreads();
         }
         if (full) set_status(status, ECHO_ST_FULL);
-        __syncthreads();
-        // ---- handed out; the counts of the pages replaced fall when all have been, since two requests may replace the same one
-        for (int b = warp; b < B; b += kPlanT / 32) {
-            int64_t at = need[b];
-            if (at < 0) continue;
-            Region r;
-            (void)region_of(tok_off, tok_end, n_tokens, a.page, b, &r);
-            const int64_t e0 = quot(r.end, a.page), e1 = pages_to(want[b], a.page);
-            const int part = rest(r.end, a.page);
-            for (int64_t first = e0; first < e1; first += 32) {
-                const int64_t e = first + lane;
-                int32_t p = -1;
-                bool bad = false;
-                const bool it = e < e1 && needs_page(a, e, &bad, &p);
-                const uint32_t m = __ballot_sync(0xffffffffu, it);
-                if (it) {
-                    const int64_t k = at + __popc(m & ((1u << lane) - 1u));
-                    const int32_t to = w.list[k];
-                    a.tab[e] = to;
-                    a.refs[to] = 1;
-                    w.map[k] = p;
-                    if (p >= 0 && e == e0 && part)
-                        w.move[atomicAdd(&s_moves, 1)] = Move{static_cast<int64_t>(p) * a.page, static_cast<int64_t>(to) * a.page, part, 0};
-                }
-                at += __popc(m);
-            }
-        }
-        __syncthreads();
-        for (int k = tid; k < s_given; k += kPlanT)
+        for (int64_t k = tid; k < given; k += kPlanT)
             if (w.map[k] >= 0) drop_ref(a, w.map[k], status);
-        if (tid == 0) *w.moves = s_moves;
+        if (tid == 0) *w.moves = sm.moves;
     }
     cluster_sync_all();
     move_all<kPlanT>(a, w.move, static_cast<uint32_t>(*w.moves), blockIdx.x, kReserveCtas, 0, 1);
@@ -331,14 +395,22 @@ __global__ void __launch_bounds__(kFT) pages_share_kernel(PoolArgs a, ForkArgs f
     const int i = blockIdx.x;
     Region from, to;
     const bool ok = fork_pair(f, a.page, i, &from, &to);
-    if (threadIdx.x == 0 && blockIdx.y == 0) {
-        w.map[i] = ok;
-        if (!ok) set_status(status, ECHO_ST_BADDATA);
+    if (!ok) {
+        if (threadIdx.x == 0 && blockIdx.y == 0) {
+            w.tail[i].dst = -1;
+            set_status(status, ECHO_ST_BADDATA);
+        }
+        return;
     }
-    if (!ok) return;
     const int64_t full = quot(from.end - from.off, a.page), entries = pages_to(to.last, a.page) - quot(to.off, a.page);
     const int32_t* const s = a.tab + quot(from.off, a.page);
     int32_t* const d = a.tab + quot(to.off, a.page);
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
+        const int over = static_cast<int>(from.end - from.off - full * a.page);
+        const int32_t p = over ? s[full] : -1;
+        if (p >= 0 && !in_pool(a, p)) set_status(status, ECHO_ST_BADDATA);
+        w.tail[i] = Tail{quot(to.off, a.page) + full, to.off + full * a.page, f.dst[i], in_pool(a, p) ? p : -1, over, 0};
+    }
     for (int64_t e = static_cast<int64_t>(blockIdx.y) * kFT + threadIdx.x; e < entries; e += static_cast<int64_t>(gridDim.y) * kFT) {
         const int32_t old = d[e];
         int32_t p = e < full ? s[e] : -1;
@@ -357,56 +429,29 @@ __global__ void __launch_bounds__(kPlanT) pages_tails_kernel(PoolArgs a, ForkArg
     __shared__ uint32_t scratch[kPlanT / 32 + 1];
     const int tid = threadIdx.x;
     pdl_wait();
-    uint32_t total = 0;
+    uint32_t given = 0;
+    bool full = false;
     for (int i0 = 0; i0 < f.n; i0 += kPlanT) {
-        const int i = i0 + tid;
-        bool it = false;
-        if (i < f.n && w.map[i]) {
-            const int64_t off = f.tok_off[f.src[i]], n = f.tok_end[f.src[i]] - off;
-            it = rest(n, a.page) && in_pool(a, a.tab[quot(off, a.page) + quot(n, a.page)]);
+        Tail t = {0, 0, -1, -1, 0, 0};
+        if (i0 + tid < f.n) t = w.tail[i0 + tid];
+        const bool it = t.dst >= 0 && t.page >= 0;
+        uint32_t total;
+        const uint32_t at = block_exclusive_scan<kPlanT>(it, scratch, &total);
+        const int64_t have = list_free(a, min(static_cast<int64_t>(total), a.n_pages), w.list, scratch);
+        const bool without = it && at >= have;
+        if (it && !without) {
+            const int32_t to = w.list[at];
+            a.tab[t.entry] = to;
+            a.refs[to] = 1;
+            w.move[given + at] = Move{static_cast<int64_t>(t.page) * a.page, static_cast<int64_t>(to) * a.page, t.rows, 0};
         }
-        uint32_t sum;
-        (void)block_exclusive_scan<kPlanT>(it, scratch, &sum);
-        total += sum;
-    }
-    const int64_t have = list_free(a, min(static_cast<int64_t>(total), a.n_pages), w.list, scratch);
-    uint32_t base = 0;
-    bool full = false, bad = false;
-    for (int i0 = 0; i0 < f.n; i0 += kPlanT) {
-        const int i = i0 + tid;
-        int64_t n = 0, over = 0, off = 0, to_off = 0;
-        int32_t p = -1;
-        const bool ok = i < f.n && w.map[i];
-        if (ok) {
-            off = f.tok_off[f.src[i]];
-            n = f.tok_end[f.src[i]] - off;
-            over = rest(n, a.page);
-            to_off = f.tok_off[f.dst[i]];
-            if (over) {
-                p = a.tab[quot(off, a.page) + quot(n, a.page)];
-                bad |= p >= 0 && !in_pool(a, p);
-            }
-        }
-        const bool it = in_pool(a, p);
-        uint32_t sum;
-        const uint32_t at = base + block_exclusive_scan<kPlanT>(it, scratch, &sum);
-        if (it) {
-            if (at < have) {
-                const int32_t to = w.list[at];
-                a.tab[quot(to_off, a.page) + quot(n, a.page)] = to;
-                a.refs[to] = 1;
-                w.move[at] = Move{static_cast<int64_t>(p) * a.page, static_cast<int64_t>(to) * a.page, over, 0};
-            } else {
-                full = true;
-                n -= over;
-            }
-        }
-        if (ok) f.tok_end[f.dst[i]] = to_off + n;
-        base += sum;
+        full |= without;
+        if (t.dst >= 0) f.tok_end[t.dst] = t.end + (without ? 0 : t.rows);
+        given += static_cast<uint32_t>(have);
+        __syncthreads();
     }
     if (full) set_status(status, ECHO_ST_FULL);
-    if (bad) set_status(status, ECHO_ST_BADDATA);
-    if (tid == 0) *w.moves = static_cast<int32_t>(have);
+    if (tid == 0) *w.moves = static_cast<int32_t>(given);
 }
 
 // ---------------------------------------------------------------- compact
@@ -416,45 +461,50 @@ __global__ void __launch_bounds__(kPlanT) pages_compact_kernel(PoolArgs a, int32
     __shared__ uint32_t scratch[kPlanT / 32 + 1];
     const int tid = threadIdx.x;
     uint32_t mine = 0, U;
-    int32_t r[16];
-    for (int64_t p0 = 0; p0 < a.n_pages; p0 += 16 * kPlanT) {
-        counts_of(a, p0 + 16 * tid, r);
+    int32_t r[kRun];
+    for (int64_t p0 = 0; p0 < a.n_pages; p0 += kRun * kPlanT) {
+        counts_of(a, p0 + kRun * tid, r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mine += r[i] > 0 && p0 + 16 * tid + i < a.n_pages;
+        for (int i = 0; i < kRun; ++i) mine += r[i] > 0 && p0 + kRun * tid + i < a.n_pages;
     }
     (void)block_exclusive_scan<kPlanT>(mine, scratch, &U);
     uint32_t holes = 0, far = 0;
-    for (int64_t p0 = 0; p0 < U; p0 += 16 * kPlanT) {
-        const int64_t p = p0 + 16 * tid;
+    for (int64_t p0 = 0; p0 < U; p0 += kRun * kPlanT) {
+        const int64_t p = p0 + kRun * tid;
         counts_of(a, p, r);
         uint32_t n = 0, total;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) n += r[i] <= 0 && p + i < U;
+        for (int i = 0; i < kRun; ++i) n += r[i] <= 0 && p + i < U;
         uint32_t at = holes + block_exclusive_scan<kPlanT>(n, scratch, &total);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < kRun; ++i)
             if (r[i] <= 0 && p + i < U) w.list[at++] = static_cast<int32_t>(p + i);
         holes += total;
     }
     __syncthreads();
-    for (int64_t p0 = U & ~15u; p0 < a.n_pages; p0 += 16 * kPlanT) {
-        const int64_t p = p0 + 16 * tid;
+    for (int64_t p0 = U & ~(kRun - 1u); p0 < a.n_pages; p0 += kRun * kPlanT) {
+        const int64_t p = p0 + kRun * tid;
         counts_of(a, p, r);
         uint32_t n = 0, total;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) n += r[i] > 0 && p + i >= U && p + i < a.n_pages;
+        for (int i = 0; i < kRun; ++i) n += r[i] > 0 && p + i >= U && p + i < a.n_pages;
         uint32_t at = far + block_exclusive_scan<kPlanT>(n, scratch, &total);
+        int32_t to[kRun];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < kRun; ++i) {  // all loads before a store
+            to[i] = -1;
+            if (r[i] > 0 && p + i >= U && p + i < a.n_pages) to[i] = w.list[at++];
+        }
+        at -= n;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
             if (p + i < U || p + i >= a.n_pages) continue;
-            int32_t to = -1;
-            if (r[i] > 0) {
-                to = w.list[at];
+            if (to[i] >= 0) {
                 w.far[at++] = static_cast<int32_t>(p + i);
-                a.refs[to] = r[i];
+                a.refs[to[i]] = r[i];
                 a.refs[p + i] = 0;
             }
-            w.map[p + i] = to;
+            w.map[p + i] = to[i];
         }
         far += total;
     }
