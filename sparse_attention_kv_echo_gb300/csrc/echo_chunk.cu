@@ -73,6 +73,8 @@ constexpr int kInline = 32;              // groups and requests of a call that n
 constexpr float kLazy = 8.f;
 constexpr int kOver = 3;                 // a group's fixed cost in tiles
 constexpr int kMinUnits = 2;             // least units per cluster
+constexpr int kMinTreeUnits = 4;         // of a tree's call: it has several rows, whose parts the join reads (8 nodes over
+                                         // 1000 tokens: 2 units 23.6 us, 4 21.6, 6 23.7, 10 26.9)
 constexpr int kMaxClusters = 96;         // bounds the workspace (the device has 76 pairs of SMs)
 constexpr uint32_t kIdescS = idesc_bf16_f32(kM, kTok);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kM, 256) | (1u << 16);  // B (V) MN-major
@@ -118,6 +120,7 @@ struct Plan {
     int cap;
     int clusters;
     bool small;     // at most kInline groups and requests: no plan kernel
+    int least;      // units per cluster
     int ahead;      // tiles that K rows are brought to L2 ahead of their copy, 0: not
 };
 
@@ -174,12 +177,12 @@ __device__ __forceinline__ Group make_group(const ChunkArgs& a, int b, int64_t r
     return r;
 }
 
-__device__ __forceinline__ PlanHead make_head(int64_t total, int groups, int clusters) {
+__device__ __forceinline__ PlanHead make_head(int64_t total, int groups, const Plan& plan) {
     PlanHead h;
     h.total = total;
     h.groups = groups;
     h.parts =
-        static_cast<int32_t>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(clusters), total / kMinUnits)));
+        static_cast<int32_t>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(plan.clusters), total / plan.least)));
     return h;
 }
 
@@ -233,7 +236,7 @@ __device__ __forceinline__ void plan_small(const ChunkArgs& a, const Plan& plan,
     if (lane < groups) cum[lane] = at - cost;
     if (lane == 0) {
         cum[groups] = total;
-        *head = make_head(total, groups, plan.clusters);
+        *head = make_head(total, groups, plan);
     }
 }
 
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kPT) chunk_plan_kernel(ChunkArgs a, Plan plan)
     }
     if (tid == 0) {
         plan.cum[groups] = sum;
-        *plan.head = make_head(sum, groups, plan.clusters);
+        *plan.head = make_head(sum, groups, plan);
     }
 }
 
@@ -1141,6 +1144,7 @@ int launch_chunk(const ChunkArgs& a, uint16_t* out, float* lse, void* ws, size_t
     plan.cum = reinterpret_cast<int64_t*>(w + l.cum);
     plan.part = w + l.part;
     plan.cap = static_cast<int>(cap);
+    plan.least = kTree ? kMinTreeUnits : kMinUnits;
     plan.ahead = cap <= 2 * B ? kAhead : 0;
     CUtensorMap qmap;
     if (encode_tmap_bytes_2d(&qmap, a.q, kLatRowBytes, static_cast<uint64_t>(n_rows) * heads, 128, 64)) return ECHO_ECUDA;
@@ -1154,7 +1158,8 @@ int launch_chunk(const ChunkArgs& a, uint16_t* out, float* lse, void* ws, size_t
         chunk_plan_kernel<<<1, kPT, 0, s>>>(a, plan);
         ECHO_CUDA_OK(cudaGetLastError());
     }
-    ECHO_CUDA_OK(launch_after(plan.small, chunk_kernel<kTree>, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan, qmap,
+    // (a tree's call comes behind the one that made its masks, whose kernel lets it start; nothing is read before that has ended)
+    ECHO_CUDA_OK(launch_after(plan.small && !kTree, chunk_kernel<kTree>, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan, qmap,
                               a.scale * 1.4426950408889634f, out, lse));
     if (plan.clusters > 1)
         ECHO_CUDA_OK(launch_after(false, chunk_join_kernel, dim3(static_cast<unsigned>(8 * sm_count())), kJT, 0, s, a, plan, out, lse));

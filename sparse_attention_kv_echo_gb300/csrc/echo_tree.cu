@@ -15,6 +15,7 @@ __global__ void __launch_bounds__(kTreeThreads)
     tree_masks_kernel(int B, const int64_t* __restrict__ row_off, int64_t n_rows, const int32_t* __restrict__ parent, int words,
                       uint32_t* __restrict__ mask, int32_t* __restrict__ depth, int32_t* status) {
     __shared__ int16_t up[ECHO_TREE_MAX_NODES];
+    pdl_launch_dependents();
     for (int b = blockIdx.x; b < B; b += gridDim.x) {
         const int64_t r0 = row_off[b], r1 = row_off[b + 1], n = r1 - r0;
         if (r0 < 0 || r1 < r0 || r1 > n_rows) {
