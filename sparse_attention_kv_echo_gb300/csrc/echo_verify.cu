@@ -9,17 +9,18 @@
 // without the tokens rejected so far.
 //
 // A cluster of CTAs works on a request: each has a slice of the vocabulary, a warp of it a
-// slice of that, read 16 bytes a lane.  CTA 0 reads the tree and each node's own probabilities
-// in its parent's rows and hands them to all; then every CTA walks (a warp; the children of a node are
-// found by ballot among 32 parents at a time) and the cluster sums where a child is rejected:
-// one cluster barrier a rejection, behind which all CTAs know all slices' sums and go on
-// alike.  At the end the token behind the path is drawn, from the last rejection's sums when no
-// child was accepted since: the slice whose running sum passes u * total, in it the warp's, in that
-// one sixteenth, in that the token.
-// Values are 64-bit integers in units of 2^-60, so sums do not hang on their order, and
-// the token drawn is the same on any number of CTAs.  They are made by shifts: conversions
-// to 64-bit integers ran at a small fraction of the rate of integer operations (64 chains of six over
-// 131072 tokens took 96 us with them).
+// slice of that, read 16 bytes a lane.  CTA 0 reads the tree, each node's own probabilities
+// in its parent's rows and whether it would be accepted as a first child, and hands them to all; then every CTA walks (a
+// warp; the children of a node are found by ballot among 32 parents at a time) and the cluster sums where a
+// child is rejected: one cluster barrier a rejection, behind which all CTAs know all slices'
+// sums and go on alike.  At the end the token behind the path is drawn, from the last rejection's
+// sums when no child was accepted since: the slice whose running sum passes u * total, in it the
+// warp's, in that the part that a warp of the CTA now takes, in that the token.
+//
+// Sums are of whole numbers, so they do not hang on their order, and the token drawn is the same on
+// any number of CTAs.  What bounds the call: a few chains or trees, the latency of its steps (one chain of five
+// over 32000 tokens: 1.9 us to read the tree, 0.5 a walk, 2 a sum with its barrier, 2 the draw); many, the
+// instructions of the sums, some 10 a token and pair of values.
 #include <cuda_bf16.h>
 
 #include "echo_common.cuh"
@@ -32,7 +33,7 @@ constexpr int kVT = 384;
 constexpr int kVWarps = kVT / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kNodes = ECHO_TREE_MAX_NODES;
-constexpr int kTile = 8;                 // tokens a lane works on at a time
+constexpr int kTile = 8;                 // tokens a lane works on at a time (16: more registers, 2 CTAs an SM no longer without spills)
 
 struct VerifyArgs {
     const int64_t* row_off;
@@ -55,24 +56,40 @@ enum Ask : int { kSum, kBest, kEnd };
 
 constexpr uint64_t kOne = 1ull << 50;  // S = 1
 
+// Row `row` of the [n_rows, vocab] matrices target and draft as 16-byte pieces on 16-byte boundaries: piece j holds
+// the tokens first(j) .. first(j) + n - 1, of which the first and the last piece may have some outside the row.
+struct Row {
+    const uint8_t* base;  // of the target's piece 0, at or before the row's first element
+    int64_t to_draft;     // bytes from there to the draft's
+    int vocab;
+    int shift;            // elements of piece 0 before the row
+    int pieces;
+    int inner;            // pieces [1, inner) lie within the row and the matrix
+    int whole;            // pieces [0, whole) lie within the matrix
+    int per;              // pieces of a warp's slice
+};
+
 struct VerifySmem {
     // from CTA 0: the tree
     int64_t r0;
     int32_t n;
     float u_pick;
     int16_t up[kNodes];
+    uint16_t yes[kNodes];          // accepted as a first child
     int32_t tok[kNodes];
     float u[kNodes], p[kNodes], d[kNodes];  // a node's uniform number, its token's probabilities in its parent's rows
     // from every CTA: its sum or its best key, by parity of the question
     uint64_t slot[2][kMaxCluster];
     // the question
-    int ask, node, gone;
-    bool fresh;                    // the last sums are of this node and residual
+    Row row;
     uint64_t S;
+    int ask, outs;
+    bool last;                     // the child in question is its parent's last
+    bool fresh;                    // the last sums are of this node and residual
     int32_t out[kNodes];           // tokens left out (drafts without probabilities)
     // the walk of this CTA's warp 0, between its turns
     uint64_t S_at, R;              // the residual at v
-    int v, c, len, outs, best;     // node, the last child tried, nodes accepted, tokens left out, greedy: v's best
+    int v, c, len, outs_at, best;  // node, the last child tried, nodes accepted, tokens left out, greedy: v's best
     int16_t path[kNodes];
     uint64_t warp_sum[kVWarps];
     uint64_t fine[kVWarps];
@@ -104,43 +121,81 @@ __device__ __forceinline__ uint64_t minus(uint64_t p, uint64_t x) { return p > x
 // S as the sum of two floats (48 bits of it).
 struct Scale {
     float hi, lo;
-    uint64_t S;
 };
 __device__ __forceinline__ Scale scale_of(uint64_t S) {
     const float hi = __ull2float_rn(S);
     const float lo = __ll2float_rn(static_cast<int64_t>(S - __float2ull_rn(hi)));
-    return Scale{hi * 8.8817841970012523e-16f, lo * 8.8817841970012523e-16f, S};  // 2^-50
+    return Scale{hi * 8.8817841970012523e-16f, lo * 8.8817841970012523e-16f};  // 2^-50
 }
 
-// s + t is what is left of a token, max(0, p - S d), t below the last place of p or of S d.  kUnit: S is 1, or d is 0.
+// Two floats that one instruction works on.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 two(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 both(float a) { return two(a, a); }
+__device__ __forceinline__ void apart(F2 x, float* a, float* b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(x.v)); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, both(-1.f), a); }  // (exact product: rounded once)
+
+// What is left of two tokens, max(0, p - S d), is s + t, with t below the last place of p or of S d.  kUnit: S is 1, or d is 0.
 template <bool kUnit>
-__device__ __forceinline__ void left_of(float p, float d, const Scale& S, float* s, float* t) {
+__device__ __forceinline__ void left_of(F2 p, F2 d, const Scale& S, F2* s, F2* t) {
+    float p0, p1, d0, d1;
+    apart(p, &p0, &p1);
     if (kUnit) {
-        const float x = fminf(d, p);  // p >= x: what the difference loses is exact
-        *s = __fsub_rn(p, x);
-        *t = __fsub_rn(__fsub_rn(p, *s), x);
+        apart(d, &d0, &d1);
+        const F2 x = two(fminf(d0, p0), fminf(d1, p1));  // p >= x: what the difference loses is exact
+        *s = sub(p, x);
+        *t = sub(sub(p, *s), x);
     } else {
-        const float x = __fmul_rn(S.hi, d), w = __fmaf_rn(S.lo, d, __fmaf_rn(S.hi, d, -x));
-        *s = __fsub_rn(p, x);
-        *t = __fsub_rn(__fsub_rn(__fsub_rn(p, *s), x), w);
-        const bool some = p >= x && __fadd_rn(*s, *t) > 0.f;
-        *s = some ? *s : 0.f;
-        *t = some ? *t : 0.f;
+        const F2 x = mul(both(S.hi), d), w = fma(both(S.lo), d, fma(both(S.hi), d, fma(x, both(-1.f), both(0.f))));
+        const F2 a = sub(p, x), b = sub(sub(sub(p, a), x), w), sum = add(a, b);
+        float x0, x1, a0, a1, b0, b1, s0, s1;
+        apart(x, &x0, &x1);
+        apart(a, &a0, &a1);
+        apart(b, &b0, &b1);
+        apart(sum, &s0, &s1);
+        const bool some0 = p0 >= x0 && s0 > 0.f, some1 = p1 >= x1 && s1 > 0.f;
+        *s = two(some0 ? a0 : 0.f, some1 ? a1 : 0.f);
+        *t = two(some0 ? b0 : 0.f, some1 ? b1 : 0.f);
     }
 }
 
 // s + t in units of 2^-60, spread over three 32-bit numbers whose sums are exact: a constant added to a float rounds it to
-// units that the low bits then count, and the remainder, scaled up, goes the same way again.  That runs on the pipe of FFMA and
-// FADD; shifting mantissas into 64-bit numbers ran on the integers' pipe, half as wide.  What a value loses
-// is below 2^-48, the same wherever it is summed.
+// units that the low bits then count, and the remainder, scaled up, goes the same way again.  That runs two values at a time on
+// the pipe of FFMA and FADD.  (Conversions to 64-bit integers run at a fraction of that: 64 chains of six over 131072 tokens
+// took 96 us with them, 29 with shifts of the mantissas, on the integers' pipe.)  What a value loses is below 2^-48, the same
+// wherever it is summed.
 constexpr uint32_t kTopBits = 0x40000000u, kLowBits = 0x40400000u;  // of 2 and 3
 struct Units {
-    uint32_t hi, mid, lo;  // of 2^-22, 2^-44 and 2^-60, + kTopBits, kLowBits, kLowBits
+    uint32_t hi[2], mid[2], lo[2];  // of 2^-22, 2^-44 and 2^-60, + kTopBits, kLowBits, kLowBits
 };
-__device__ __forceinline__ Units spread(float s, float t) {
-    const float y = __fadd_rn(s, 2.f), r = __fadd_rn(__fsub_rn(s, __fsub_rn(y, 2.f)), t);
-    const float z = __fmaf_rn(r, 4194304.f, 3.f), q = __fmaf_rn(r, 4194304.f, __fsub_rn(3.f, z));
-    return Units{__float_as_uint(y), __float_as_uint(z), __float_as_uint(__fmaf_rn(q, 65536.f, 3.f))};
+__device__ __forceinline__ Units spread(F2 s, F2 t) {
+    const F2 y = add(s, both(2.f)), r = add(add(s, fma(y, both(-1.f), both(2.f))), t);
+    const F2 z = fma(r, both(4194304.f), both(3.f)), q = fma(r, both(4194304.f), fma(z, both(-1.f), both(3.f)));
+    const F2 l = fma(q, both(65536.f), both(3.f));
+    return Units{{static_cast<uint32_t>(y.v), static_cast<uint32_t>(y.v >> 32)},
+                 {static_cast<uint32_t>(z.v), static_cast<uint32_t>(z.v >> 32)},
+                 {static_cast<uint32_t>(l.v), static_cast<uint32_t>(l.v >> 32)}};
 }
 // The sum of n values from the sums of their parts.
 __device__ __forceinline__ uint64_t together(uint32_t n, uint32_t hi, uint32_t mid, uint32_t lo) {
@@ -181,43 +236,36 @@ struct Vec<__nv_bfloat16> {
     }
 };
 
-// Row `row` of the [n_rows, vocab] matrices target and draft as 16-byte pieces on 16-byte boundaries: piece j holds
-// the tokens first(j) .. first(j) + n - 1, of which the first and the last piece may have some outside the row.
 template <class T>
-struct Row {
-    const T* base;      // of the target's piece 0, at or before the row's first element
-    int64_t to_draft;   // bytes from there to the draft's
-    int64_t whole;      // pieces before the matrix ends
-    int vocab;
-    int shift;          // elements of piece 0 before the row
-    int pieces;
-    int inner;          // pieces [1, inner) lie within the row and the matrix
-    __device__ __forceinline__ Row(const VerifyArgs& a, int64_t row) {
-        constexpr int n = Vec<T>::n;
-        const int64_t at = row * a.vocab;
-        shift = static_cast<int>(at % n);
-        base = static_cast<const T*>(a.target) + (at - shift);
-        to_draft = a.draft ? static_cast<const uint8_t*>(a.draft) - static_cast<const uint8_t*>(a.target) : 0;
-        whole = (a.n_rows * a.vocab - (at - shift)) / n;
-        vocab = static_cast<int>(a.vocab);
-        pieces = static_cast<int>((a.vocab + shift + n - 1) / n);
-        inner = static_cast<int>(min(whole, (a.vocab + shift) / n));
-    }
-    __device__ __forceinline__ int first(int j) const { return j * Vec<T>::n - shift; }
-    __device__ __forceinline__ const uint4* at(int j, bool draft) const {
-        return reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(base) + (draft ? to_draft : 0)) + j;
-    }
-    __device__ __forceinline__ uint4 load_inner(int j, bool draft) const { return __ldg(at(j, draft)); }
-    __device__ __forceinline__ uint4 load(int j, bool draft) const {
-        constexpr int n = Vec<T>::n;
-        if (j < whole) return __ldg(at(j, draft));
-        uint32_t x[n];  // the matrix ends within the piece
+__device__ __forceinline__ Row row_of(const VerifyArgs& a, int64_t row, int parts) {
+    constexpr int n = Vec<T>::n;
+    const int64_t at = row * a.vocab, shift = at % n;
+    Row r;
+    r.base = static_cast<const uint8_t*>(a.target) + (at - shift) * static_cast<int64_t>(sizeof(T));
+    r.to_draft = a.draft ? static_cast<const uint8_t*>(a.draft) - static_cast<const uint8_t*>(a.target) : 0;
+    r.vocab = static_cast<int>(a.vocab);
+    r.shift = static_cast<int>(shift);
+    r.pieces = static_cast<int>((a.vocab + shift + n - 1) / n);
+    r.whole = static_cast<int>(min((a.n_rows * a.vocab - (at - shift)) / n, static_cast<int64_t>(r.pieces)));
+    r.inner = static_cast<int>(min(static_cast<int64_t>(r.whole), (a.vocab + shift) / n));
+    r.per = (r.pieces + parts - 1) / parts;
+    return r;
+}
+template <class T>
+__device__ __forceinline__ int first_of(const Row& r, int j) { return j * Vec<T>::n - r.shift; }
+__device__ __forceinline__ bool in_row(const Row& r, int t) { return t >= 0 && t < r.vocab; }
+__device__ __forceinline__ const uint4* piece_at(const Row& r, int j, bool draft) {
+    return reinterpret_cast<const uint4*>(r.base + (draft ? r.to_draft : 0)) + j;
+}
+template <class T>
+__device__ __forceinline__ uint4 load_piece(const Row& r, int j, bool draft) {
+    constexpr int n = Vec<T>::n;
+    if (j < r.whole) return __ldg(piece_at(r, j, draft));
+    uint32_t x[n];  // the matrix ends within the piece
 #pragma unroll
-        for (int i = 0; i < n; ++i) x[i] = in(first(j) + i) ? Vec<T>::one(at(j, draft), i) : 0u;
-        return Vec<T>::pack(x);
-    }
-    __device__ __forceinline__ bool in(int t) const { return t >= 0 && t < vocab; }
-};
+    for (int i = 0; i < n; ++i) x[i] = in_row(r, first_of<T>(r, j) + i) ? Vec<T>::one(piece_at(r, j, draft), i) : 0u;
+    return Vec<T>::pack(x);
+}
 
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t x) {
 #pragma unroll
@@ -266,36 +314,38 @@ __device__ __forceinline__ void remote_store16(uint32_t a, int16_t x) {
 // The values of piece j made fit: tokens outside the row and those left out are 0, so are NaN and negative values, and
 // values above 2 are 2.
 template <class T>
-__device__ __forceinline__ void mend_piece(const Row<T>& row, int j, const int32_t* out, int outs, uint32_t* p, uint32_t* d, bool* bad) {
+__device__ __forceinline__ void mend_piece(const VerifySmem& sm, const Row& r, int j, uint32_t* p, uint32_t* d, bool* bad) {
     constexpr int n = Vec<T>::n;
-    const int t0 = row.first(j);
+    const int t0 = first_of<T>(r, j);
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-        const bool in = row.in(t0 + i);
+        const bool in = in_row(r, t0 + i);
         p[i] = in ? tame(p[i], bad) : 0u;
         d[i] = in ? tame(d[i], bad) : 0u;
     }
-    for (int k = 0; k < outs; ++k) {
-        const int at = out[k] - t0;
+    for (int k = 0; k < sm.outs; ++k) {
+        const int at = sm.out[k] - t0;
 #pragma unroll
         for (int i = 0; i < n; ++i)
             if (at == i) p[i] = 0u;
     }
 }
 
-// The sum of what is left in pieces [j0, j1), of the whole warp in every lane; kTile tokens a lane at a time.
+// The sum of what is left in pieces [j0, j1) of the row in question, of the whole warp in every lane; kTile tokens a lane at a time.
 template <class T, bool kUnit>
-__device__ __forceinline__ uint64_t sum_left(const Row<T>& row, int j0, int j1, const Scale& S, const int32_t* out, int outs, bool* bad) {
+__device__ __forceinline__ uint64_t sum_left(const VerifySmem& sm, int j0, int j1, bool* bad) {
     constexpr int n = Vec<T>::n, kFly = kTile / n;
-    const int lane = threadIdx.x & 31;
-    const bool draft = S.S != 0;
+    const int lane = threadIdx.x & 31, outs = sm.outs;
+    const Row r = sm.row;
+    const Scale S = scale_of(sm.S);
+    const bool draft = sm.S != 0;
     uint64_t sum = 0;
     uint32_t hi = 0u, mid = 0u, lo = 0u, held = 0u;  // of at most 256 values: below 2^32
 #pragma unroll 1
     for (int j = j0; j < j1; j += 32 * kFly) {
         // the ends of a row, and of the matrix, and tokens left out are looked for one by one
-        bool inner = j > 0 && min(j + 32 * kFly, j1) <= row.inner;
-        for (int k = 0; k < outs; ++k) inner = inner && (out[k] < row.first(j) || out[k] >= row.first(j + 32 * kFly));
+        bool inner = j > 0 && min(j + 32 * kFly, j1) <= r.inner;
+        for (int k = 0; k < outs; ++k) inner = inner && (sm.out[k] < first_of<T>(r, j) || sm.out[k] >= first_of<T>(r, j + 32 * kFly));
         uint32_t p[kTile], d[kTile], most = 0u;
 #pragma unroll
         for (int f = 0; f < kFly; ++f) {
@@ -303,11 +353,11 @@ __device__ __forceinline__ uint64_t sum_left(const Row<T>& row, int j0, int j1, 
             uint4 pv = make_uint4(0u, 0u, 0u, 0u), dv = pv;
             if (at < j1) {
                 if (inner) {
-                    pv = row.load_inner(at, false);
-                    if (draft) dv = row.load_inner(at, true);
+                    pv = __ldg(piece_at(r, at, false));
+                    if (draft) dv = __ldg(piece_at(r, at, true));
                 } else {
-                    pv = row.load(at, false);
-                    if (draft) dv = row.load(at, true);
+                    pv = load_piece<T>(r, at, false);
+                    if (draft) dv = load_piece<T>(r, at, true);
                 }
             }
             Vec<T>::unpack(pv, p + n * f);
@@ -318,20 +368,16 @@ __device__ __forceinline__ uint64_t sum_left(const Row<T>& row, int j0, int j1, 
         if (!inner || most > kTwo) {
 #pragma unroll
             for (int f = 0; f < kFly; ++f)
-                if (j + 32 * f + lane < j1) mend_piece<T>(row, j + 32 * f + lane, out, outs, p + n * f, d + n * f, bad);
+                if (j + 32 * f + lane < j1) mend_piece<T>(sm, r, j + 32 * f + lane, p + n * f, d + n * f, bad);
         }
 #pragma unroll
         for (int i = 0; i < kTile; i += 2) {
-            Units u[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float s, t;
-                left_of<kUnit>(__uint_as_float(p[i + k]), __uint_as_float(d[i + k]), S, &s, &t);
-                u[k] = spread(s, t);
-            }
-            hi += u[0].hi + u[1].hi;
-            mid += u[0].mid + u[1].mid;
-            lo += u[0].lo + u[1].lo;
+            F2 s, t;
+            left_of<kUnit>(two(__uint_as_float(p[i]), __uint_as_float(p[i + 1])), two(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), S, &s, &t);
+            const Units u = spread(s, t);
+            hi += u.hi[0] + u.hi[1];
+            mid += u.mid[0] + u.mid[1];
+            lo += u.lo[0] + u.lo[1];
         }
         held += kTile;
         if (held == 256) {
@@ -342,6 +388,11 @@ __device__ __forceinline__ uint64_t sum_left(const Row<T>& row, int j0, int j1, 
     sum += together(held, hi, mid, lo);
     return warp_sum64(sum);
 }
+// (One copy of it in the kernel: the walk's questions and the draw both call it.)
+template <class T>
+__device__ __noinline__ uint64_t slice_left(const VerifySmem& sm, int j0, int j1, bool* bad) {
+    return sm.S == 0 || sm.S == kOne ? sum_left<T, true>(sm, j0, j1, bad) : sum_left<T, false>(sm, j0, j1, bad);
+}
 
 __device__ __forceinline__ float max_or_nan(float a, float b) {
     float m;
@@ -351,9 +402,10 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
 
 // The first of the largest in pieces [j0, j1): its order key above, the complement of its index below (NaN: key 0).
 template <class T>
-__device__ __forceinline__ uint64_t best_of(const Row<T>& row, int j0, int j1, bool* nan) {
+__device__ __forceinline__ uint64_t best_of(const VerifySmem& sm, int j0, int j1, bool* nan) {
     constexpr int n = Vec<T>::n, kFly = 2;
     const int lane = threadIdx.x & 31;
+    const Row r = sm.row;
     float best = -INFINITY;
     int at = -1, first = -1;  // the best number's token, the first token
 #pragma unroll 1
@@ -361,7 +413,7 @@ __device__ __forceinline__ uint64_t best_of(const Row<T>& row, int j0, int j1, b
         uint4 v[kFly];
 #pragma unroll
         for (int f = 0; f < kFly; ++f)
-            if (j + 32 * f + lane < j1) v[f] = row.load(j + 32 * f + lane, false);
+            if (j + 32 * f + lane < j1) v[f] = load_piece<T>(r, j + 32 * f + lane, false);
 #pragma unroll
         for (int f = 0; f < kFly; ++f) {
             if (j + 32 * f + lane >= j1) break;
@@ -371,11 +423,11 @@ __device__ __forceinline__ uint64_t best_of(const Row<T>& row, int j0, int j1, b
 #pragma unroll
             for (int i = 1; i < n; ++i) m = max_or_nan(m, __uint_as_float(x[i]));
             if (!(m <= best) || at < 0) {  // seldom once some have been seen
-                const int t0 = row.first(j + 32 * f + lane);
+                const int t0 = first_of<T>(r, j + 32 * f + lane);
 #pragma unroll
                 for (int i = 0; i < n; ++i) {
                     const float y = __uint_as_float(x[i]);
-                    if (!row.in(t0 + i)) continue;
+                    if (!in_row(r, t0 + i)) continue;
                     if (first < 0) first = t0 + i;
                     if (y != y) {
                         *nan = true;
@@ -406,6 +458,91 @@ __device__ __forceinline__ bool accepts(float u, uint64_t d, uint64_t R, uint64_
     return __umul64hi(y, static_cast<uint64_t>(fraction(u)) << 32) << 1 < left;
 }
 
+// A turn of the walk, by a warp: on from the last child tried to the next question.
+template <class T>
+__device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, bool greedy, int parts, bool* odd) {
+    __syncwarp();
+    const int lane = threadIdx.x & 31, n = sm.n;
+    int ask = -1, v = sm.v, c = sm.c, len = sm.len, outs = sm.outs_at;
+    uint64_t S = sm.S_at, R = sm.R;
+    bool fresh = sm.fresh, last = false;
+    const auto next_child = [&](int of, int behind) {
+        for (int i0 = behind + 1; i0 < n; i0 += 32) {
+            const uint32_t m = __ballot_sync(0xffffffffu, i0 + lane < n && sm.up[i0 + lane] == of);
+            if (m) return i0 + __ffs(m) - 1;
+        }
+        return -1;
+    };
+    int found = next_child(v, c);
+    while (ask < 0) {
+        if (found < 0) {
+            ask = kEnd;
+            break;
+        }
+        c = found;
+        const int x = sm.tok[c];
+        if (x < 0 || x >= a.vocab) {
+            *odd = true;
+            found = next_child(v, c);
+            continue;
+        }
+        bool yes;
+        if (greedy) {
+            yes = x == sm.best;
+        } else if (S == 0 && outs == 0) {
+            yes = sm.yes[c];
+        } else {
+            const uint32_t d = __float_as_uint(sm.d[c]);
+            uint64_t left = to_units(__float_as_uint(sm.p[c]));
+            if (S) left = minus(left, scaled(S, d));
+            bool had = false;
+            for (int k = lane; k < outs; k += 32) had |= sm.out[k] == x;
+            if (__any_sync(0xffffffffu, had)) left = 0;
+            yes = accepts(sm.u[c], to_units(d), R, left);
+        }
+        if (yes) {
+            if (lane == 0) sm.path[len] = static_cast<int16_t>(c);
+            ++len;
+            v = c;
+            S = 0;
+            R = 1ull << 60;
+            outs = 0;
+            fresh = false;
+            if (greedy) ask = kBest;
+            else found = next_child(v, c);
+        } else if (greedy) {
+            found = next_child(v, c);
+        } else {
+            ask = kSum;
+            last = next_child(v, c) < 0;
+        }
+    }
+    __syncwarp();
+    if (lane == 0) {
+        sm.v = v;
+        sm.c = c;
+        sm.len = len;
+        sm.outs_at = outs;
+        sm.S_at = S;
+        sm.R = R;
+        sm.fresh = fresh;
+        sm.ask = ask;
+        sm.last = last;
+        sm.S = S;
+        sm.outs = outs;
+        if (ask == kSum) {
+            if (a.draft) {
+                sm.S = S + (R >> 10);
+            } else {
+                sm.out[outs] = sm.tok[c];
+                sm.outs = outs + 1;
+            }
+        }
+        sm.row = row_of<T>(a, sm.r0 + v, parts);
+    }
+    __syncwarp();
+}
+
 // T: the probabilities' type.
 template <class T>
 __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
@@ -416,14 +553,18 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
     const int parts = static_cast<int>(ctas) * kVWarps, mine = static_cast<int>(rank) * kVWarps + warp;
     const bool greedy = a.u_pick == nullptr;
     bool bad = false, odd = false;  // probabilities / other data that are none
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has started: the others may write to it
     // ---- CTA 0 reads the tree and hands it to all, so that every CTA walks on the same data
     const int64_t r0 = a.row_off[b], r1 = a.row_off[b + 1];
     const bool whole = r0 >= 0 && r1 >= r0 && r1 <= a.n_rows && r1 - r0 <= kNodes;
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (rank == 0) {
         const int n = whole ? static_cast<int>(r1 - r0) : 0;
         odd = !whole;
         if (r1 - r0 > kNodes && r0 >= 0 && r1 <= a.n_rows)
             for (int64_t i = r0 + tid; i < r1; i += kVT) a.path[i] = -1;
+        float pick = 0.f;
+        if (tid < static_cast<int>(ctas) && !greedy && n > 0) pick = a.u_pick[b];
         for (int i = tid; i < n; i += kVT) {
             int up = a.parent[r0 + i];
             const int x = a.token[r0 + i];
@@ -439,8 +580,10 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
                 d = a.draft ? tame(Vec<T>::one(a.draft, at), &bad) : 0x3F800000u;
             }
             const float uu = up >= 0 ? unit_interval(u, &odd) : 0.f;
+            const bool yes = accepts(uu, to_units(d), 1ull << 60, to_units(p));
             for (uint32_t k = 0; k < ctas; ++k) {
                 remote_store16(remote_addr(&sm.up[i], k), static_cast<int16_t>(up));
+                remote_store16(remote_addr(&sm.yes[i], k), static_cast<int16_t>(yes));
                 remote_store32(remote_addr(&sm.tok[i], k), static_cast<uint32_t>(x));
                 remote_store32(remote_addr(&sm.u[i], k), __float_as_uint(uu));
                 remote_store32(remote_addr(&sm.p[i], k), p);
@@ -448,173 +591,52 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
             }
         }
         if (tid < static_cast<int>(ctas)) {
-            float u = 0.f;
-            if (!greedy && n > 0) u = unit_interval(a.u_pick[b], &odd);
+            if (!greedy && n > 0) pick = unit_interval(pick, &odd);
             remote_store64(remote_addr(&sm.r0, tid), static_cast<uint64_t>(n > 0 ? r0 : 0));
             remote_store32(remote_addr(&sm.n, tid), static_cast<uint32_t>(n));
-            remote_store32(remote_addr(&sm.u_pick, tid), __float_as_uint(u));
+            remote_store32(remote_addr(&sm.u_pick, tid), __float_as_uint(pick));
         }
         __syncwarp();
     }
+    // greedy: the root's best is asked for at once, and answered behind the same barrier as the tree
+    bool first = greedy;
     if (tid == 0) {
         sm.path[0] = 0;
-        sm.v = sm.c = sm.outs = 0;
+        sm.v = sm.c = sm.outs_at = sm.outs = 0;
         sm.len = 1;
-        sm.S_at = 0;
+        sm.S_at = sm.S = 0;
         sm.R = 1ull << 60;
         sm.fresh = false;
+        if (first) {
+            sm.ask = kBest;
+            sm.row = row_of<T>(a, whole && r1 > r0 ? r0 : 0, parts);
+            if (!whole || r1 == r0) sm.row.pieces = sm.row.per = 0;
+        }
     }
-    // greedy: the root's best is asked for at once, and answered behind the same barrier as the tree
-    bool first = greedy, fine = false;
-    int asked = 0, j0 = 0, j1 = 0;
-    uint64_t at = 0;              // what is left to pass of the draw's sum
-    if (!first) {
-        cluster_sync_all();
-        if (sm.n == 0) goto done;
-    }
-    for (;;) {
-        if (!first && !fine) {
+    if (first) __syncthreads();
+    else cluster_sync_all();
+    for (int asked = 1; first || sm.n > 0; ++asked) {
+        if (!first) {
+            if (warp == 0) walk<T>(a, sm, greedy, parts, &odd);
+            __syncthreads();
+            if (sm.ask == kEnd && greedy) break;
+        }
+        const int ask = sm.ask;
+        if (ask != kEnd || !sm.fresh) {
+            // ---- every CTA: its slice, a warp's slice of it
+            const int j0 = min(mine * sm.row.per, sm.row.pieces), j1 = min(j0 + sm.row.per, sm.row.pieces);
+            const uint64_t sum = ask == kBest ? best_of<T>(sm, j0, j1, &bad) : slice_left<T>(sm, j0, j1, &bad);
+            if (lane == 0) sm.warp_sum[warp] = sum;
+            __syncthreads();
             if (warp == 0) {
+                uint64_t all = lane < kVWarps ? sm.warp_sum[lane] : 0;
+                all = ask == kBest ? warp_max64(all) : warp_sum64(all);
+                if (lane < static_cast<int>(ctas)) remote_store64(remote_addr(&sm.slot[asked & 1][rank], lane), all);
                 __syncwarp();
-                const int n = sm.n;
-                int ask = -1, v = sm.v, c = sm.c, len = sm.len, outs = sm.outs, tried = outs;
-                uint64_t S = sm.S_at, R = sm.R, S_try = S;
-                bool fresh = sm.fresh;
-                while (ask < 0) {
-                    // the next child of v behind c
-                    int found = -1;
-                    for (int i0 = c + 1; i0 < n && found < 0; i0 += 32) {
-                        const uint32_t m = __ballot_sync(0xffffffffu, i0 + lane < n && sm.up[i0 + lane] == v);
-                        if (m) found = i0 + __ffs(m) - 1;
-                    }
-                    if (found < 0) {
-                        ask = kEnd;
-                        break;
-                    }
-                    c = found;
-                    const int x = sm.tok[c];
-                    if (x < 0 || x >= a.vocab) {
-                        odd = true;
-                        continue;
-                    }
-                    bool yes;
-                    if (greedy) {
-                        yes = x == sm.best;
-                    } else {
-                        const uint32_t d = __float_as_uint(sm.d[c]);
-                        uint64_t left = to_units(__float_as_uint(sm.p[c]));
-                        if (S) left = minus(left, scaled(S, d));
-                        if (outs) {
-                            bool had = false;
-                            for (int k = lane; k < outs; k += 32) had |= sm.out[k] == x;
-                            if (__any_sync(0xffffffffu, had)) left = 0;
-                        }
-                        yes = accepts(sm.u[c], to_units(d), R, left);
-                    }
-                    if (yes) {
-                        if (lane == 0) sm.path[len] = static_cast<int16_t>(c);
-                        ++len;
-                        v = c;
-                        S = 0;
-                        R = 1ull << 60;
-                        outs = 0;
-                        fresh = false;
-                        if (greedy) ask = kBest;
-                    } else if (!greedy) {
-                        ask = kSum;
-                        if (a.draft) {
-                            S_try = S + (R >> 10);
-                        } else {
-                            if (lane == 0) sm.out[outs] = x;
-                            tried = outs + 1;
-                        }
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    sm.v = v;
-                    sm.c = c;
-                    sm.len = len;
-                    sm.outs = outs;
-                    sm.S_at = S;
-                    sm.R = R;
-                    sm.fresh = fresh;
-                    sm.ask = ask;
-                    sm.node = v;
-                    sm.S = ask == kSum ? S_try : S;
-                    sm.gone = ask == kSum ? tried : outs;
-                }
             }
-            __syncthreads();
-        }
-        const int ask = first ? kBest : sm.ask, outs_now = first ? 0 : sm.gone;
-        const Scale S_now = scale_of(first ? 0 : sm.S);
-        const bool unit = S_now.S == 0 || S_now.S == kOne;
-        if (ask == kEnd && greedy) break;
-        const int64_t row = first ? (whole && r1 > r0 ? r0 : 0) : sm.r0 + sm.node;
-        const Row<T> p(a, row);
-        const int per = (p.pieces + parts - 1) / parts;
-        if (fine || ask != kEnd || !sm.fresh) {
-            // ---- every CTA: its slice, a warp's slice of it, or the warp's part of the slice that holds the token
-            if (!fine) {
-                j0 = min(mine * per, p.pieces);
-                j1 = first && !(whole && r1 > r0) ? j0 : min(j0 + per, p.pieces);
-            }
-            uint64_t sum;
-            if (ask == kBest) sum = best_of<T>(p, j0, j1, &bad);
-            else if (unit) sum = sum_left<T, true>(p, j0, j1, S_now, sm.out, outs_now, &bad);
-            else sum = sum_left<T, false>(p, j0, j1, S_now, sm.out, outs_now, &bad);
-            if (lane == 0) (fine ? sm.fine : sm.warp_sum)[warp] = sum;
-            __syncthreads();
-            if (!fine) {
-                ++asked;
-                if (warp == 0) {
-                    uint64_t all = lane < kVWarps ? sm.warp_sum[lane] : 0;
-                    all = ask == kBest ? warp_max64(all) : warp_sum64(all);
-                    if (lane < static_cast<int>(ctas)) remote_store64(remote_addr(&sm.slot[asked & 1][rank], lane), all);
-                    __syncwarp();
-                }
-                cluster_sync_all();
-            }
-        }
-        if (fine) {  // ---- the token: a warp's part, a lane's piece
-            if (warp_find(lane < kVWarps ? sm.fine[lane] : 0, &at) != warp) break;
-            for (int base = j0; base < j1; base += 32) {
-                uint64_t x[Vec<T>::n], s = 0;
-                const int j = base + lane;
-#pragma unroll
-                for (int i = 0; i < Vec<T>::n; ++i) x[i] = 0;
-                if (j < j1) {
-                    uint32_t pb[Vec<T>::n], db[Vec<T>::n];
-                    Vec<T>::unpack(p.load(j, false), pb);
-                    Vec<T>::unpack(S_now.S ? p.load(j, true) : make_uint4(0u, 0u, 0u, 0u), db);
-                    mend_piece<T>(p, j, sm.out, outs_now, pb, db, &bad);
-#pragma unroll
-                    for (int i = 0; i < Vec<T>::n; ++i) {
-                        float l, t;
-                        if (unit) left_of<true>(__uint_as_float(pb[i]), __uint_as_float(db[i]), S_now, &l, &t);
-                        else left_of<false>(__uint_as_float(pb[i]), __uint_as_float(db[i]), S_now, &l, &t);
-                        const Units y = spread(l, t);
-                        x[i] = together(1u, y.hi, y.mid, y.lo);
-                        s += x[i];
-                    }
-                }
-                const int found = warp_find(s, &at);
-                if (found >= 0) {
-                    if (lane == found) {
-                        uint64_t run = 0;
-                        int t = -1;
-#pragma unroll
-                        for (int i = 0; i < Vec<T>::n; ++i) {
-                            run += x[i];
-                            if (t < 0 && run > at) t = p.first(j) + i;
-                        }
-                        a.next[b] = t;
-                    }
-                    break;
-                }
-            }
-            break;
+            cluster_sync_all();
+        } else {
+            --asked;  // the last sums' slots
         }
         const uint64_t* const slot = sm.slot[asked & 1];
         uint64_t total = 0, before = 0;
@@ -624,36 +646,78 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
             if (k < rank) before += x;
         }
         if (ask == kBest) {
-            if (sm.n == 0) break;
             if (tid == 0) sm.best = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(total));
             first = false;
-        } else if (ask == kSum) {
+            continue;
+        }
+        if (ask == kSum && !(sm.last && total > 0)) {  // (a last child's rejection is followed by the draw at once)
             if (tid == 0) {
                 sm.fresh = total > 0;
                 if (total > 0) {
-                    sm.S_at = S_now.S;
+                    sm.S_at = sm.S;
                     sm.R = total;
-                    sm.outs = outs_now;
+                    sm.outs_at = sm.outs;
                 }
             }
-        } else {  // ---- the token behind the path is in the CTA, the warp's slice and then the part of it that holds u * total
-            if (total == 0) {
-                odd = true;
-                if (rank == 0 && tid == 0) a.next[b] = 0;
+            continue;
+        }
+        // ---- the token behind the path is in the CTA, the warp's slice and then the part of it that holds u * total
+        if (total == 0) {
+            odd = true;
+            if (rank == 0 && tid == 0) a.next[b] = 0;
+            break;
+        }
+        uint64_t at = __umul64hi(total, static_cast<uint64_t>(fraction(sm.u_pick)) << 32);
+        if (at < before || at - before >= slot[rank]) break;
+        at -= before;
+        const int w = static_cast<int>(rank) * kVWarps + warp_find(lane < kVWarps ? sm.warp_sum[lane] : 0, &at);
+        const int s0 = min(w * sm.row.per, sm.row.pieces), s1 = min(s0 + sm.row.per, sm.row.pieces), sub = (s1 - s0 + kVWarps - 1) / kVWarps;
+        const int j0 = min(s0 + warp * sub, s1), j1 = min(j0 + sub, s1);
+        const uint64_t sum = slice_left<T>(sm, j0, j1, &bad);
+        if (lane == 0) sm.fine[warp] = sum;
+        __syncthreads();
+        if (warp_find(lane < kVWarps ? sm.fine[lane] : 0, &at) != warp) break;
+        const Row r = sm.row;
+        const Scale S = scale_of(sm.S);
+        const bool unit = sm.S == 0 || sm.S == kOne;
+        for (int base = j0; base < j1; base += 32) {
+            uint64_t x[Vec<T>::n], s = 0;
+            const int j = base + lane;
+#pragma unroll
+            for (int i = 0; i < Vec<T>::n; ++i) x[i] = 0;
+            if (j < j1) {
+                uint32_t p[Vec<T>::n], d[Vec<T>::n];
+                Vec<T>::unpack(load_piece<T>(r, j, false), p);
+                Vec<T>::unpack(sm.S ? load_piece<T>(r, j, true) : make_uint4(0u, 0u, 0u, 0u), d);
+                mend_piece<T>(sm, r, j, p, d, &bad);
+#pragma unroll
+                for (int i = 0; i < Vec<T>::n; i += 2) {
+                    const F2 pf = two(__uint_as_float(p[i]), __uint_as_float(p[i + 1])), df = two(__uint_as_float(d[i]), __uint_as_float(d[i + 1]));
+                    F2 l, t;
+                    if (unit) left_of<true>(pf, df, S, &l, &t);
+                    else left_of<false>(pf, df, S, &l, &t);
+                    const Units y = spread(l, t);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) s += x[i + k] = together(1u, y.hi[k], y.mid[k], y.lo[k]);
+                }
+            }
+            const int found = warp_find(s, &at);
+            if (found >= 0) {
+                if (lane == found) {
+                    uint64_t run = 0;
+                    int t = -1;
+#pragma unroll
+                    for (int i = 0; i < Vec<T>::n; ++i) {
+                        run += x[i];
+                        if (t < 0 && run > at) t = first_of<T>(r, j) + i;
+                    }
+                    a.next[b] = t;
+                }
                 break;
             }
-            at = __umul64hi(total, static_cast<uint64_t>(fraction(sm.u_pick)) << 32);
-            if (at < before || at - before >= slot[rank]) break;
-            at -= before;
-            const int w = warp_find(lane < kVWarps ? sm.warp_sum[lane] : 0, &at);
-            const int s0 = min((static_cast<int>(rank) * kVWarps + w) * per, p.pieces), s1 = min(s0 + per, p.pieces);
-            const int sub = (s1 - s0 + kVWarps - 1) / kVWarps;
-            j0 = min(s0 + warp * sub, s1);
-            j1 = min(j0 + sub, s1);
-            fine = true;
         }
+        break;
     }
-done:
     // ---- CTA 0's warp 0 knows the path
     if (rank == 0 && warp == 0) {
         __syncwarp();
