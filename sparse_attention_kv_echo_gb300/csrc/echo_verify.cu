@@ -394,6 +394,14 @@ __device__ __noinline__ uint64_t slice_left(const VerifySmem& sm, int j0, int j1
     return sm.S == 0 || sm.S == kOne ? sum_left<T, true>(sm, j0, j1, bad) : sum_left<T, false>(sm, j0, j1, bad);
 }
 
+// Value i of a piece.
+template <class T>
+__device__ __forceinline__ float one_of(const uint4& v, int i) {
+    const int k = Vec<T>::n == 4 ? i : i >> 1;
+    const uint32_t w = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+    return __uint_as_float(Vec<T>::n == 4 ? w : i & 1 ? w & 0xFFFF0000u : w << 16);
+}
+
 __device__ __forceinline__ float max_or_nan(float a, float b) {
     float m;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
@@ -407,7 +415,7 @@ __device__ __forceinline__ uint64_t best_of(const VerifySmem& sm, int j0, int j1
     const int lane = threadIdx.x & 31;
     const Row r = sm.row;
     float best = -INFINITY;
-    int at = -1, first = -1;  // the best number's token, the first token
+    int at = -1, first = -1;  // the best number's token; the first token, where all are NaN
 #pragma unroll 1
     for (int j = j0; j < j1; j += 32 * kFly) {
         uint4 v[kFly];
@@ -419,28 +427,38 @@ __device__ __forceinline__ uint64_t best_of(const VerifySmem& sm, int j0, int j1
             if (j + 32 * f + lane >= j1) break;
             uint32_t x[n];
             Vec<T>::unpack(v[f], x);
+            const int t0 = first_of<T>(r, j + 32 * f + lane);
+            const bool edge = t0 < 0 || t0 + n > r.vocab;
             float m = __uint_as_float(x[0]);
 #pragma unroll
             for (int i = 1; i < n; ++i) m = max_or_nan(m, __uint_as_float(x[i]));
-            if (!(m <= best) || at < 0) {  // seldom once some have been seen
-                const int t0 = first_of<T>(r, j + 32 * f + lane);
+            if (!edge && m == m) {
+                if (at < 0 || m > best) {
+                    best = m;
 #pragma unroll
+                    for (int i = n - 1; i >= 0; --i)
+                        if (__uint_as_float(x[i]) == m) at = t0 + i;
+                }
+            } else {  // the ends of a row, and NaN
+#pragma unroll 1
                 for (int i = 0; i < n; ++i) {
-                    const float y = __uint_as_float(x[i]);
-                    if (!in_row(r, t0 + i)) continue;
-                    if (first < 0) first = t0 + i;
+                    const int t = t0 + i;
+                    const float y = one_of<T>(v[f], i);
+                    if (!in_row(r, t)) continue;
+                    if (first < 0) first = t;
                     if (y != y) {
                         *nan = true;
-                    } else if (y > best || at < 0) {  // ascending: an equal one comes later
+                    } else if (at < 0 || y > best) {  // ascending: an equal one comes later
                         best = y;
-                        at = t0 + i;
+                        at = t;
                     }
                 }
             }
         }
     }
     uint64_t key = 0;
-    if (first >= 0) key = (static_cast<uint64_t>(at < 0 ? 0u : order_key(best)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(at < 0 ? first : at));
+    if (at >= 0) key = (static_cast<uint64_t>(order_key(best)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(at));
+    else if (first >= 0) key = 0xFFFFFFFFu - static_cast<uint32_t>(first);
     return warp_max64(key);
 }
 
