@@ -692,14 +692,14 @@ int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, cons
  * NULL: greedy; target may then hold logits, draft is not read, a child is accepted
  * when its token is the first of target[v]'s largest, and that is the token behind the path.
  *   path [n_rows] int32: the accepted nodes of request b in order from row_off[b] on
- *     (node 0 first), -1 behind; count [B] int32: how many (>= 1 with rows, else 0);
+ *     (node 0 first), -1 behind; rows outside every request left as they were; count [B] int32: how many (>= 1 with rows, else 0);
  *     next [B] int32: the token behind the path (-1 without rows).
  *   dtype ECHO_F32 or ECHO_BF16, of target and draft both (16-byte aligned).
- * The sums are exact to 2^-60 a value (64-bit integers), so equal inputs give equal
- * results on any launch, and a test falls on the right side of its border unless it is
- * within 2^-48 of it.  Probabilities are to be in [0, 1] with a sum of at most 8: NaN and
- * values outside [0, 2] count as 0 and 2 and set ECHO_ST_NAN; a row that is 0 throughout
- * gives token 0 and ECHO_ST_BADDATA; uniform numbers outside [0, 1) (or NaN) count as the
+ * What is left of a token is summed as a whole number, good to 2^-48, so equal inputs give equal
+ * results in any batch and on any launch, and a test falls on the right side of its border unless it is
+ * within some 2^-40 of it.  Probabilities are to be in [0, 1] with a sum of at most 8 (of a row
+ * with a larger sum any token may come): NaN and values outside [0, 2] count as 0 and 2 and
+ * set ECHO_ST_NAN where they are read; a row that is 0 throughout gives token 0 and ECHO_ST_BADDATA; uniform numbers outside [0, 1) (or NaN) count as the
  * nearest in it.  Greedy: NaN is below every number and sets ECHO_ST_NAN.  A node
  * whose token is not in [0, vocab) is not accepted and changes nothing (when it is tried:
  * ECHO_ST_BADDATA); a request of more than ECHO_TREE_MAX_NODES rows or with inconsistent row
@@ -730,7 +730,8 @@ int echo_draft_verify(int B, const int64_t* row_off, int64_t n_rows, const int32
  * pool, and counts that would fall below 0, set ECHO_ST_BADDATA.
  * All of them: one call at a time on a pool (the calls read and write its table and
  * counts); equal inputs give equal tables, whatever the launch.  ws:
- * echo_pages_workspace_size(B, n_pages) bytes, 256-byte aligned, B being the requests or pairs of the call; contents need not be kept.
+ * echo_pages_workspace_size(B, n_pages) bytes, 256-byte aligned, B being the requests or pairs of the call; contents need not
+ * be kept, calls on two pools that may run at the same time need their own.
  * Errors: ECHO_EINVAL (sizes, NULL or misaligned pointers, a small workspace),
  * ECHO_EUNSUPPORTED (B > ECHO_MAX_REQUESTS, n_pages > ECHO_POOL_MAX_PAGES), ECHO_ECUDA.
  */

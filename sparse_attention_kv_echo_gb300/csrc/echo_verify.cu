@@ -613,6 +613,7 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
             remote_store64(remote_addr(&sm.r0, tid), static_cast<uint64_t>(n > 0 ? r0 : 0));
             remote_store32(remote_addr(&sm.n, tid), static_cast<uint32_t>(n));
             remote_store32(remote_addr(&sm.u_pick, tid), __float_as_uint(pick));
+            if (tid == 0 && n > 0) a.next[b] = 0;  // (stays where sums beyond 64 bits, of no probabilities, hide the token)
         }
         __syncwarp();
     }
@@ -682,13 +683,14 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
         // ---- the token behind the path is in the CTA, the warp's slice and then the part of it that holds u * total
         if (total == 0) {
             odd = true;
-            if (rank == 0 && tid == 0) a.next[b] = 0;
             break;
         }
         uint64_t at = __umul64hi(total, static_cast<uint64_t>(fraction(sm.u_pick)) << 32);
         if (at < before || at - before >= slot[rank]) break;
         at -= before;
-        const int w = static_cast<int>(rank) * kVWarps + warp_find(lane < kVWarps ? sm.warp_sum[lane] : 0, &at);
+        const int in = warp_find(lane < kVWarps ? sm.warp_sum[lane] : 0, &at);
+        if (in < 0) break;
+        const int w = static_cast<int>(rank) * kVWarps + in;
         const int s0 = min(w * sm.row.per, sm.row.pieces), s1 = min(s0 + sm.row.per, sm.row.pieces), sub = (s1 - s0 + kVWarps - 1) / kVWarps;
         const int j0 = min(s0 + warp * sub, s1), j1 = min(j0 + sub, s1);
         const uint64_t sum = slice_left<T>(sm, j0, j1, &bad);

@@ -114,6 +114,18 @@ def test_any_mask_and_rows_that_see_nothing(lens, rows, heads):
         assert torch.isinf(lse[0]).all()
 
 
+@pytest.mark.parametrize("absent", [0.0, 0.4])
+def test_trees_over_slots_of_each_requests_own(absent):
+    # page 1 and rows per request: the slots of a layer's cache
+    g = torch.Generator().manual_seed(4)
+    rows = [9, 1, 20]
+    seen = [ancestors(random_parents(n, g, 4)) for n in rows]
+    bt = TreeBatch([100, 30, 61], rows, seen, heads=16, page=1, seed=7, absent=absent, per_request=128)
+    out, lse, status = _attend(bt)
+    assert status == 0
+    _compare(bt, out, lse)
+
+
 def test_a_chain_is_the_causal_call():
     L = _lib()
     bt = TreeBatch([700, 300], [40, 3], [ancestors([-1] + list(range(39))), ancestors([-1, 0, 1])], heads=128, page=64, seed=3)

@@ -191,6 +191,24 @@ def test_values_that_are_no_probabilities():
     assert (path, count, behind) == e.expected() and st == L.ST_BADDATA
 
 
+@pytest.mark.parametrize("half", [False, True])
+def test_rows_of_no_probabilities_give_some_token(half):
+    # sums far beyond what the call is made for, and beyond 64 bits: a token in range all the same
+    L = _lib()
+    for value in (1.0, 2.0, 0.01):
+        for seed in range(4):
+            d = Drafts([3] * 5, 20000, half=half, seed=seed)
+            d.target[:] = value
+            d.draft[:] = value / 4
+            path, count, behind, st = d.run()
+            assert all(0 <= y < 20000 for y in behind) and all(1 <= c <= 3 for c in count)
+            assert st in (0, L.ST_BADDATA)                             # (a sum may come out as 0 in 64 bits)
+    d = Drafts([3] * 5, 20000, half=half, seed=1)
+    d.target = (5 * torch.randn((15, 20000))).to(d.target.dtype)       # logits
+    path, count, behind, st = d.run()
+    assert all(0 <= y < 20000 for y in behind) and st & L.ST_NAN
+
+
 def test_tokens_and_parents_out_of_range():
     L = _lib()
     d = Drafts([5], 40, 5, seed=8)
