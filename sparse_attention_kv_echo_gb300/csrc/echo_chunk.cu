@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kPT) chunk_plan_kernel(ChunkArgs a, Plan plan)
         plan.cum[groups] = sum;
         *plan.head = make_head(sum, groups, plan);
     }
+    pdl_wait();  // a tree's plan may start beside the kernel that makes its masks: the attention behind it needs both ended
 }
 
 // A leg, at most kLeg tiles, of the part of a group that a share holds (a piece): tiles [lo, hi) of `tiles`.
@@ -1155,10 +1156,9 @@ int launch_chunk(const ChunkArgs& a, uint16_t* out, float* lse, void* ws, size_t
     ECHO_CUDA_OK(prefer_max_shared(chunk_join_kernel));
     plan.small = cap <= kInline && B <= kInline;  // 1 row of 1000 tokens: 20 us with a plan kernel, 18 without
     if (!plan.small) {
-        chunk_plan_kernel<<<1, kPT, 0, s>>>(a, plan);
-        ECHO_CUDA_OK(cudaGetLastError());
+        ECHO_CUDA_OK(launch_after(!kTree, chunk_plan_kernel, dim3(1), kPT, 0, s, a, plan));
     }
-    // (a tree's call comes behind the one that made its masks, whose kernel lets it start; nothing is read before that has ended)
+    // (a tree's call comes behind the one that made its masks, whose kernel lets it start; the masks are read when that has ended)
     ECHO_CUDA_OK(launch_after(plan.small && !kTree, chunk_kernel<kTree>, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan, qmap,
                               a.scale * 1.4426950408889634f, out, lse));
     if (plan.clusters > 1)
