@@ -44,7 +44,6 @@
 // of a cut group go to the workspace in fp32 with their maximum and sum, and
 // chunk_join_kernel adds them in order (the same bits every time).  A part of more than
 // kLeg tiles is walked in legs, added up in its place in the workspace.
-#include <stdlib.h>
 #include "echo_chunk.cuh"
 
 namespace echo {
@@ -70,8 +69,6 @@ constexpr uint32_t kSCol = 256;
 constexpr int kAhead = 1;
 constexpr float kLazy = 8.f;
 constexpr int kMinUnits = 2;             // least units per cluster
-constexpr int kMinTreeUnits = 4;         // of a tree's call: it has several rows, whose parts the join reads (8 nodes over
-                                         // 1000 tokens: 2 units 23.6 us, 4 21.6, 6 23.7, 10 26.9)
 constexpr uint32_t kIdescS = idesc_bf16_f32(kM, kTok);
 constexpr uint32_t kIdescO = idesc_bf16_f32(kM, 256) | (1u << 16);  // B (V) MN-major
 // ---------------------------------------------------------------- attention
@@ -128,8 +125,6 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t sP, uint32_t sV
                       (add || kk > 0) ? 1u : 0u);
 }
 
-// kTree: rows see the context before their tree and, of the tree, what their masks say.
-template <bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_kernel(ChunkArgs a, Plan plan, const __grid_constant__ CUtensorMap qmap, float scale_log2, uint16_t* __restrict__ out, float* __restrict__ lse) {
     extern __shared__ __align__(1024) uint8_t chunk_smem[];  // the swizzled tiles need 1024 bytes
@@ -224,25 +219,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            [[maybe_unused]] const uint32_t* nodes = nullptr;  // this row's mask
-            if constexpr (kTree) {
-                if (lives) nodes = a.mask + static_cast<int64_t>(p.g.row0 + rig) * a.words;
-            }
             float m = -INFINITY, l = 0.f;
             for (int it = p.lo; it < p.hi; ++it, ++t) {
                 const uint32_t st = t & 1u;
-                [[maybe_unused]] uint32_t seen = 0xFFFFFFFFu;
-                if constexpr (kTree) {
-                    // the mask's bits of tokens v0 .. v0 + 31, those before the tree set; asked for before the
-                    // wait, and by the last tiles alone
-                    const int d = it * kTok + half * 32 - p.g.kept;
-                    if (d > -32 && nodes) {
-                        const int w = d >> 5;
-                        const uint32_t lo = w < 0 ? 0xFFFFFFFFu : w < a.words ? nodes[w] : 0u;
-                        const uint32_t hi = w + 1 < a.words ? nodes[w + 1] : 0u;
-                        seen = __funnelshift_r(lo, hi, d & 31);
-                    }
-                }
                 ok = ok && mbar_wait(smem_addr(&ctl->s_full[t & (kSBufs - 1)]), (t / kSBufs) & 1u, abort);
                 tc_fence_after();
                 __syncwarp();
@@ -252,8 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->s_free[t & (kSBufs - 1)]), 0);
                 const int v0 = it * kTok + half * 32;
-                uint32_t there = ctl->valid[t & (kValid - 1)][half];
-                if constexpr (kTree) there &= seen;
+                const uint32_t there = ctl->valid[t & (kValid - 1)][half];
                 const bool clean = there == 0xFFFFFFFFu && v0 + 32 <= vhi && (vb <= va || v0 >= vb || v0 + 32 <= va);
                 if (!__all_sync(0xffffffffu, clean)) {
 #pragma unroll
@@ -593,42 +571,6 @@ extern "C" size_t echo_mla_chunk_workspace_size(int64_t n_rows, int heads, int B
     return plan_layout(plan_cap(n_rows, heads, B, true)).total;  // a row to a group is the most
 }
 
-namespace echo {
-namespace {
-
-template <bool kTree>
-int launch_chunk(const ChunkArgs& a, uint16_t* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t s) {
-    const int B = a.B, heads = a.heads;
-    const int64_t n_rows = a.n_rows;
-    if (!out || !lse || !ws || !is_aligned(out, 16) || !is_aligned(ws, 256)) return ECHO_EINVAL;
-    if (ws_bytes < echo_mla_chunk_workspace_size(n_rows, heads, B)) return ECHO_EINVAL;
-    if (kTree && getenv("WIDE")) return launch_tree_wide(a, out, lse, ws, s);
-    const int64_t cap = plan_cap(n_rows, heads, B, a.sel != nullptr);
-    Plan plan = plan_in(ws, cap);
-    plan.least = kTree ? kMinTreeUnits : kMinUnits;
-    plan.ahead = cap <= 2 * B ? kAhead : 0;
-    CUtensorMap qmap;
-    if (encode_tmap_bytes_2d(&qmap, a.q, kLatRowBytes, static_cast<uint64_t>(n_rows) * heads, 128, 64)) return ECHO_ECUDA;
-    static int cached[64];
-    plan.clusters = cluster2_count(chunk_kernel<kTree>, kThreads, kSmem, kMaxClusters, cached);
-    if (plan.clusters < 1) return ECHO_ECUDA;
-    ECHO_CUDA_OK(prefer_max_shared(chunk_plan_kernel<kTok>));
-    ECHO_CUDA_OK(prefer_max_shared(chunk_join_kernel));
-    plan.small = cap <= kInline && B <= kInline;  // 1 row of 1000 tokens: 20 us with a plan kernel, 18 without
-    if (!plan.small) {
-        ECHO_CUDA_OK(launch_after(!kTree, chunk_plan_kernel<kTok>, dim3(1), kPT, 0, s, a, plan));
-    }
-    // (a tree's call comes behind the one that made its masks, whose kernel lets it start; the masks are read when that has ended)
-    ECHO_CUDA_OK(launch_after(plan.small && !kTree, chunk_kernel<kTree>, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan, qmap,
-                              a.scale * 1.4426950408889634f, out, lse));
-    if (plan.clusters > 1)
-        ECHO_CUDA_OK(launch_after(false, chunk_join_kernel, dim3(static_cast<unsigned>(8 * sm_count())), kJT, 0, s, a, plan, out, lse));
-    return ECHO_OK;
-}
-
-}  // namespace
-}  // namespace echo
-
 extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q,
                               const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens,
                               const echo_pages* pages, const int32_t* sel, int k, int64_t window, int64_t sinks,
@@ -640,24 +582,30 @@ extern "C" int echo_mla_chunk(int B, const int64_t* row_off, int64_t n_rows, int
     if (sel && (k <= 0 || window || sinks)) return ECHO_EINVAL;
     if (sel && k > kMaxLen) return ECHO_EUNSUPPORTED;
     if (n_rows == 0) return ECHO_OK;
+    if (!out || !lse || !ws || !is_aligned(out, 16) || !is_aligned(ws, 256)) return ECHO_EINVAL;
+    if (ws_bytes < echo_mla_chunk_workspace_size(n_rows, heads, B)) return ECHO_EINVAL;
     const ChunkArgs a = chunk_args(B, row_off, n_rows, heads, q, tok_off, tok_end, n_tokens, pages, sel, k, window,
                                    sinks, scale, status);
-    return launch_chunk<false>(a, out, lse, ws, ws_bytes, static_cast<cudaStream_t>(stream));
-}
-
-extern "C" int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q,
-                             const uint32_t* mask, int words, const int64_t* tok_off, const int64_t* tok_end,
-                             int64_t n_tokens, const echo_pages* pages, float scale, uint16_t* out, float* lse, void* ws,
-                             size_t ws_bytes, int32_t* status, echo_stream_t stream) {
-    using namespace echo;
-    const int rc = check_chunk(B, row_off, n_rows, heads, q, tok_off, n_tokens, pages, 0, 0, scale, status);
-    if (rc) return rc;
-    if (words < 1) return ECHO_EINVAL;
-    if (words > ECHO_TREE_MAX_WORDS) return ECHO_EUNSUPPORTED;
-    if (n_rows == 0) return ECHO_OK;
-    if (!mask) return ECHO_EINVAL;
-    ChunkArgs a = chunk_args(B, row_off, n_rows, heads, q, tok_off, tok_end, n_tokens, pages, nullptr, 0, 0, 0, scale, status);
-    a.mask = mask;
-    a.words = words;
-    return launch_chunk<true>(a, out, lse, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t cap = plan_cap(n_rows, heads, B, sel != nullptr);
+    Plan plan = plan_in(ws, cap);
+    plan.least = kMinUnits;
+    plan.ahead = cap <= 2 * B ? kAhead : 0;
+    CUtensorMap qmap;
+    if (encode_tmap_bytes_2d(&qmap, q, kLatRowBytes, static_cast<uint64_t>(n_rows) * heads, 128, 64)) return ECHO_ECUDA;
+    static int cached[64];
+    plan.clusters = cluster2_count(chunk_kernel, kThreads, kSmem, kMaxClusters, cached);
+    if (plan.clusters < 1) return ECHO_ECUDA;
+    ECHO_CUDA_OK(prefer_max_shared(chunk_plan_kernel<kTok>));
+    ECHO_CUDA_OK(prefer_max_shared(chunk_join_kernel));
+    plan.small = cap <= kInline && B <= kInline;  // 1 row of 1000 tokens: 20 us with a plan kernel, 18 without
+    if (!plan.small) {
+        chunk_plan_kernel<kTok><<<1, kPT, 0, s>>>(a, plan);
+        ECHO_CUDA_OK(cudaGetLastError());
+    }
+    ECHO_CUDA_OK(launch_after(plan.small, chunk_kernel, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan, qmap,
+                              scale * 1.4426950408889634f, out, lse));
+    if (plan.clusters > 1)
+        ECHO_CUDA_OK(launch_after(false, chunk_join_kernel, dim3(static_cast<unsigned>(8 * sm_count())), kJT, 0, s, a, plan, out, lse));
+    return ECHO_OK;
 }

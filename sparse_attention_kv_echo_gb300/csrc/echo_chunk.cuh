@@ -8,9 +8,6 @@
 
 namespace echo {
 
-// Trees in tiles of 128 tokens (echo_mla_tree.cu); arguments checked, workspace and outputs too.
-int launch_tree_wide(const ChunkArgs& a, uint16_t* out, float* lse, void* ws, cudaStream_t s);
-
 namespace {
 
 constexpr int kM = 128;                  // (row, head) pairs per group

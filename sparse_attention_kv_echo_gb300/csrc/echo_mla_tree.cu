@@ -536,27 +536,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 }  // namespace
+}  // namespace echo
 
-int launch_tree_wide(const ChunkArgs& a, uint16_t* out, float* lse, void* ws, cudaStream_t s) {
-    const int64_t cap = plan_cap(a.n_rows, a.heads, a.B, false);
+extern "C" int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q,
+                             const uint32_t* mask, int words, const int64_t* tok_off, const int64_t* tok_end,
+                             int64_t n_tokens, const echo_pages* pages, float scale, uint16_t* out, float* lse, void* ws,
+                             size_t ws_bytes, int32_t* status, echo_stream_t stream) {
+    using namespace echo;
+    const int rc = check_chunk(B, row_off, n_rows, heads, q, tok_off, n_tokens, pages, 0, 0, scale, status);
+    if (rc) return rc;
+    if (words < 1) return ECHO_EINVAL;
+    if (words > ECHO_TREE_MAX_WORDS) return ECHO_EUNSUPPORTED;
+    if (n_rows == 0) return ECHO_OK;
+    if (!mask || !out || !lse || !ws || !is_aligned(out, 16) || !is_aligned(ws, 256)) return ECHO_EINVAL;
+    if (ws_bytes < echo_mla_chunk_workspace_size(n_rows, heads, B)) return ECHO_EINVAL;
+    ChunkArgs a = chunk_args(B, row_off, n_rows, heads, q, tok_off, tok_end, n_tokens, pages, nullptr, 0, 0, 0, scale, status);
+    a.mask = mask;
+    a.words = words;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t cap = plan_cap(n_rows, heads, B, false);
     Plan plan = plan_in(ws, cap);
-    plan.least = kMinUnits;
-    plan.ahead = 0;
     CUtensorMap qmap;
-    if (encode_tmap_bytes_2d(&qmap, a.q, kLatRowBytes, static_cast<uint64_t>(a.n_rows) * a.heads, 128, 64)) return ECHO_ECUDA;
+    if (encode_tmap_bytes_2d(&qmap, q, kLatRowBytes, static_cast<uint64_t>(n_rows) * heads, 128, 64)) return ECHO_ECUDA;
     static int cached[64];
     plan.clusters = cluster2_count(tree_kernel, kThreads, kSmem, kMaxClusters, cached);
     if (plan.clusters < 1) return ECHO_ECUDA;
     ECHO_CUDA_OK(prefer_max_shared(chunk_plan_kernel<kTok>));
     ECHO_CUDA_OK(prefer_max_shared(chunk_join_kernel));
+    plan.least = kMinUnits;
+    plan.ahead = 0;
     plan.small = false;
-    // (behind the call that made the masks, whose kernel lets these start; the masks are read when that has ended)
+    // behind the call that made the masks, whose kernel lets the plan start: the masks are read when that has ended
     ECHO_CUDA_OK(launch_after(false, chunk_plan_kernel<kTok>, dim3(1), kPT, 0, s, a, plan));
     ECHO_CUDA_OK(launch_after(false, tree_kernel, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan, qmap,
-                              a.scale * 1.4426950408889634f, out, lse));
+                              scale * 1.4426950408889634f, out, lse));
     if (plan.clusters > 1)
         ECHO_CUDA_OK(launch_after(false, chunk_join_kernel, dim3(static_cast<unsigned>(8 * sm_count())), kJT, 0, s, a, plan, out, lse));
     return ECHO_OK;
 }
-
-}  // namespace echo
