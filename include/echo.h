@@ -697,7 +697,7 @@ int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, cons
  *   dtype ECHO_F32 or ECHO_BF16, of target and draft both (16-byte aligned).
  * What is left of a token is summed as a whole number, good to 2^-48, so equal inputs give equal
  * results in any batch and on any launch, and a test falls on the right side of its border unless it is
- * within some 2^-40 of it.  Probabilities are to be in [0, 1] with a sum of at most 8 (of a row
+ * within some 2^-40 of it.  Probabilities are to be in [0, 1] with a sum below 8 (of a row
  * with a larger sum any token may come): NaN and values outside [0, 2] count as 0 and 2 and
  * set ECHO_ST_NAN where they are read; a row that is 0 throughout gives token 0 and ECHO_ST_BADDATA; uniform numbers outside [0, 1) (or NaN) count as the
  * nearest in it.  Greedy: NaN is below every number and sets ECHO_ST_NAN.  A node

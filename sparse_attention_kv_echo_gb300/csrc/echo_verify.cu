@@ -641,6 +641,7 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
             if (sm.ask == kEnd && greedy) break;
         }
         const int ask = sm.ask;
+        const bool last = sm.last;  // (read here: warp 0 may be in its next walk before the others ask for it)
         if (ask != kEnd || !sm.fresh) {
             // ---- every CTA: its slice, a warp's slice of it
             const int j0 = min(mine * sm.row.per, sm.row.pieces), j1 = min(j0 + sm.row.per, sm.row.pieces);
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
             first = false;
             continue;
         }
-        if (ask == kSum && !(sm.last && total > 0)) {  // (a last child's rejection is followed by the draw at once)
+        if (ask == kSum && !(last && total > 0)) {  // (a last child's rejection is followed by the draw at once)
             if (tid == 0) {
                 sm.fresh = total > 0;
                 if (total > 0) {
