@@ -173,7 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
         bool ok = true, over = false;
         uint32_t pieces = 0;  // with tiles
-        while (ok && walk.next(&p)) {
+        while (walk.next(&p)) {  // a warp whose wait ran out goes on to the next vote, where all eight leave
             const bool lives = rig < p.g.rows;
             const int vhi = lives && p.g.nv > 0 ? p.g.pos0 + rig + 1 : 0;  // this row's tokens: v < vhi that its mask lets it see
             const uint32_t* const nodes = lives ? a.mask + static_cast<int64_t>(p.g.row0 + rig) * a.words : nullptr;
@@ -320,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = mbar_wait_watch(smem_addr(&ctl->fin_ready), (pieces - 1) & 1u, watch) &&
                  mbar_wait(smem_addr(&ctl->pv_done[1]), (t - 1) & 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            if (!ok) continue;
             tc_fence_after();
             uint8_t* const part =
                 part_of(plan, ci, p) + (static_cast<size_t>(static_cast<int>(c) * 64 + r_cta) * kLatDv + half * 256) * 4;
