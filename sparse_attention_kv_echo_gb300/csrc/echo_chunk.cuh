@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kPT) chunk_plan_kernel(ChunkArgs a, Plan plan)
     __shared__ uint32_t scratch[kPT / 32 + 1];
     __shared__ int64_t scratch64[kPT / 32];
     pdl_launch_dependents();
+    pdl_wait();  // a tree's plan is scheduled beside the kernel before it, whatever that reads and writes
     const int tid = threadIdx.x;
     const int per = rows_per_group(a.heads, a.sel != nullptr);
     uint32_t base = 0;
@@ -233,7 +234,6 @@ __global__ void __launch_bounds__(kPT) chunk_plan_kernel(ChunkArgs a, Plan plan)
         plan.cum[groups] = sum;
         *plan.head = make_head(sum, groups, plan);
     }
-    pdl_wait();  // a tree's plan may start beside the kernel that makes its masks: the attention behind it needs both ended
 }
 
 // A leg, at most kLeg<kTok> tiles, of the part of a group that a share holds (a piece): tiles [lo, hi) of `tiles`.
