@@ -236,6 +236,19 @@ __global__ void __launch_bounds__(kPT) chunk_plan_kernel(ChunkArgs a, Plan plan)
     }
 }
 
+// The plan of a small call by a kernel of one warp.
+template <int kTok>
+__global__ void __launch_bounds__(32) chunk_plan_small_kernel(ChunkArgs a, Plan plan) {
+    __shared__ int64_t cum[kInline + 1];
+    pdl_launch_dependents();
+    pdl_wait();
+    plan_small<kTok>(a, plan, plan.head, plan.group, cum);
+    __syncwarp();
+    const int lane = threadIdx.x, groups = plan.head->groups;
+    if (lane <= groups) plan.cum[lane] = cum[lane];
+    if (lane == 0 && groups == 32) plan.cum[32] = cum[32];
+}
+
 // A leg, at most kLeg<kTok> tiles, of the part of a group that a share holds (a piece): tiles [lo, hi) of `tiles`.
 struct Piece {
     Group g;

@@ -562,12 +562,14 @@ extern "C" int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int 
     plan.clusters = cluster2_count(tree_kernel, kThreads, kSmem, kMaxClusters, cached);
     if (plan.clusters < 1) return ECHO_ECUDA;
     ECHO_CUDA_OK(prefer_max_shared(chunk_plan_kernel<kTok>));
+    ECHO_CUDA_OK(prefer_max_shared(chunk_plan_small_kernel<kTok>));
     ECHO_CUDA_OK(prefer_max_shared(chunk_join_kernel));
     plan.least = kMinUnits;
     plan.ahead = 0;
     plan.small = false;
     // behind the call that made the masks, whose kernel lets the plan start: the masks are read when that has ended
-    ECHO_CUDA_OK(launch_after(false, chunk_plan_kernel<kTok>, dim3(1), kPT, 0, s, a, plan));
+    if (B <= kInline && cap <= kInline) ECHO_CUDA_OK(launch_after(false, chunk_plan_small_kernel<kTok>, dim3(1), 32, 0, s, a, plan));
+    else ECHO_CUDA_OK(launch_after(false, chunk_plan_kernel<kTok>, dim3(1), kPT, 0, s, a, plan));
     ECHO_CUDA_OK(launch_after(false, tree_kernel, dim3(static_cast<unsigned>(2 * plan.clusters)), kThreads, kSmem, s, a, plan, qmap,
                               scale * 1.4426950408889634f, out, lse));
     if (plan.clusters > 1)
