@@ -667,9 +667,11 @@ int echo_tree_masks(int B, const int64_t* row_off, int64_t n_rows, const int32_t
  * bits, not ancestors alone: a row without its own bit does not see itself).  Tokens
  * without a cache row are not seen; a row that sees nothing has out = 0 and lse = -inf.
  * mask [n_rows,words] u32, device.  The rows of a request with more than 32 * words see
- * nothing and set ECHO_ST_BADDATA.  The other arguments, the workspace (echo_mla_chunk_workspace_size)
- * and the errors as echo_mla_chunk; words < 1 or no mask: ECHO_EINVAL, words >
- * ECHO_TREE_MAX_WORDS: ECHO_EUNSUPPORTED.
+ * nothing and set ECHO_ST_BADDATA.  Every cache row of a request's context must be finite,
+ * those of nodes that no row sees too: they are read, with weights of zero.  The other
+ * arguments, the workspace (echo_mla_chunk_workspace_size) and the errors as
+ * echo_mla_chunk; words < 1 or no mask: ECHO_EINVAL, words > ECHO_TREE_MAX_WORDS:
+ * ECHO_EUNSUPPORTED.
  */
 int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q, const uint32_t* mask,
                   int words, const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_pages* pages,
@@ -692,20 +694,23 @@ int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, cons
  * NULL: greedy; target may then hold logits, draft is not read, a child is accepted
  * when its token is the first of target[v]'s largest, and that is the token behind the path.
  *   path [n_rows] int32: the accepted nodes of request b in order from row_off[b] on
- *     (node 0 first), -1 behind; rows outside every request left as they were; count [B] int32: how many (>= 1 with rows, else 0);
- *     next [B] int32: the token behind the path (-1 without rows).
+ *     (node 0 first), -1 behind; rows outside every request left as they were;
+ *   count [B] int32: how many (>= 1 with rows, else 0);
+ *   next [B] int32: the token behind the path (-1 without rows);
  *   dtype ECHO_F32 or ECHO_BF16, of target and draft both (16-byte aligned).
- * What is left of a token is summed as a whole number, good to 2^-48, so equal inputs give equal
- * results in any batch and on any launch, and a test falls on the right side of its border unless it is
- * within some 2^-40 of it.  Probabilities are to be in [0, 1] with a sum below 8 (of a row
- * with a larger sum any token may come): NaN and values outside [0, 2] count as 0 and 2 and
- * set ECHO_ST_NAN where they are read; a row that is 0 throughout gives token 0 and ECHO_ST_BADDATA; uniform numbers outside [0, 1) (or NaN) count as the
- * nearest in it.  Greedy: NaN is below every number and sets ECHO_ST_NAN.  A node
- * whose token is not in [0, vocab) is not accepted and changes nothing (when it is tried:
- * ECHO_ST_BADDATA); a request of more than ECHO_TREE_MAX_NODES rows or with inconsistent row
- * bounds has count 0 and next -1, and sets ECHO_ST_BADDATA.  Nodes whose parent is out of range are never
- * reached.  Which rows of target and draft are read whole: those of nodes with a rejection,
- * and of the last.
+ * What is left of a token is summed as a whole number, good to 2^-48, so equal inputs give
+ * equal results in any batch and on any launch, and a test falls on the right side of its
+ * border unless it is within some 2^-40 of it.
+ * Probabilities are to be in [0, 1] with a sum below 8 (of a row with a larger sum any token
+ * may come): NaN and values outside [0, 2] count as 0 and 2 and set ECHO_ST_NAN where they
+ * are read; a row that is 0 throughout gives token 0 and ECHO_ST_BADDATA; uniform numbers
+ * outside [0, 1) (or NaN) count as the nearest in it and set ECHO_ST_BADDATA.  Greedy: NaN
+ * is below every number and sets ECHO_ST_NAN.
+ * A node whose token is not in [0, vocab) is not accepted and changes nothing (when it is
+ * tried: ECHO_ST_BADDATA).  Nodes whose parent is out of range are never reached and set
+ * ECHO_ST_BADDATA.  A request of more than ECHO_TREE_MAX_NODES rows or with inconsistent row
+ * bounds has count 0 and next -1, and sets ECHO_ST_BADDATA.  Read whole are the rows of
+ * target and draft of nodes with a rejection, and of the last node.
  * Errors: ECHO_EINVAL (sizes, NULL or misaligned pointers, one of u_node and u_pick),
  * ECHO_EUNSUPPORTED (B, n_rows, vocab > ECHO_MAX_VOCAB, dtype), ECHO_ECUDA.
  */
@@ -726,12 +731,13 @@ int echo_draft_verify(int B, const int64_t* row_off, int64_t n_rows, const int32
  * page_tab, page and req_rows = 0 are the echo_pages of a layer.
  * Here tok_off[b] must be a multiple of page, so that each entry belongs to one
  * request (else, or with inconsistent bounds, the request is left as it was and
- * ECHO_ST_BADDATA set); tok_end [B] is required where it is an argument.  Table entries that name no page of the
- * pool, and counts that would fall below 0, set ECHO_ST_BADDATA.
+ * ECHO_ST_BADDATA set); tok_end [B] is required where it is an argument.  Table entries
+ * that name no page of the pool, and counts that would fall below 0, set ECHO_ST_BADDATA.
  * All of them: one call at a time on a pool (the calls read and write its table and
- * counts); equal inputs give equal tables, whatever the launch.  ws:
- * echo_pages_workspace_size(B, n_pages) bytes, 256-byte aligned, B being the requests or pairs of the call; contents need not
- * be kept, calls on two pools that may run at the same time need their own.
+ * counts); equal inputs give equal tables, whatever the launch.
+ * ws: echo_pages_workspace_size(B, n_pages) bytes, 256-byte aligned, B being the requests or
+ * pairs of the call; contents need not be kept, calls on two pools that may run at the same
+ * time need their own.
  * Errors: ECHO_EINVAL (sizes, NULL or misaligned pointers, a small workspace),
  * ECHO_EUNSUPPORTED (B > ECHO_MAX_REQUESTS, n_pages > ECHO_POOL_MAX_PAGES), ECHO_ECUDA.
  */
@@ -751,14 +757,14 @@ size_t echo_pages_workspace_size(int B, int64_t n_pages);
 
 /*
  * Pages for the tokens [tok_end[b], want[b]) of every request, to be written by the
- * caller: entries of those tokens without a page take the lowest free pages, in the order of
- * requests and entries.  A page of theirs that other entries name too is
- * replaced by a free one (copy on write; the rows before tok_end[b] are copied to it).  A
- * request is served whole or not at all: when the free pages do not reach, it and
- * those after it that need any are left as they were, and ECHO_ST_FULL is set.  room [B] int64 (may be
- * NULL): want[b] when served, else tok_end[b].  tok_end[b] <= want[b] <=
- * tok_off[b+1], and a request whose last page is partly used must have that page (else ECHO_ST_BADDATA; not served).
- * The caller sets tok_end when it has the rows.
+ * caller: entries of those tokens without a page take the lowest free pages, in the order
+ * of requests and entries.  A page of theirs that other entries name too is replaced by a
+ * free one (copy on write; the rows before tok_end[b] are copied to it).  A request is
+ * served whole or not at all: when the free pages do not reach, it and those after it that
+ * need any are left as they were, and ECHO_ST_FULL is set.
+ * room [B] int64 (may be NULL): want[b] when served, else tok_end[b].  tok_end[b] <= want[b]
+ * <= tok_off[b+1], and a request whose last page is partly used must have that page (else
+ * ECHO_ST_BADDATA; not served).  The caller sets tok_end when it has the rows.
  */
 int echo_pages_reserve(int B, const int64_t* tok_off, const int64_t* tok_end, const int64_t* want, int64_t n_tokens,
                        const echo_page_pool* pool, int64_t* room, void* ws, size_t ws_bytes, int32_t* status,
@@ -776,10 +782,11 @@ int echo_pages_free(int B, const int64_t* tok_off, const int64_t* tok_end, int64
  * Forks: for each pair i < n, request dst[i] gives up what it holds and gets the context of
  * request src[i] (requests of the B that tok_off and tok_end describe): its full pages shared,
  * the rows of a partly used last page copied to the lowest free one (in the order of the
- * pairs), and tok_end[dst[i]] set to its length.  No page for the last rows: the context ends with its
- * last full page, and ECHO_ST_FULL is set.  Several pairs may have one src.  A pair with
- * src or dst out of range or equal, a dst that an earlier pair has, that is some pair's src, or whose
- * region is shorter than the context is left out and sets ECHO_ST_BADDATA.  n <= ECHO_MAX_REQUESTS; ws for n.
+ * pairs), and tok_end[dst[i]] set to where its context then ends.  No page for the last
+ * rows: the context ends with its last full page, and ECHO_ST_FULL is set.  Several pairs
+ * may have one src.  A pair with src or dst out of range or equal, a dst that an earlier
+ * pair has, that is some pair's src, or whose region is shorter than the context is left
+ * out and sets ECHO_ST_BADDATA.  n <= ECHO_MAX_REQUESTS; ws for n.
  */
 int echo_pages_fork(int n, const int32_t* src, const int32_t* dst, int B, const int64_t* tok_off, int64_t* tok_end,
                     int64_t n_tokens, const echo_page_pool* pool, void* ws, size_t ws_bytes, int32_t* status,
@@ -798,9 +805,10 @@ int echo_pages_compact(int64_t n_tokens, const echo_page_pool* pool, int32_t* us
  * row_off), the cache rows of the tokens base + path[row_off[b] + i] move to the
  * tokens base + i, i < count[b], in every layer, and new_end[b] = base + count[b]
  * (new_end [B] int64, another array than tok_end).  path and count as echo_draft_verify writes them: ascending.
- * Enqueue echo_pages_free with new_end for the pages of the rejected rows.  A path
- * that does not ascend or leaves the tree, a count beyond n_b, more rows than tokens, a token without a page or one
- * whose page others name too: the request is left as it was, new_end[b] = tok_end[b], ECHO_ST_BADDATA.
+ * Enqueue echo_pages_free with new_end for the pages of the rejected rows.  A path that does
+ * not ascend or leaves the tree, a count beyond n_b, more rows than tokens, a row to move
+ * without a page, or to a page that others name too: the request is left as it was,
+ * new_end[b] = tok_end[b], and ECHO_ST_BADDATA is set.
  */
 int echo_rows_keep(int B, const int64_t* row_off, int64_t n_rows, const int32_t* path, const int32_t* count,
                    const int64_t* tok_off, const int64_t* tok_end, int64_t n_tokens, const echo_page_pool* pool,

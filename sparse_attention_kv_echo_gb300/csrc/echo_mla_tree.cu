@@ -1,12 +1,23 @@
-// echo_mla_tree.cu -- attention of trees of drafted tokens over a long paged latent cache.
+// echo_mla_tree.cu -- attention of trees of drafted tokens over a paged latent cache (echo.h, echo_mla_tree).
 //
-// echo_chunk.cu with tiles of 128 tokens, for trees alone.  There an MMA of QK (M = 128 pairs, N = 64 tokens) reads 3 KB of
-// shared memory for 16 cycles of products and takes 25; with N = 128 it reads 4 KB for 32 and takes 32, so a token costs 1.1
-// K cycles' worth less.  Shared memory has no second stage for 128 tokens' K: the stage is a ring of three thirds (three of the
-// nine 64-dim atoms each), freed by QK and filled with the next tile's third while QK goes on through the others and PV runs.
-// Per CTA of the pair: 64 tokens' K (CTA c: tokens [64c, 64c + 64) of the tile), 256 dims of V of 64 tokens at a time (two
-// halves of the tile, a stage each), P of each half in a buffer of its own, four buffers of S of 64 columns.  In the
-// tensor memory S of a tile is lane = (token half, row), 64 columns, so the threads of half h write P of half h, whole rows.
+// As echo_chunk.cu: a cluster of two CTAs takes 128 (row, head) pairs at a time, S = Q K^T and O += P V by
+// cta_group::2 MMAs (M = 128) with O in the tensor memory, a lazy reference maximum, equal shares of tiles,
+// cut groups joined behind.  A tree differs in what a row sees: every token before the tree, and of the tree's own
+// tokens those whose bit the row's mask has; only the tiles that reach into the tree look at masks.
+//
+// Tiles have 128 tokens here.  An MMA of QK (M = 128 pairs, N = 64 tokens) reads 3 KB of shared memory for 16 cycles of
+// products and takes 25; with N = 128 it reads 4 KB for 32 and takes 32.  Shared memory has no second stage for 128
+// tokens' K: the stage is a ring of three thirds (three of the nine 64-dim atoms each), freed by QK and filled with the next
+// tile's third while QK goes on through the others and PV runs.  Per CTA of the pair: 64 tokens' K (CTA c: tokens
+// [64c, 64c + 64) of the tile), 256 dims of V of 64 tokens at a time (two halves of the tile, a stage each), P of each half
+// in a buffer of its own, four buffers of S of 64 columns.  In the tensor memory S of a tile is lane = (token half, row),
+// 64 columns, so the threads of half h write P of half h, whole rows.  Softmax takes two sets of four warps, 32 columns
+// each: one set needs 3300 cycles a tile, more than the MMAs.
+//
+// What bounds it: the MMAs of a tile are 2176 cycles, a tile takes some 2690: copies into shared memory and the operands
+// read from it share its ports.  Tensor pipe 75% active on 16 trees of 12 to 48 nodes over 2048 to 32768 tokens, 128 heads
+// (1.18 ms a launch by itself, 1.52 PFLOP/s; 1.35 among others, under the power cap).  Tiles of 64 tokens took 1.31 ms, 58%.
+// 64 nodes over 131072 tokens: 1.41 ms by itself, 1.65 among others (tiles of 64: 1.82).
 #include "echo_chunk.cuh"
 
 namespace echo {

@@ -3,7 +3,8 @@
 // A block takes the requests in turn, a thread its nodes: it walks from its node up to
 // the root over the parents in shared memory, setting bits.  Indices fall on the way (a
 // parent comes before its child), so the words are finished from the last to the first and
-// each is written once.  What bounds it is the latency of one walk.
+// each is written once.  What bounds it is the launch and the latency of one walk (48 chains of
+// four 3.9 us, a tree of 64 nodes 6, by themselves).
 #include "echo_common.cuh"
 
 namespace echo {
