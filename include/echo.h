@@ -710,7 +710,8 @@ int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, cons
  * tried: ECHO_ST_BADDATA).  Nodes whose parent is out of range are never reached and set
  * ECHO_ST_BADDATA.  A request of more than ECHO_TREE_MAX_NODES rows or with inconsistent row
  * bounds has count 0 and next -1, and sets ECHO_ST_BADDATA.  Read whole are the rows of
- * target and draft of nodes with a rejection, and of the last node.
+ * target and draft of nodes with a rejection, and of the last node; greedy, those of
+ * target of the path's nodes, or of all nodes (a NaN is reported where the path goes).
  * Errors: ECHO_EINVAL (sizes, NULL or misaligned pointers, one of u_node and u_pick),
  * ECHO_EUNSUPPORTED (B, n_rows, vocab > ECHO_MAX_VOCAB, dtype), ECHO_ECUDA.
  */

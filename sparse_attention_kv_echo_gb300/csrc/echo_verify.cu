@@ -17,12 +17,15 @@
 // sums when no child was accepted since: the slice whose running sum passes u * total, in it the
 // warp's, in that the part that a warp of the CTA now takes, in that the token.
 //
+// Greedy asks for the largest of a row in the same way, node after node, or for those of all nodes at once where they are
+// few and short.
+//
 // Sums are of whole numbers, so they do not hang on their order, and the token drawn is the same on
 // any number of CTAs.  What bounds the call: a few chains or trees, the latency of its steps (one chain of five
 // over 32000 tokens, 9.8 us in a graph: 1.9 to read the tree, 0.5 a walk, 2 a sum with its barrier, 2 the draw); many, the
 // instructions of the sums, some 10 a token and pair of values, and the chain of rejections of the longest walk.  64 chains of
-// six over 131072 tokens in fp32 19 us (60 MB, a third of the memory's rate), 32 trees of 32 to 48 nodes in bf16 33 us, 16
-// greedy trees over 50001 tokens 21 us (each in a graph).
+// six over 131072 tokens in fp32 19 us (60 MB, a third of the memory's rate), 32 trees of 32 to 48 nodes in bf16 31 us, 16
+// greedy trees of 8 to 24 over 50001 tokens 15 us (each in a graph).
 #include <cuda_bf16.h>
 
 #include "echo_common.cuh"
@@ -51,7 +54,17 @@ struct VerifyArgs {
     int32_t* count;
     int32_t* next;
     int32_t* status;
+    int64_t all_bytes;  // greedy: rows of at most so many bytes have their best found at once
 };
+
+// Greedy: a request whose rows are at most so many bytes for each CTA that has an SM to itself (half where two share one) has
+// the best of every node found at once, all on the way or not; a larger one, node after node, 2.3 us and more each.  At
+// once against in turn: a chain of 5, 32000 tokens in fp32 (80 KB a CTA), 8.6 against 14.9 us, 8 chains of 6 over 131072 in bf16
+// (196 KB) 11.3 against 15.4, a tree of 16 (524 KB) 18.5 against 9.3, 64 trees of 16 over 32000 (256 KB, two to an SM) 16.4
+// against 13.9.
+constexpr int64_t kAllBytes = 256 * 1024;
+constexpr int kAllNodes = 128;
+constexpr int kAllFly = 8;               // 16-byte pieces a lane has in flight then (4: up to 5% slower)
 
 // What the walk asks of the cluster: sum up what is left, or find the largest, at a node.
 enum Ask : int { kSum, kBest, kEnd };
@@ -92,6 +105,12 @@ struct VerifySmem {
     // the walk of this CTA's warp 0, between its turns
     uint64_t S_at, R;              // the residual at v
     int v, c, len, outs_at, best;  // node, the last child tried, nodes accepted, tokens left out, greedy: v's best
+    bool all;                      // greedy: every node's best is known
+    // each node's best key over this CTA's pieces, and whether they have a NaN; the same of every CTA
+    unsigned long long own[kAllNodes];
+    uint32_t own_nan[kAllNodes / 32];
+    uint64_t bests[kMaxCluster][kAllNodes];
+    uint32_t nans[kMaxCluster][kAllNodes / 32];
     int16_t path[kNodes];
     uint64_t warp_sum[kVWarps];
     uint64_t fine[kVWarps];
@@ -411,11 +430,10 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
 }
 
 // The first of the largest in pieces [j0, j1): its order key above, the complement of its index below (NaN: key 0).
-template <class T>
-__device__ __forceinline__ uint64_t best_of(const VerifySmem& sm, int j0, int j1, bool* nan) {
-    constexpr int n = Vec<T>::n, kFly = 2;
+template <class T, int kFly>
+__device__ __forceinline__ uint64_t best_of(const Row r, int j0, int j1, bool* nan) {
+    constexpr int n = Vec<T>::n;
     const int lane = threadIdx.x & 31;
-    const Row r = sm.row;
     float best = -INFINITY;
     int at = -1, first = -1;  // the best number's token; the first token, where all are NaN
 #pragma unroll 1
@@ -464,6 +482,41 @@ __device__ __forceinline__ uint64_t best_of(const VerifySmem& sm, int j0, int j1
     return warp_max64(key);
 }
 
+__device__ __forceinline__ int token_of(uint64_t key) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key)); }
+
+// Greedy, every node's best at once: the pieces of a request's rows are shared out evenly among the cluster's warps, and
+// each CTA tells the others its best of each node.
+template <class T>
+__device__ __forceinline__ void all_bests(const VerifyArgs& a, VerifySmem& sm, int64_t r0, int n, int mine, int parts, uint32_t ctas) {
+    constexpr int w = Vec<T>::n;
+    const int tid = threadIdx.x, lane = tid & 31, words = (n + 31) >> 5;
+    if (tid < n) sm.own[tid] = 0;
+    if (tid < words) sm.own_nan[tid] = 0u;
+    __syncthreads();
+    const int P = static_cast<int>((a.vocab + 2 * (w - 1)) / w);  // a row has this many pieces at most
+    const int64_t total = static_cast<int64_t>(n) * P;            // (kAllBytes: far below 2^31)
+    int x = static_cast<int>(total * mine / parts);
+    const int end = static_cast<int>(total * (mine + 1) / parts);
+    while (x < end) {
+        const int node = x / P, j0 = x - node * P, j1 = min(P, j0 + end - x);
+        const Row r = row_of<T>(a, r0 + node, parts);
+        bool nan = false;
+        const uint64_t key = best_of<T, kAllFly>(r, j0, min(j1, r.pieces), &nan);
+        nan = __any_sync(0xffffffffu, nan);
+        if (lane == 0) {
+            atomicMax(&sm.own[node], static_cast<unsigned long long>(key));
+            if (nan) atomicOr(&sm.own_nan[node >> 5], 1u << (node & 31));
+        }
+        x += j1 - j0;
+    }
+    __syncthreads();
+    const uint32_t rank = cluster_rank();
+    for (uint32_t k = 0; k < ctas; ++k) {
+        if (tid < n) remote_store64(remote_addr(&sm.bests[rank][tid], k), sm.own[tid]);
+        if (tid < words) remote_store32(remote_addr(&sm.nans[rank][tid], k), sm.own_nan[tid]);
+    }
+}
+
 __device__ __forceinline__ float unit_interval(float u, bool* bad) {
     *bad |= !(u >= 0.f && u < 1.f);
     return fminf(fmaxf(u, 0.f), 0.99999994f);  // NaN: 0
@@ -480,12 +533,23 @@ __device__ __forceinline__ bool accepts(float u, uint64_t d, uint64_t R, uint64_
 
 // A turn of the walk, by a warp: on from the last child tried to the next question.
 template <class T>
-__device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, bool greedy, int parts, bool* odd) {
+__device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, bool greedy, int parts, uint32_t ctas, bool* odd, bool* bad) {
     __syncwarp();
     const int lane = threadIdx.x & 31, n = sm.n;
     int ask = -1, v = sm.v, c = sm.c, len = sm.len, outs = sm.outs_at;
     uint64_t S = sm.S_at, R = sm.R;
     bool fresh = sm.fresh, last = false;
+    const bool all = sm.all;
+    int best = sm.best;
+    const auto known = [&](int of) {
+        uint64_t key = 0;
+        for (uint32_t k = 0; k < ctas; ++k) {
+            key = max(key, sm.bests[k][of]);
+            *bad |= (sm.nans[k][of >> 5] >> (of & 31)) & 1u;
+        }
+        return token_of(key);
+    };
+    if (all) best = known(v);
     const auto next_child = [&](int of, int behind) {
         for (int i0 = behind + 1; i0 < n; i0 += 32) {
             const uint32_t m = __ballot_sync(0xffffffffu, i0 + lane < n && sm.up[i0 + lane] == of);
@@ -508,7 +572,7 @@ __device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, bool g
         }
         bool yes;
         if (greedy) {
-            yes = x == sm.best;
+            yes = x == best;
         } else if (S == 0 && outs == 0) {
             yes = sm.yes[c];
         } else {
@@ -528,7 +592,8 @@ __device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, bool g
             R = 1ull << 60;
             outs = 0;
             fresh = false;
-            if (greedy) ask = kBest;
+            if (all) best = known(v);
+            if (greedy && !all) ask = kBest;
             else found = next_child(v, c);
         } else if (greedy) {
             found = next_child(v, c);
@@ -547,6 +612,7 @@ __device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, bool g
         sm.R = R;
         sm.fresh = fresh;
         sm.ask = ask;
+        sm.best = best;
         sm.last = last;
         sm.S = S;
         sm.outs = outs;
@@ -619,9 +685,11 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
         }
         __syncwarp();
     }
-    // greedy: the root's best is asked for at once, and answered behind the same barrier as the tree
-    bool first = greedy;
+    // greedy: every node's best is found, or the root's is asked for, at once, and known behind the same barrier as the tree
+    const bool all = greedy && whole && r1 > r0 && r1 - r0 <= kAllNodes && (r1 - r0) * a.vocab * static_cast<int64_t>(sizeof(T)) <= a.all_bytes;
+    bool first = greedy && !all;
     if (tid == 0) {
+        sm.all = all;
         sm.path[0] = 0;
         sm.v = sm.c = sm.outs_at = sm.outs = 0;
         sm.len = 1;
@@ -634,11 +702,12 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
             if (!whole || r1 == r0) sm.row.pieces = sm.row.per = 0;
         }
     }
+    if (all) all_bests<T>(a, sm, r0, static_cast<int>(r1 - r0), mine, parts, ctas);
     if (first) __syncthreads();
     else cluster_sync_all();
     for (int asked = 1; first || sm.n > 0; ++asked) {
         if (!first) {
-            if (warp == 0) walk<T>(a, sm, greedy, parts, &odd);
+            if (warp == 0) walk<T>(a, sm, greedy, parts, ctas, &odd, &bad);
             __syncthreads();
             if (sm.ask == kEnd && greedy) break;
         }
@@ -647,7 +716,7 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
         if (ask != kEnd || !sm.fresh) {
             // ---- every CTA: its slice, a warp's slice of it
             const int j0 = min(mine * sm.row.per, sm.row.pieces), j1 = min(j0 + sm.row.per, sm.row.pieces);
-            const uint64_t sum = ask == kBest ? best_of<T>(sm, j0, j1, &bad) : slice_left<T>(sm, j0, j1, &bad);
+            const uint64_t sum = ask == kBest ? best_of<T, 2>(sm.row, j0, j1, &bad) : slice_left<T>(sm, j0, j1, &bad);
             if (lane == 0) sm.warp_sum[warp] = sum;
             __syncthreads();
             if (warp == 0) {
@@ -668,7 +737,7 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
             if (k < rank) before += x;
         }
         if (ask == kBest) {
-            if (tid == 0) sm.best = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(total));
+            if (tid == 0) sm.best = token_of(total);
             first = false;
             continue;
         }
@@ -755,9 +824,11 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
 }
 
 template <class T>
-int launch_verify(const VerifyArgs& a, int B, cudaStream_t s) {
+int launch_verify(VerifyArgs a, int B, cudaStream_t s) {
+    const int sms = sm_count();
     int ctas = kMaxCluster;
-    while (ctas > 1 && static_cast<int64_t>(B) * ctas > 2ll * sm_count()) ctas /= 2;
+    while (ctas > 1 && static_cast<int64_t>(B) * ctas > 2ll * sms) ctas /= 2;
+    a.all_bytes = ctas * (static_cast<int64_t>(B) * ctas > sms ? kAllBytes / 2 : kAllBytes);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(B) * ctas);
     cfg.blockDim = dim3(kVT);
@@ -786,7 +857,7 @@ extern "C" int echo_draft_verify(int B, const int64_t* row_off, int64_t n_rows, 
     if (n_rows > 0 && (!parent || !token || !target || !path)) return ECHO_EINVAL;
     if ((u_node != nullptr) != (u_pick != nullptr)) return ECHO_EINVAL;
     if (!is_aligned(target, 16) || !is_aligned(draft, 16)) return ECHO_EINVAL;
-    const VerifyArgs a = {row_off, n_rows, parent, token, vocab, target, u_node ? draft : nullptr, u_node, u_pick, path, count, next, status};
+    const VerifyArgs a = {row_off, n_rows, parent, token, vocab, target, u_node ? draft : nullptr, u_node, u_pick, path, count, next, status, 0};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == ECHO_F32 ? launch_verify<float>(a, B, s) : launch_verify<__nv_bfloat16>(a, B, s);
 }

@@ -324,3 +324,25 @@ def test_another_stream_and_a_replayed_graph():
         torch.cuda.synchronize()
         assert (args[4].tolist(), args[5].tolist(), args[6].tolist()) == d.expected()
         d.u_node = torch.rand(15, generator=torch.Generator().manual_seed(k))
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("rows,vocab", [([128, 129, 1, 0, 127], 501), ([40, 3, 9], 20001), ([6] * 70, 4099), ([5] * 20, 33001),
+                                        ([2] * 170, 3001), ([17], 60000)])
+def test_greedy_with_few_and_many_nodes(rows, vocab, half):
+    # requests whose rows are looked through at once stand beside those that are walked row by row
+    t = Drafts(rows, vocab, reach=3, half=half, mode="greedy", seed=sum(rows))
+    t.check()
+
+
+@pytest.mark.parametrize("vocab", [300, 90001])
+def test_greedy_nan_counts_where_the_walk_goes(vocab):
+    # nodes 0 -> 1 -> 3 accepted, 2 not: only a NaN in a row of the path is reported, and no NaN is the largest
+    t = Drafts([4, 4], vocab, mode="greedy", seed=9)
+    t.parent = [-1, 0, 0, 1] * 2
+    best = [int(r.argmax()) for r in t.target]
+    t.token = [0, best[0], (best[0] + 1) % vocab, best[1], 0, best[4], (best[4] + 1) % vocab, best[5]]
+    t.target[2, 7] = t.target[6, 250] = float("nan")
+    assert t.check() == [3, 3]
+    t.target[3, (best[3] + 5) % vocab] = float("nan")
+    t.check(status=_lib().ST_NAN)
