@@ -381,16 +381,17 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int q) {
     }
 }
 
-// A warp's 32 rows x 256 dims of O, times f (a factor for each of a lane's rows), as bf16 to dst or, where that is
-// null, in fp32 to part; kLater: what the legs before left in part, by this thread, times fb is added first.
-template <bool kLater>
+// A warp's 32 rows x 256 dims of O (or kDims of them, from dim x0 on), times f (a factor for each of a lane's rows), as bf16
+// to dst or, where that is null, in fp32 to part; kLater: what the legs before left in part, by this thread, times fb is
+// added first.
+template <bool kLater, uint32_t kDims = 256>
 __device__ __forceinline__ void store_o(uint32_t taddr, const float (&f)[4], const float (&fb)[4], uint8_t* dst, uint8_t* part,
-                                        int live) {
+                                        int live, uint32_t x0 = 0) {
     const int lane = threadIdx.x & 31, q = lane & 3;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll 1
-        for (uint32_t x = 0; x < 256u; x += 32u) {
+        for (uint32_t x = x0; x < x0 + kDims; x += 32u) {
             float2 was[8];
             if constexpr (kLater) {
 #pragma unroll

@@ -12,7 +12,7 @@
 // [64c, 64c + 64) of the tile), 256 dims of V of 64 tokens at a time (two halves of the tile, a stage each), P of each half
 // in a buffer of its own, four buffers of S of 64 columns.  In the tensor memory S of a tile is lane = (token half, row),
 // 64 columns, so the threads of half h write P of half h, whole rows.  Softmax takes two sets of four warps, 32 columns
-// each: one set needs 3300 cycles a tile, more than the MMAs.
+// each, and 128 of the 256 of O in the storing: one set needs 3300 cycles a tile, more than the MMAs.
 //
 // What bounds it: the MMAs of a tile are 2176 cycles, a tile takes some 2690: copies into shared memory and the operands
 // read from it share its ports.  Tensor pipe 75% active on 16 trees of 12 to 48 nodes over 2048 to 32768 tokens, 128 heads
@@ -39,6 +39,10 @@ constexpr uint32_t kPBytes = 64 * 128;
 constexpr uint32_t kTmemCols = 512;      // O [0, 256) | S buffers of 64 columns
 constexpr int kSBufs = 4;
 constexpr uint32_t kSCol = 256;
+// Tokens that one or two groups read come from memory, and K has one stage: the next tile's rows are brought to L2 once this
+// tile's copies are under way (32 trees of eight behind 8000 tokens, 16 heads, 86.8 -> 80.6 us; looked up and fetched one to five
+// tiles further ahead, 90 to 104).  Tokens that many groups read are in L2 already (fetched ahead, 16 trees of 128 heads took
+// 1.58 ms for 1.32).
 constexpr float kLazy = 8.f;
 constexpr int kMinUnits = 2;             // least units per cluster (1, 3 and 4: slower small calls)
 constexpr uint32_t kIdescS = idesc_bf16_f32(kM, kTok);
@@ -62,7 +66,6 @@ struct Ctl {
     Watch watch;
     int first;                                           // the share's first group
     float mx[2][4][64];                                  // tile maxima, or a piece's sums, by (parity, 32 of the columns, row)
-    uint64_t fin_ready, fin_free;                        // a piece's factors are in fin / have been read
     uint64_t o_free;                                     // O of a piece has been read in both CTAs
     float fin[64];                                       // what O of a row is multiplied by
     // tokens of a tile that have a row, a bit each: written for tile t when QK of t - 1 has begun, hence S of t - 5 read
@@ -143,9 +146,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&ctl->s_full[i]), 1);
             mbar_init(smem_addr(&ctl->s_free[i]), 2 * kSoftmax / 32);
         }
-        mbar_init(smem_addr(&ctl->fin_ready), kSoftmax / 64);
-        mbar_init(smem_addr(&ctl->fin_free), kSoftmax / 64);
-        mbar_init(smem_addr(&ctl->o_free), 2 * kSoftmax / 64);
+        mbar_init(smem_addr(&ctl->o_free), 2 * kSoftmax / 32);
         for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&ctl->drain[i]), 1);
         watch_init(watch, a.wait_ns);
         fence_barrier_init();
@@ -177,13 +178,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t t = 0;  // tiles so far: the phase of a barrier passed once a tile is t & 1
 
     if (warp < 4 || warp >= 16) {
-        // ---- softmax: two threads to a TMEM lane = (token half, row of this CTA's 64), 32 of its 64 columns each; the second
-        // set of warps also stores the results
+        // ---- softmax and the storing of results: two threads to a TMEM lane = (token half, row of this CTA's 64), 32 of its 64
+        // columns of S each, 128 of its 256 of O
         const int set = warp >= 16, wq = warp & 3, half = wq >> 1, row = (wq & 1) * 32 + lane, mi = static_cast<int>(c) * 64 + row;
         const int rig = mi / a.heads;  // row within the group
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
         bool ok = true, over = false;
-        uint32_t pieces = 0;  // with tiles
         while (walk.next(&p)) {  // a warp whose wait ran out goes on to the next vote, where all eight leave
             const bool lives = rig < p.g.rows;
             const int vhi = lives && p.g.nv > 0 ? p.g.pos0 + rig + 1 : 0;  // this row's tokens: v < vhi that its mask lets it see
@@ -282,8 +282,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (p.hi > p.lo) {
                 float(&sums)[4][64] = ctl->mx[t & 1u];
                 sums[2 * half + set][row] = l;
-                if (pieces >= 1) ok = ok && mbar_wait(smem_addr(&ctl->fin_free), (pieces - 1) & 1u, abort);
-                ++pieces;
                 ok = !softmax_or(!ok);
                 if (!ok) break;
                 L = (sums[0][row] + sums[1][row]) + (sums[2][row] + sums[3][row]);
@@ -310,13 +308,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     lse[static_cast<int64_t>(p.g.row0) * a.heads + mi] = any ? (m + log2f(L)) * 0.69314718055994531f : -INFINITY;
                 }
             }
-            if (p.hi > p.lo) {
-                __syncwarp();
-                if (lane == 0 && set == 0) mbar_arrive(smem_addr(&ctl->fin_ready));
-                (void)softmax_or(false);  // the sums are read before the next tile's maxima
-            }
-            if (set == 0) continue;
-            // ---- the results: 16 rows x 32 columns at a time, four lanes to a row, so that stores are whole sectors
+            // ---- the results: 16 rows x 32 columns at a time, four lanes to a row, so that stores are whole sectors.  (One set
+            // storing alone kept the other waiting: 3.1 us of the 10 of a share of one tree of eight.)
             const bool direct = !p.left && !p.right && p.last;
             const int r_cta = (wq & 1) * 32;  // dims 256 half .., rows of this CTA's 64
             const int live = p.g.rows * a.heads - static_cast<int>(c) * 64 - r_cta;  // of this warp's 32 rows
@@ -324,12 +317,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint8_t* const dst = direct ? reinterpret_cast<uint8_t*>(out + at * kLatDv + half * 256) : nullptr;
             if (p.hi == p.lo) {  // nothing was seen
                 if (warp == 16 && lane == 0) watch_beat(watch);
-                for (int i = lane; i < 32 * 32; i += 32)
-                    if ((i >> 5) < live) reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i >> 5) * (kLatDv * 2))[i & 31] = make_uint4(0, 0, 0, 0);
+                for (int i = lane; i < 32 * 16; i += 32)
+                    if ((i >> 4) < live)
+                        reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i >> 4) * (kLatDv * 2))[16 * set + (i & 15)] = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            ok = mbar_wait_watch(smem_addr(&ctl->fin_ready), (pieces - 1) & 1u, watch) &&
-                 mbar_wait(smem_addr(&ctl->pv_done[1]), (t - 1) & 1u, abort);
+            (void)softmax_or(false);  // the factors are there, the sums read before the next tile's maxima
+            ok = mbar_wait(smem_addr(&ctl->pv_done[1]), (t - 1) & 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
             tc_fence_after();
@@ -344,9 +338,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 4; ++i) fb[i] = factors[8 * i + (lane >> 2)];
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ctl->fin_free));
-            if (p.later) store_o<true>(tmem + lane_base, f, fb, dst, part, live);
-            else store_o<false>(tmem + lane_base, f, fb, dst, part, live);
+            if (p.later) store_o<true, 128>(tmem + lane_base, f, fb, dst, part, live, 128u * set);
+            else store_o<false, 128>(tmem + lane_base, f, fb, dst, part, live, 128u * set);
             tc_fence_before();  // O is read: the next group's first PV may overwrite it
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(smem_addr(&ctl->o_free), 0);
@@ -392,6 +385,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 static_cast<uint16_t>(bits >> (16 * lane));
                         mbar_arrive(smem_addr(&ctl->k_full[0]));
                     }
+                }
+                if (plan.ahead && lane < 16) {  // this CTA's rows of the next tile
+                    const int64_t next = own.row(a);
+                    if (next >= 0) prefetch_l2(a.kv + next * kLatRowBytes, kLatRowBytes);
                 }
             }
         }
@@ -573,7 +570,7 @@ extern "C" int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int 
     plan.clusters = cluster2_count(tree_kernel, kThreads, kSmem, kMaxClusters, cached);
     if (plan.clusters < 1) return ECHO_ECUDA;
     plan.least = kMinUnits;
-    plan.ahead = 0;
+    plan.ahead = cap <= 2 * B;
     plan.small = false;
     // The plan is scheduled beside the kernel before it (the masks' lets it be) and waits for that to end.  One warp plans
     // a call of at most 32 requests and groups: one tree of eight nodes, 128 heads, 20.7 us against 22.0 with a block of 1024.
