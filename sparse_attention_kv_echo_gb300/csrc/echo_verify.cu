@@ -22,10 +22,10 @@
 //
 // Sums are of whole numbers, so they do not hang on their order, and the token drawn is the same on
 // any number of CTAs.  What bounds the call: a few chains or trees, the latency of its steps (one chain of five
-// over 32000 tokens, 9.8 us in a graph: 1.9 to read the tree, 0.5 a walk, 2 a sum with its barrier, 2 the draw); many, the
+// over 32000 tokens, 8.7 us in a graph: 1.9 to read the tree, 0.5 a walk, 2 a sum with its barrier, 2 the draw); many, the
 // instructions of the sums, some 10 a token and pair of values, and the chain of rejections of the longest walk.  64 chains of
-// six over 131072 tokens in fp32 19 us (60 MB, a third of the memory's rate), 32 trees of 32 to 48 nodes in bf16 31 us, 16
-// greedy trees of 8 to 24 over 50001 tokens 15 us (each in a graph).
+// six over 131072 tokens in fp32 19 us (60 MB, a third of the memory's rate), 32 trees of 32 to 48 nodes in bf16 30 us, 16
+// greedy trees of 8 to 24 over 50001 tokens 14 us (each in a graph).
 #include <cuda_bf16.h>
 
 #include "echo_common.cuh"
@@ -59,8 +59,8 @@ struct VerifyArgs {
 
 // Greedy: a request whose rows are at most so many bytes for each CTA that has an SM to itself (half where two share one) has
 // the best of every node found at once, all on the way or not; a larger one, node after node, 2.3 us and more each.  At
-// once against in turn: a chain of 5, 32000 tokens in fp32 (80 KB a CTA), 8.6 against 14.9 us, 8 chains of 6 over 131072 in bf16
-// (196 KB) 11.3 against 15.4, a tree of 16 (524 KB) 18.5 against 9.3, 64 trees of 16 over 32000 (256 KB, two to an SM) 16.4
+// once against in turn: a chain of 5, 32000 tokens in fp32 (80 KB a CTA), 8.2 against 14.9 us, 8 chains of 6 over 131072 in bf16
+// (196 KB) 11.0 against 15.4, a tree of 16 (524 KB) 18.5 against 9.3, 64 trees of 16 over 32000 (256 KB, two to an SM) 16.4
 // against 13.9.
 constexpr int64_t kAllBytes = 256 * 1024;
 constexpr int kAllNodes = 128;
@@ -532,15 +532,15 @@ __device__ __forceinline__ bool accepts(float u, uint64_t d, uint64_t R, uint64_
 }
 
 // A turn of the walk, by a warp: on from the last child tried to the next question.
-template <class T>
-__device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, bool greedy, int parts, uint32_t ctas, bool* odd, bool* bad) {
+template <class T, bool greedy>
+__device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, int parts, uint32_t ctas, bool* odd, bool* bad) {
     __syncwarp();
     const int lane = threadIdx.x & 31, n = sm.n;
     int ask = -1, v = sm.v, c = sm.c, len = sm.len, outs = sm.outs_at;
     uint64_t S = sm.S_at, R = sm.R;
     bool fresh = sm.fresh, last = false;
-    const bool all = sm.all;
-    int best = sm.best;
+    const bool all = greedy && sm.all;
+    int best = greedy ? sm.best : 0;
     const auto known = [&](int of) {
         uint64_t key = 0;
         for (uint32_t k = 0; k < ctas; ++k) {
@@ -612,7 +612,7 @@ __device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, bool g
         sm.R = R;
         sm.fresh = fresh;
         sm.ask = ask;
-        sm.best = best;
+        if (greedy) sm.best = best;
         sm.last = last;
         sm.S = S;
         sm.outs = outs;
@@ -629,15 +629,15 @@ __device__ __forceinline__ void walk(const VerifyArgs& a, VerifySmem& sm, bool g
     __syncwarp();
 }
 
-// T: the probabilities' type.
-template <class T>
+// T: the probabilities' type.  (Greedy apart: with both in one kernel, a chain of five took 17 us for 11 in a launch whose
+// instructions have to be fetched.)
+template <class T, bool greedy>
 __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
     __shared__ VerifySmem sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
     const int b = blockIdx.x / ctas;
     const int parts = static_cast<int>(ctas) * kVWarps, mine = static_cast<int>(rank) * kVWarps + warp;
-    const bool greedy = a.u_pick == nullptr;
     bool bad = false, odd = false;  // probabilities / other data that are none
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has started: the others may write to it
     // ---- CTA 0 reads the tree and hands it to all, so that every CTA walks on the same data
@@ -702,12 +702,14 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
             if (!whole || r1 == r0) sm.row.pieces = sm.row.per = 0;
         }
     }
-    if (all) all_bests<T>(a, sm, r0, static_cast<int>(r1 - r0), mine, parts, ctas);
+    if constexpr (greedy) {
+        if (all) all_bests<T>(a, sm, r0, static_cast<int>(r1 - r0), mine, parts, ctas);
+    }
     if (first) __syncthreads();
     else cluster_sync_all();
     for (int asked = 1; first || sm.n > 0; ++asked) {
         if (!first) {
-            if (warp == 0) walk<T>(a, sm, greedy, parts, ctas, &odd, &bad);
+            if (warp == 0) walk<T, greedy>(a, sm, parts, ctas, &odd, &bad);
             __syncthreads();
             if (sm.ask == kEnd && greedy) break;
         }
@@ -716,12 +718,14 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
         if (ask != kEnd || !sm.fresh) {
             // ---- every CTA: its slice, a warp's slice of it
             const int j0 = min(mine * sm.row.per, sm.row.pieces), j1 = min(j0 + sm.row.per, sm.row.pieces);
-            const uint64_t sum = ask == kBest ? best_of<T, 2>(sm.row, j0, j1, &bad) : slice_left<T>(sm, j0, j1, &bad);
+            uint64_t sum;
+            if constexpr (greedy) sum = best_of<T, 2>(sm.row, j0, j1, &bad);
+            else sum = slice_left<T>(sm, j0, j1, &bad);
             if (lane == 0) sm.warp_sum[warp] = sum;
             __syncthreads();
             if (warp == 0) {
                 uint64_t all = lane < kVWarps ? sm.warp_sum[lane] : 0;
-                all = ask == kBest ? warp_max64(all) : warp_sum64(all);
+                all = greedy ? warp_max64(all) : warp_sum64(all);
                 if (lane < static_cast<int>(ctas)) remote_store64(remote_addr(&sm.slot[asked & 1][rank], lane), all);
                 __syncwarp();
             }
@@ -733,10 +737,10 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
         uint64_t total = 0, before = 0;
         for (uint32_t k = 0; k < ctas; ++k) {
             const uint64_t x = slot[k];
-            total = ask == kBest ? max(total, x) : total + x;
+            total = greedy ? max(total, x) : total + x;
             if (k < rank) before += x;
         }
-        if (ask == kBest) {
+        if constexpr (greedy) {
             if (tid == 0) sm.best = token_of(total);
             first = false;
             continue;
@@ -839,7 +843,7 @@ int launch_verify(VerifyArgs a, int B, cudaStream_t s) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    ECHO_CUDA_OK(cudaLaunchKernelEx(&cfg, verify_kernel<T>, a));
+    ECHO_CUDA_OK(cudaLaunchKernelEx(&cfg, a.u_pick ? verify_kernel<T, false> : verify_kernel<T, true>, a));
     return ECHO_OK;
 }
 
