@@ -15,9 +15,9 @@
 // each, and 128 of the 256 of O in the storing: one set needs 3300 cycles a tile, more than the MMAs.
 //
 // What bounds it: the MMAs of a tile are 2176 cycles, a tile takes some 2690: copies into shared memory and the operands
-// read from it share its ports.  Tensor pipe 75% active on 16 trees of 12 to 48 nodes over 2048 to 32768 tokens, 128 heads
-// (1.18 ms a launch by itself, 1.52 PFLOP/s; 1.35 among others, under the power cap).  Tiles of 64 tokens took 1.31 ms, 58%.
-// 64 nodes over 131072 tokens: 1.41 ms by itself, 1.65 among others (tiles of 64: 1.82).
+// read from it share its ports.  Tensor pipe 76% active on 16 trees of 12 to 48 nodes over 2048 to 32768 tokens, 128 heads
+// (1.20 ms a launch by itself, 1.49 PFLOP/s; 1.38 among others, under the power cap).  Tiles of 64 tokens took 1.31 ms, 58%.
+// 64 nodes over 131072 tokens: 1.42 ms by itself, 1.66 among others (tiles of 64: 1.82).
 #include "echo_chunk.cuh"
 
 namespace echo {
