@@ -111,7 +111,8 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t sP, uint32_t sV
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    tree_kernel(ChunkArgs a, Plan plan, const __grid_constant__ CUtensorMap qmap, float scale_log2, uint16_t* __restrict__ out, float* __restrict__ lse) {
+    tree_kernel(ChunkArgs a, Plan plan, const __grid_constant__ CUtensorMap qmap, float scale_log2, uint16_t* __restrict__ out,
+                float* __restrict__ lse) {
     extern __shared__ __align__(1024) uint8_t tree_smem[];  // the swizzled tiles need 1024 bytes
     uint8_t* const gbase = tree_smem;
     const uint32_t base = smem_addr(gbase);
@@ -227,7 +228,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = !softmax_or(!ok);
                 over = !ok;
                 if (over) break;  // all eight warps together
-                const float tmx = fmaxf(fmaxf(ctl->mx[st][0][row], ctl->mx[st][1][row]), fmaxf(ctl->mx[st][2][row], ctl->mx[st][3][row])) * scale_log2;
+                const float(&all)[4][64] = ctl->mx[st];
+                const float tmx = fmaxf(fmaxf(all[0][row], all[1][row]), fmaxf(all[2][row], all[3][row])) * scale_log2;
                 const bool need = tmx > m + kLazy;  // also m = -inf with a visible token
                 const bool moves = __any_sync(0xffffffffu, need);
                 float corr = 1.f;
@@ -329,7 +331,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after();
             uint8_t* const part =
                 part_of(plan, ci, p) + (static_cast<size_t>(static_cast<int>(c) * 64 + r_cta) * kLatDv + half * 256) * 4;
-            const float* const factors = reinterpret_cast<const float*>(part_of(plan, ci, p) + kPartO) + 2 * kM + static_cast<int>(c) * 64 + r_cta;
+            const float* const factors =
+                reinterpret_cast<const float*>(part_of(plan, ci, p) + kPartO) + 2 * kM + static_cast<int>(c) * 64 + r_cta;
             float f[4], fb[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = ctl->fin[r_cta + 8 * i + (lane >> 2)];

@@ -394,7 +394,8 @@ __device__ __forceinline__ bool fork_pair(const ForkArgs& f, int page, int i, Re
     to->off = f.tok_off[d];
     to->last = f.tok_off[d + 1];
     to->end = to->off;
-    return ok && to->off >= 0 && to->last >= to->off && to->last <= f.n_tokens && rest(to->off, page) == 0 && to->last - to->off >= from->end - from->off;
+    return ok && to->off >= 0 && to->last >= to->off && to->last <= f.n_tokens && rest(to->off, page) == 0 &&
+           to->last - to->off >= from->end - from->off;
 }
 
 __global__ void __launch_bounds__(kFT) pages_share_kernel(PoolArgs a, ForkArgs f, Work w, int32_t* status) {
@@ -614,7 +615,8 @@ __global__ void __launch_bounds__(kKT)
             __syncthreads();
         }
         const int m = static_cast<int>(min(static_cast<int64_t>(kBatch), c - i0));
-        for (int64_t k = static_cast<int64_t>(blockIdx.y) * kKT + tid; k < static_cast<int64_t>(cols) * a.layers; k += static_cast<int64_t>(gridDim.y) * kKT) {
+        const int64_t columns = static_cast<int64_t>(cols) * a.layers, step = static_cast<int64_t>(gridDim.y) * kKT;
+        for (int64_t k = static_cast<int64_t>(blockIdx.y) * kKT + tid; k < columns; k += step) {
             const int64_t l = quot(k, cols);
             uint8_t* const kv = a.kv + l * a.layer_bytes + (k - l * cols) * 16;
             for (int i = 0; i < m; i += kHeld) {
@@ -741,7 +743,8 @@ extern "C" int echo_pages_compact(int64_t n_tokens, const echo_page_pool* pool, 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     pages_compact_kernel<<<1, kPlanT, 0, s>>>(a, used, w);
     ECHO_CUDA_OK(cudaGetLastError());
-    ECHO_CUDA_OK(launch_after(false, pages_place_kernel, dim3(static_cast<unsigned>((8 * sm_count() + layer_blocks(a) - 1) / layer_blocks(a)), layer_blocks(a)), kMT, 0, s, a, const_cast<const int32_t*>(used), w, status));
+    const unsigned rows = layer_blocks(a), blocks = (8u * static_cast<unsigned>(sm_count()) + rows - 1) / rows;
+    ECHO_CUDA_OK(launch_after(false, pages_place_kernel, dim3(blocks, rows), kMT, 0, s, a, const_cast<const int32_t*>(used), w, status));
     return ECHO_OK;
 }
 

@@ -394,7 +394,8 @@ __device__ __forceinline__ uint64_t sum_left(const VerifySmem& sm, int j0, int j
 #pragma unroll
         for (int i = 0; i < kTile; i += 2) {
             F2 s, t;
-            left_of<kUnit>(two(__uint_as_float(p[i]), __uint_as_float(p[i + 1])), two(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), S, &s, &t);
+            left_of<kUnit>(two(__uint_as_float(p[i]), __uint_as_float(p[i + 1])),
+                           two(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), S, &s, &t);
             const Units u = spread(s, t);
             hi += u.hi[0] + u.hi[1];
             mid += u.mid[0] + u.mid[1];
@@ -686,7 +687,8 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
         __syncwarp();
     }
     // greedy: every node's best is found, or the root's is asked for, at once, and known behind the same barrier as the tree
-    const bool all = greedy && whole && r1 > r0 && r1 - r0 <= kAllNodes && (r1 - r0) * a.vocab * static_cast<int64_t>(sizeof(T)) <= a.all_bytes;
+    const bool all = greedy && whole && r1 > r0 && r1 - r0 <= kAllNodes &&
+                     (r1 - r0) * a.vocab * static_cast<int64_t>(sizeof(T)) <= a.all_bytes;
     bool first = greedy && !all;
     if (tid == 0) {
         sm.all = all;
@@ -788,7 +790,8 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
                 mend_piece<T>(sm, r, j, p, d, &bad);
 #pragma unroll
                 for (int i = 0; i < Vec<T>::n; i += 2) {
-                    const F2 pf = two(__uint_as_float(p[i]), __uint_as_float(p[i + 1])), df = two(__uint_as_float(d[i]), __uint_as_float(d[i + 1]));
+                    const F2 pf = two(__uint_as_float(p[i]), __uint_as_float(p[i + 1]));
+                    const F2 df = two(__uint_as_float(d[i]), __uint_as_float(d[i + 1]));
                     F2 l, t;
                     if (unit) left_of<true>(pf, df, S, &l, &t);
                     else left_of<false>(pf, df, S, &l, &t);
@@ -861,7 +864,8 @@ extern "C" int echo_draft_verify(int B, const int64_t* row_off, int64_t n_rows, 
     if (n_rows > 0 && (!parent || !token || !target || !path)) return ECHO_EINVAL;
     if ((u_node != nullptr) != (u_pick != nullptr)) return ECHO_EINVAL;
     if (!is_aligned(target, 16) || !is_aligned(draft, 16)) return ECHO_EINVAL;
-    const VerifyArgs a = {row_off, n_rows, parent, token, vocab, target, u_node ? draft : nullptr, u_node, u_pick, path, count, next, status, 0};
+    const VerifyArgs a = {row_off, n_rows, parent, token, vocab, target, u_node ? draft : nullptr, u_node, u_pick,
+                          path, count, next, status, 0};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == ECHO_F32 ? launch_verify<float>(a, B, s) : launch_verify<__nv_bfloat16>(a, B, s);
 }
