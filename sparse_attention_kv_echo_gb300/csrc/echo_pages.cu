@@ -381,7 +381,7 @@ struct ForkArgs {
 };
 
 // Three launches: every pair shares pages (a block or more each, 5.8 us for 64 pairs), one block hands out the pages of the
-// last rows (4.8), a grid copies them (5.7: 64 x up to 64 rows of 4 layers).
+// last rows (4.8), a grid copies them (4.9: 64 x up to 64 rows of 4 layers).
 
 // Whether pair i may be forked; a block together.
 __device__ __forceinline__ bool fork_pair(const ForkArgs& f, int page, int i, Region* from, Region* to) {
@@ -464,8 +464,8 @@ __global__ void __launch_bounds__(kPlanT) pages_tails_kernel(PoolArgs a, ForkArg
 }
 
 // ---------------------------------------------------------------- compact
-// One block counts and pairs (6.3 us over 3077 pages), a grid moves rows and renames entries: 403 MB read and 403 written in
-// 138 us, 5.8 TB/s, 0.86 of a plain copy's rate.
+// One block counts and pairs (6.3 us over 3077 pages), a grid moves rows and renames entries: 453 MB read and written in
+// 129 us, 7.0 TB/s, a plain copy's rate (the last 50 MB are still in L2 then).
 //
 // list[k]: the k-th free place before U, far[k]: the k-th page in use from U on, which goes there; map[p]: where page p >= U
 // goes (-1: it is free).
@@ -674,7 +674,7 @@ unsigned entry_blocks(const PoolArgs& a, int B) {
 unsigned layer_blocks(const PoolArgs& a) { return static_cast<unsigned>(a.layers < 8 ? a.layers : 8); }
 
 // Blocks that carry out at most `most` moves, a piece each at a time, up to 32 an SM: many short blocks keep more bytes under way
-// than the 8 that are resident, each waiting for its loads, then storing (403 MB: 138 us with 8 an SM, 125 with 32; 123 with 64, but
+// than the 8 that are resident, each waiting for its loads, then storing (453 MB: 138 us with 8 an SM, 129 with 32; 127 with 64, but
 // 3 us more where there is little to move).
 unsigned move_blocks(const PoolArgs& a, int64_t most) {
     const int64_t rows = layer_blocks(a), cap = (32 * static_cast<int64_t>(sm_count()) + rows - 1) / rows;
