@@ -597,16 +597,6 @@ def pages_workspace_size(B: int, n_pages: int) -> int:
     return int(load().echo_pages_workspace_size(int(B), int(n_pages)))
 
 
-def _check_pool(call, tok_off, n_tokens, pool, status, per_request, *more):
-    # per_request: tensors with an int64 for each request
-    B = tok_off.shape[0] - 1
-    dev = _device()
-    _expect(call, dev, ("tok_off", tok_off, torch.int64, (B + 1,)), ("status", status, torch.int32, (1,)),
-            *[(name, t, torch.int64, (B,)) for name, t in per_request], *more)
-    _check_table(call, n_tokens, pool, dev)
-    return B
-
-
 def _check_table(call, n_tokens, pool, dev):
     if pool.tokens < n_tokens or pool.device != dev:
         raise ValueError(f"{call}: the page table covers {pool.tokens} token rows, not {n_tokens}, or lies on another device")
@@ -616,10 +606,12 @@ def pages_reserve(tok_off, tok_end, want, n_tokens, pool, room, ws, status, stre
     """echo_pages_reserve: pages for the tokens [tok_end[b], want[b]) of every request (want [B] int64, token rows),
     the lowest free ones; a page others hold too is replaced.  room [B] int64 (or None): want[b] where served, else
     tok_end[b].  ws: uint8, pages_workspace_size(B, n_pages)."""
-    per = [("tok_end", tok_end), ("want", want)]
-    if room is not None:
-        per.append(("room", room))
-    B = _check_pool("pages_reserve", tok_off, n_tokens, pool, status, per, ("ws", ws, torch.uint8, (ws.numel(),)))
+    B, dev, i64 = tok_off.shape[0] - 1, _device(), torch.int64
+    per = (B,)
+    _expect("pages_reserve", dev, ("tok_off", tok_off, i64, (B + 1,)), ("status", status, torch.int32, (1,)),
+            ("tok_end", tok_end, i64, per), ("want", want, i64, per), ("ws", ws, torch.uint8, (ws.numel(),)),
+            *(() if room is None else (("room", room, i64, per),)))
+    _check_table("pages_reserve", n_tokens, pool, dev)
     _check("echo_pages_reserve", load().echo_pages_reserve(
         B, tok_off.data_ptr(), tok_end.data_ptr(), want.data_ptr(), int(n_tokens), pool.struct, _ptr(room), ws.data_ptr(),
         ws.numel(), status.data_ptr(), _stream(stream)))
@@ -627,7 +619,10 @@ def pages_reserve(tok_off, tok_end, want, n_tokens, pool, room, ws, status, stre
 
 def pages_free(tok_off, tok_end, n_tokens, pool, status, stream=None):
     """echo_pages_free: gives up the pages behind every request's end (tok_end[b] = tok_off[b]: all of them)."""
-    B = _check_pool("pages_free", tok_off, n_tokens, pool, status, [("tok_end", tok_end)])
+    B, dev = tok_off.shape[0] - 1, _device()
+    _expect("pages_free", dev, ("tok_off", tok_off, torch.int64, (B + 1,)), ("status", status, torch.int32, (1,)),
+            ("tok_end", tok_end, torch.int64, (B,)))
+    _check_table("pages_free", n_tokens, pool, dev)
     _check("echo_pages_free", load().echo_pages_free(B, tok_off.data_ptr(), tok_end.data_ptr(), int(n_tokens), pool.struct,
                                                      status.data_ptr(), _stream(stream)))
 
@@ -636,9 +631,11 @@ def pages_fork(src, dst, tok_off, tok_end, n_tokens, pool, ws, status, stream=No
     """echo_pages_fork: request dst[i] gives up its pages and gets the context of request src[i] (src, dst [m] int32):
     full pages shared, the rows of a partly used last page copied, tok_end[dst[i]] set.  ws: uint8,
     pages_workspace_size(m, n_pages)."""
-    m = src.numel()
-    B = _check_pool("pages_fork", tok_off, n_tokens, pool, status, [("tok_end", tok_end)], ("src", src, torch.int32, (m,)),
-                    ("dst", dst, torch.int32, (m,)), ("ws", ws, torch.uint8, (ws.numel(),)))
+    m, B, dev = src.numel(), tok_off.shape[0] - 1, _device()
+    _expect("pages_fork", dev, ("tok_off", tok_off, torch.int64, (B + 1,)), ("status", status, torch.int32, (1,)),
+            ("tok_end", tok_end, torch.int64, (B,)), ("src", src, torch.int32, (m,)), ("dst", dst, torch.int32, (m,)),
+            ("ws", ws, torch.uint8, (ws.numel(),)))
+    _check_table("pages_fork", n_tokens, pool, dev)
     _check("echo_pages_fork", load().echo_pages_fork(
         m, src.data_ptr(), dst.data_ptr(), B, tok_off.data_ptr(), tok_end.data_ptr(), int(n_tokens), pool.struct,
         ws.data_ptr(), ws.numel(), status.data_ptr(), _stream(stream)))
@@ -659,10 +656,11 @@ def rows_keep(row_off, path, count, tok_off, tok_end, n_tokens, pool, new_end, s
     """echo_rows_keep: the cache rows of the accepted nodes of each request's draft tree (path, count of
     draft_verify) move together behind the context, in every layer; new_end [B] int64: where the contexts then end
     (not tok_end itself).  pages_free(new_end) gives up the pages behind."""
-    B, n = tok_off.shape[0] - 1, path.numel()
-    _check_pool("rows_keep", tok_off, n_tokens, pool, status, [("tok_end", tok_end), ("new_end", new_end)],
-                ("row_off", row_off, torch.int64, (B + 1,)), ("path", path, torch.int32, (n,)),
-                ("count", count, torch.int32, (B,)))
+    B, n, dev, i64, i32 = tok_off.shape[0] - 1, path.numel(), _device(), torch.int64, torch.int32
+    ends, per = (B + 1,), (B,)
+    _expect("rows_keep", dev, ("tok_off", tok_off, i64, ends), ("status", status, i32, (1,)), ("tok_end", tok_end, i64, per),
+            ("new_end", new_end, i64, per), ("row_off", row_off, i64, ends), ("path", path, i32, (n,)), ("count", count, i32, per))
+    _check_table("rows_keep", n_tokens, pool, dev)
     _check("echo_rows_keep", load().echo_rows_keep(
         B, row_off.data_ptr(), n, path.data_ptr(), count.data_ptr(), tok_off.data_ptr(), tok_end.data_ptr(), int(n_tokens),
         pool.struct, new_end.data_ptr(), status.data_ptr(), _stream(stream)))
