@@ -74,6 +74,72 @@ struct Ctl {
 constexpr uint32_t kSmem = kQBytes + kKBytes + 2 * kVBytes + 2 * kPBytes + ((sizeof(Ctl) + 15u) & ~15u);
 static_assert(kSmem <= 227u * 1024u, "tree shared memory");
 
+// The walk of a share, with the order in which a piece's tiles are taken: at unit u of its share a cluster is at tile
+// u mod (the group's tiles) as far as the piece has it, so that the groups of a request, which read the same tokens, read them at the same
+// time whatever their shares begin with.
+struct TreeWalk : Walk<kTok> {
+    int64_t start;
+    int from, len, turn;  // of the piece: its first tile, how many, and which of them is taken first
+    __device__ __forceinline__ bool step(Piece* p) {
+        const int64_t before = u0;
+        if (!next(p)) return false;
+        if (!p->later && p->hi > p->lo) {
+            from = p->lo;
+            len = (p->last ? p->hi : static_cast<int>(min(u1 - cum[g], static_cast<int64_t>(kOver<kTok> + p->tiles)) - kOver<kTok>)) - from;
+            const int now = static_cast<int>(static_cast<uint32_t>(before - start) % static_cast<uint32_t>(p->tiles));
+            const int ahead = now >= from ? now - from : now - from + p->tiles;  // tiles from the first to the one that is due
+            turn = ahead < len ? ahead : p->tiles - ahead < len ? len - (p->tiles - ahead) : 0;
+        }
+        return true;
+    }
+    __device__ __forceinline__ int first(const Piece& p) const {  // tile of a leg's first
+        const int x = p.lo - from + turn;
+        return from + (x >= len ? x - len : x);
+    }
+    __device__ __forceinline__ int behind(int x) const { return x + 1 == from + len ? from : x + 1; }
+};
+
+// One token of every tile of a piece, or of each of its kParts parts, looked up ahead of its copy: the table entry of the
+// next is in flight while this one's row is copied.
+template <int kParts>
+struct Tokens {
+    PageView pv;
+    int tile, r, part, left;  // of the token whose entry is in flight; tokens of the piece from there on
+    int32_t entry;            // < 0: none
+    uint32_t at;              // offset in that page
+    bool bad;
+    __device__ __forceinline__ void look(const ChunkArgs& a, const Piece& p) {
+        const int64_t t = static_cast<int64_t>(tile) * kTok + part * (kTok / kParts) + r;
+        entry = -1;
+        if (left > 0 && t < p.g.nv) entry = pv.tab[page_of(a, pv, static_cast<uint32_t>(t), &at)];
+    }
+    __device__ __forceinline__ void start(const ChunkArgs& a, const Piece& p, const TreeWalk& walk, int row) {
+        pv = page_view(a, p.g.req, p.g.off);
+        tile = walk.first(p);
+        r = row;
+        part = 0;
+        left = (p.hi - p.lo) * kParts;
+        bad = false;
+        at = 0;
+        look(a, p);
+    }
+    // The cache row of the token, -1 when it has none.
+    __device__ __forceinline__ int64_t row(const ChunkArgs& a) {
+        const int64_t x = entry < 0 ? -1 : page_row(a, pv, entry, at, &bad);
+        if (bad) set_status(a.status, ECHO_ST_BADDATA);
+        bad = false;
+        return x;
+    }
+    __device__ __forceinline__ void next(const ChunkArgs& a, const Piece& p, const TreeWalk& walk) {
+        --left;
+        if (++part == kParts) {
+            part = 0;
+            tile = walk.behind(tile);
+        }
+        look(a, p);
+    }
+};
+
 // Barrier over the softmax warps; true when any thread votes so.
 __device__ __forceinline__ bool softmax_or(bool v) {
     uint32_t r;
@@ -156,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_alloc2(smem_addr(&ctl->tmem), kTmemCols);
     pdl_wait();
     const PlanHead head = *plan.head;
-    Walk<kTok> walk;
+    TreeWalk walk;
     walk.group = plan.group;
     walk.cum = plan.cum;
     walk.u0 = walk.u1 = 0;
@@ -174,6 +240,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync_all();
     tc_fence_after();
     if (walk.u0 < walk.u1) walk.g = ctl->first;
+    walk.start = walk.u0;
+    walk.from = walk.len = walk.turn = 0;
     const uint32_t tmem = ctl->tmem;
     Piece p;
     uint32_t t = 0;  // tiles so far: the phase of a barrier passed once a tile is t & 1
@@ -185,14 +253,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int rig = mi / a.heads;  // row within the group
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
         bool ok = true, over = false;
-        while (walk.next(&p)) {  // a warp whose wait ran out goes on to the next vote, where all eight leave
+        while (walk.step(&p)) {  // a warp whose wait ran out goes on to the next vote, where all eight leave
             const bool lives = rig < p.g.rows;
             const int vhi = lives && p.g.nv > 0 ? p.g.pos0 + rig + 1 : 0;  // this row's tokens: v < vhi that its mask lets it see
             const uint32_t* const nodes = lives ? a.mask + static_cast<int64_t>(p.g.row0 + rig) * a.words : nullptr;
             float m = -INFINITY, l = 0.f;
-            for (int it = p.lo; it < p.hi; ++it, ++t) {
+            int tile = walk.first(p);
+            for (int it = p.lo; it < p.hi; ++it, ++t, tile = walk.behind(tile)) {
                 const uint32_t st = t & 1u, buf = t & (kSBufs - 1);
-                const int v0 = it * kTok + half * kSub + 32 * set;
+                const int v0 = tile * kTok + half * kSub + 32 * set;
                 // the mask's bits of tokens v0 .. v0 + 31, those before the tree set; asked for before the wait, and by
                 // the last tiles alone
                 uint32_t there = 0xFFFFFFFFu;
@@ -353,15 +422,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // instruction.  Lanes 0-15 look up the warp's tokens, lanes 16-31 those of the other CTA, for the valid flags.
         const int w = warp - 4, x = lane & 7, r4 = lane >> 3;
         bool ok = true;
-        while (ok && walk.next(&p)) {
+        while (ok && walk.step(&p)) {
             if (p.hi == p.lo) continue;
-            Gather<kTok> own;
-            own.start(a, p, static_cast<int>(lane < 16 ? c : c ^ 1u) * kSub + 16 * w + (lane & 15));
+            Tokens<1> own;
+            own.start(a, p, walk, static_cast<int>(lane < 16 ? c : c ^ 1u) * kSub + 16 * w + (lane & 15));
             for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
                 const uint32_t ph = t & 1u;
                 const int64_t row = own.row(a);
                 const uint32_t bits = __ballot_sync(0xffffffffu, row >= 0);  // 16 of this CTA's tokens, 16 of the other's
-                own.next(a, p);
+                own.next(a, p, walk);
                 const uint8_t* src[4];
                 uint32_t n[4], dst[4];
 #pragma unroll
@@ -401,14 +470,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- V: this CTA's 256 dims of a half's 64 tokens, 16 to a warp, copied like K
         const int w = warp - 8, x = lane & 7, r4 = lane >> 3;
         bool ok = true;
-        while (ok && walk.next(&p)) {
+        while (ok && walk.step(&p)) {
             if (p.hi == p.lo) continue;
-            Gather<kSub> own;
-            own.start(a, p, 16 * w + (lane & 15), 0, kTok / kSub);
+            Tokens<kTok / kSub> own;
+            own.start(a, p, walk, 16 * w + (lane & 15));
             for (int it = p.lo; ok && it < p.hi; ++it, ++t) {
                 for (uint32_t h = 0; h < 2; ++h) {
                     const int64_t row = own.row(a);
-                    own.next(a, p);
+                    own.next(a, p, walk);
                     const uint8_t* src[4];
                     uint32_t n[4], dst[4];
 #pragma unroll
