@@ -15,9 +15,9 @@
 // each, and 128 of the 256 of O in the storing: one set needs 3300 cycles a tile, more than the MMAs.
 //
 // What bounds it: the MMAs of a tile are 2176 cycles, a tile takes some 2690: copies into shared memory and the operands
-// read from it share its ports.  Tensor pipe 76% active on 16 trees of 12 to 48 nodes over 2048 to 32768 tokens, 128 heads
-// (1.20 ms a launch by itself, 1.49 PFLOP/s; 1.38 among others, under the power cap).  Tiles of 64 tokens took 1.31 ms, 58%.
-// 64 nodes over 131072 tokens: 1.42 ms by itself, 1.66 among others (tiles of 64: 1.82).
+// read from it share its ports.  Tensor pipe 79% active on 16 trees of 12 to 48 nodes over 2048 to 32768 tokens, 128 heads
+// (1.12 ms a launch by itself, 1.60 PFLOP/s; 1.25 among others, under the power cap).  Tiles of 64 tokens took 1.31 ms, 58%.
+// 64 nodes over 131072 tokens: 1.32 ms by itself, 1.52 among others (tiles of 64: 1.82).
 #include "echo_chunk.cuh"
 
 namespace echo {
@@ -39,10 +39,10 @@ constexpr uint32_t kPBytes = 64 * 128;
 constexpr uint32_t kTmemCols = 512;      // O [0, 256) | S buffers of 64 columns
 constexpr int kSBufs = 4;
 constexpr uint32_t kSCol = 256;
-// Tokens that one or two groups read come from memory, and K has one stage: the next tile's rows are brought to L2 once this
-// tile's copies are under way (32 trees of eight behind 8000 tokens, 16 heads, 86.8 -> 80.6 us; looked up and fetched one to five
-// tiles further ahead, 90 to 104).  Tokens that many groups read are in L2 already (fetched ahead, 16 trees of 128 heads took
-// 1.58 ms for 1.32).
+// Tokens that up to four groups read come from memory for many of them, and K has one stage: the next tile's rows are brought to
+// L2 once this tile's copies are under way (32 trees of eight behind 8000 tokens, 16 heads, one group each, 86.8 -> 80.6 us, 16 trees
+// of 16 behind 16000, two groups, 131.6 -> 125.2; looked up and fetched one to five tiles further ahead, the former took 90 to
+// 104).  Tokens that many groups read are in L2 mostly (fetched ahead, 64 nodes over 131072 took 1.60 ms for 1.51).
 constexpr float kLazy = 8.f;
 constexpr int kMinUnits = 2;             // least units per cluster (1, 3 and 4: slower small calls)
 constexpr uint32_t kIdescS = idesc_bf16_f32(kM, kTok);
@@ -76,7 +76,8 @@ static_assert(kSmem <= 227u * 1024u, "tree shared memory");
 
 // The walk of a share, with the order in which a piece's tiles are taken: at unit u of its share a cluster is at tile
 // u mod (the group's tiles) as far as the piece has it, so that the groups of a request, which read the same tokens, read them at the same
-// time whatever their shares begin with.
+// time whatever their shares begin with (16 trees of 12 to 48 groups: 3.4 GB from memory in ascending order, 1.5 so, 1344 -> 1251 us;
+// 64 groups over 131072 tokens 1690 -> 1524).
 struct TreeWalk : Walk<kTok> {
     int64_t start;
     int from, len, turn;  // of the piece: its first tile, how many, and which of them is taken first
@@ -642,7 +643,7 @@ extern "C" int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int 
     plan.clusters = cluster2_count(tree_kernel, kThreads, kSmem, kMaxClusters, cached);
     if (plan.clusters < 1) return ECHO_ECUDA;
     plan.least = kMinUnits;
-    plan.ahead = cap <= 2 * B;
+    plan.ahead = cap <= 5 * B;  // four groups a request
     plan.small = false;
     // The plan is scheduled beside the kernel before it (the masks' lets it be) and waits for that to end.  One warp plans
     // a call of at most 32 requests and groups: one tree of eight nodes, 128 heads, 20.7 us against 22.0 with a block of 1024.
