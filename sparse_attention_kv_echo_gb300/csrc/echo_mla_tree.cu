@@ -14,7 +14,7 @@
 // 64 columns, so the threads of half h write P of half h, whole rows.  Softmax takes two sets of four warps, 32 columns
 // each, and 128 of the 256 of O in the storing: one set needs 3300 cycles a tile, more than the MMAs.
 //
-// What bounds it: the MMAs of a tile are 2176 cycles, a tile takes some 2690: copies into shared memory and the operands
+// What bounds it: the MMAs of a tile are 2176 cycles, a tile takes some 2740: copies into shared memory and the operands
 // read from it share its ports.  Tensor pipe 79% active on 16 trees of 12 to 48 nodes over 2048 to 32768 tokens, 128 heads
 // (1.12 ms a launch by itself, 1.60 PFLOP/s; 1.25 among others, under the power cap).  Tiles of 64 tokens took 1.31 ms, 58%.
 // 64 nodes over 131072 tokens: 1.32 ms by itself, 1.52 among others (tiles of 64: 1.82).
