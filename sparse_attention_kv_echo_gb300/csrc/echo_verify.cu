@@ -523,13 +523,13 @@ __device__ __forceinline__ float unit_interval(float u, bool* bad) {
     return fminf(fmaxf(u, 0.f), 0.99999994f);  // NaN: 0
 }
 
-// u in units of 2^-32.
-__device__ __forceinline__ uint32_t fraction(float u) { return static_cast<uint32_t>(__float2uint_rz(u * 4294967296.f)); }
+// u in units of 2^-64: exact from 2^-40 on.  (Units of 2^-32 would cut bits off every u below 2^-8.)
+__device__ __forceinline__ uint64_t fraction(float u) { return __float2ull_rz(u * 18446744073709551616.f); }
 
 // u d R < left, all in units (R below 2^63).
 __device__ __forceinline__ bool accepts(float u, uint64_t d, uint64_t R, uint64_t left) {
     const uint64_t y = __umul64hi(d << 2, R << 1);  // d R in units of 2^-59
-    return __umul64hi(y, static_cast<uint64_t>(fraction(u)) << 32) << 1 < left;
+    return __umul64hi(y, fraction(u)) << 1 < left;
 }
 
 // A turn of the walk, by a warp: on from the last child tried to the next question.
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kVT, 2) verify_kernel(VerifyArgs a) {
             odd = true;
             break;
         }
-        uint64_t at = __umul64hi(total, static_cast<uint64_t>(fraction(sm.u_pick)) << 32);
+        uint64_t at = __umul64hi(total, fraction(sm.u_pick));
         if (at < before || at - before >= slot[rank]) break;
         at -= before;
         const int in = warp_find(lane < kVWarps ? sm.warp_sum[lane] : 0, &at);
