@@ -698,9 +698,13 @@ int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, cons
  *   count [B] int32: how many (>= 1 with rows, else 0);
  *   next [B] int32: the token behind the path (-1 without rows);
  *   dtype ECHO_F32 or ECHO_BF16, of target and draft both (16-byte aligned).
- * What is left of a token is summed as a whole number, good to 2^-48, so equal inputs give
- * equal results in any batch and on any launch, and a test falls on the right side of its
- * border unless it is within some 2^-40 of it.
+ * What is left of a token is summed as a whole number, good to 2^-45, so equal inputs give
+ * equal results in any batch and on any launch.  A first child's test falls on the right side
+ * of its border unless it is within 2^-57 of it; what hangs on sums, a test behind k rejections
+ * at a node or the draw, unless within (k + 1) * vocab * 2^-45 of it (with draft rows that sum
+ * to 1, where an error of S does not grow: it makes the next R err the other way).  Uniform
+ * numbers below 2^-40 are cut off to multiples of 2^-64.  Rows are taken as they are, R = 1
+ * at first: where a row sums to 1 + e, as rows of bf16 do, the distribution is off by some e.
  * Probabilities are to be in [0, 1] with a sum below 8 (of a row with a larger sum any token
  * may come): NaN and values outside [0, 2] count as 0 and 2 and set ECHO_ST_NAN where they
  * are read; a row that is 0 throughout gives token 0 and ECHO_ST_BADDATA; uniform numbers

@@ -180,9 +180,9 @@ __device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, both(-1.f), a); } 
 // What is left of two tokens, max(0, p - S d), is s + t, with t below the last place of p or of S d.  kUnit: S is 1, or d is 0.
 template <bool kUnit>
 __device__ __forceinline__ void left_of(F2 p, F2 d, const Scale& S, F2* s, F2* t) {
-    float p0, p1, d0, d1;
-    apart(p, &p0, &p1);
     if (kUnit) {
+        float p0, p1, d0, d1;
+        apart(p, &p0, &p1);
         apart(d, &d0, &d1);
         const F2 x = two(fminf(d0, p0), fminf(d1, p1));  // p >= x: what the difference loses is exact
         *s = sub(p, x);
@@ -190,22 +190,21 @@ __device__ __forceinline__ void left_of(F2 p, F2 d, const Scale& S, F2* s, F2* t
     } else {
         const F2 x = mul(both(S.hi), d), w = fma(both(S.lo), d, fma(both(S.hi), d, fma(x, both(-1.f), both(0.f))));
         const F2 a = sub(p, x), b = sub(sub(sub(p, a), x), w), sum = add(a, b);
-        float x0, x1, a0, a1, b0, b1, s0, s1;
-        apart(x, &x0, &x1);
+        float a0, a1, b0, b1, s0, s1;
         apart(a, &a0, &a1);
         apart(b, &b0, &b1);
         apart(sum, &s0, &s1);
-        const bool some0 = p0 >= x0 && s0 > 0.f, some1 = p1 >= x1 && s1 > 0.f;
-        *s = two(some0 ? a0 : 0.f, some1 ? a1 : 0.f);
-        *t = two(some0 ? b0 : 0.f, some1 ? b1 : 0.f);
+        // p may lie below x, by an ulp, and above S d all the same: a < 0 then, and the rest is what the sum says
+        *s = two(s0 > 0.f ? (a0 < 0.f ? s0 : a0) : 0.f, s1 > 0.f ? (a1 < 0.f ? s1 : a1) : 0.f);
+        *t = two(s0 > 0.f && a0 >= 0.f ? b0 : 0.f, s1 > 0.f && a1 >= 0.f ? b1 : 0.f);
     }
 }
 
 // s + t in units of 2^-60, spread over three 32-bit numbers whose sums are exact: a constant added to a float rounds it to
 // units that the low bits then count, and the remainder, scaled up, goes the same way again.  That runs two values at a time on
 // the pipe of FFMA and FADD.  (Conversions to 64-bit integers run at a fraction of that: 64 chains of six over 131072 tokens
-// took 96 us with them, 29 with shifts of the mantissas, on the integers' pipe.)  What a value loses is below 2^-48, the same
-// wherever it is summed.
+// took 96 us with them, 29 with shifts of the mantissas, on the integers' pipe.)  The same value loses the same
+// wherever it is summed, and for a p of at most 1 below 2^-45: 2^-49 S's two floats, 2^-48 each w and b, 2^-47 r.
 constexpr uint32_t kTopBits = 0x40000000u, kLowBits = 0x40400000u;  // of 2 and 3
 struct Units {
     uint32_t hi[2], mid[2], lo[2];  // of 2^-22, 2^-44 and 2^-60, + kTopBits, kLowBits, kLowBits
