@@ -462,6 +462,8 @@ def mla_chunk_workspace_size(n_rows: int, heads: int, B: int) -> int:
 
 
 def _check_chunk(call, row_off, q, tok_off, n_tokens, pages, lse, status, tok_end, *more):
+    if q.dim() != 3:
+        raise ValueError(f"{call}: q must be a tensor of shape [rows, heads, {MLA_DQK}], not {tuple(q.shape)}")
     (n, heads, _), B, dev = q.shape, tok_off.shape[0] - 1, _device()
     _expect(call, dev, ("row_off", row_off, torch.int64, (B + 1,)), ("tok_off", tok_off, torch.int64, (B + 1,)),
             ("q", q, torch.bfloat16, (n, heads, MLA_DQK)), ("lse", lse, torch.float32, (n, heads)),
@@ -480,7 +482,7 @@ def mla_chunk(row_off, q, tok_off, n_tokens, pages, scale, out, lse, ws, status,
     the end of its context) over the cache `pages` (a KVPages): causal; window > 0: the last
     `window` tokens and the first `sinks`; sel [n,k] int32: the tokens listed for each row -> out
     [n,heads,512] bf16, lse [n,heads] f32.  ws: uint8, mla_chunk_workspace_size(n, heads, B)."""
-    k, more = 0, [("out", out, torch.bfloat16, (q.shape[0], q.shape[1], MLA_DV)),
+    k, more = 0, [("out", out, torch.bfloat16, (*q.shape[:2], MLA_DV)),
                   ("ws", ws, torch.uint8, (ws.numel(),))]
     if sel is not None:
         k = sel.shape[-1]
@@ -537,7 +539,7 @@ def mla_tree(row_off, q, mask, tok_off, n_tokens, pages, scale, out, lse, ws, st
     (tree_masks).  ws as mla_chunk's."""
     words = mask.shape[-1]
     B, n, heads = _check_chunk("mla_tree", row_off, q, tok_off, n_tokens, pages, lse, status, tok_end,
-                               ("out", out, torch.bfloat16, (q.shape[0], q.shape[1], MLA_DV)),
+                               ("out", out, torch.bfloat16, (*q.shape[:2], MLA_DV)),
                                ("mask", mask, torch.int32, (q.shape[0], words)), ("ws", ws, torch.uint8, (ws.numel(),)))
     _check("echo_mla_tree", load().echo_mla_tree(
         B, row_off.data_ptr(), n, heads, q.data_ptr(), mask.data_ptr(), words, tok_off.data_ptr(), _ptr(tok_end),
@@ -552,6 +554,8 @@ def draft_verify(row_off, parent, token, target, path, count, next_tok, status, 
     of the same type: those its children were drawn from (None: drafts without probabilities); u_node [n] and u_pick [B]
     f32: uniform numbers in [0, 1) (both None: greedy, target may hold logits) -> path [n] int32 (accepted nodes from
     row_off[b] on, -1 behind), count [B] int32, next_tok [B] int32."""
+    if target.dim() != 2:
+        raise ValueError(f"draft_verify: target must be a tensor of shape [rows, vocab], not {tuple(target.shape)}")
     B, (n, vocab), dtype = row_off.shape[0] - 1, target.shape, target.dtype
     if dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"draft_verify: target must be float32 or bfloat16, not {dtype}")
