@@ -177,7 +177,7 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
 }
 __device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, both(-1.f), a); }  // (exact product: rounded once)
 
-// What is left of two tokens, max(0, p - S d), is s + t, with t below the last place of p or of S d.  kUnit: S is 1, or d is 0.
+// What is left of two tokens, max(0, p - S d), is s + t, with t below 2^-23 of s.  kUnit: S is 1, or d is 0.
 template <bool kUnit>
 __device__ __forceinline__ void left_of(F2 p, F2 d, const Scale& S, F2* s, F2* t) {
     if (kUnit) {
@@ -190,13 +190,15 @@ __device__ __forceinline__ void left_of(F2 p, F2 d, const Scale& S, F2* s, F2* t
     } else {
         const F2 x = mul(both(S.hi), d), w = fma(both(S.lo), d, fma(both(S.hi), d, fma(x, both(-1.f), both(0.f))));
         const F2 a = sub(p, x), b = sub(sub(sub(p, a), x), w), sum = add(a, b);
-        float a0, a1, b0, b1, s0, s1;
-        apart(a, &a0, &a1);
-        apart(b, &b0, &b1);
+        float s0, s1, t0, t1, u0, u1;
         apart(sum, &s0, &s1);
-        // p may lie below x, by an ulp, and above S d all the same: a < 0 then, and the rest is what the sum says
-        *s = two(s0 > 0.f ? (a0 < 0.f ? s0 : a0) : 0.f, s1 > 0.f ? (a1 < 0.f ? s1 : a1) : 0.f);
-        *t = two(s0 > 0.f && a0 >= 0.f ? b0 : 0.f, s1 > 0.f && a1 >= 0.f ? b1 : 0.f);
+        // (p may lie an ulp below x and above S d all the same: the sum alone tells)
+        *s = two(fmaxf(s0, 0.f), fmaxf(s1, 0.f));
+        // What the sum lost, below 2^-23 of it; where nothing is left, s and that bound are 0 and a + b is not above them.  (A
+        // choice by the sum's sign is more instructions: 34.5 us for 34.2, 32 trees of bf16.)
+        apart(add(sub(a, *s), b), &t0, &t1);
+        apart(mul(*s, both(-1.1920929e-7f)), &u0, &u1);
+        *t = two(fmaxf(t0, u0), fmaxf(t1, u1));
     }
 }
 
