@@ -59,7 +59,7 @@ struct Plan {
     int clusters;
     bool small;     // at most kInline groups and requests: no plan kernel
     int least;      // units per cluster
-    int ahead;      // tiles that K rows are brought to L2 ahead of their copy, 0: not
+    int ahead;      // tiles that K rows are brought to L2 ahead of their copy, 0: not (a tree's: not 0, the next tile's)
 };
 
 __host__ __device__ __forceinline__ int rows_per_group(int heads, bool sel) { return sel ? 1 : kM / heads; }

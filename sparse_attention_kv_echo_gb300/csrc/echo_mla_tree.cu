@@ -39,10 +39,12 @@ constexpr uint32_t kPBytes = 64 * 128;
 constexpr uint32_t kTmemCols = 512;      // O [0, 256) | S buffers of 64 columns
 constexpr int kSBufs = 4;
 constexpr uint32_t kSCol = 256;
-// Tokens that up to four groups read come from memory for many of them, and K has one stage: the next tile's rows are brought to
-// L2 once this tile's copies are under way (32 trees of eight behind 8000 tokens, 16 heads, one group each, 86.8 -> 80.6 us, 16 trees
-// of 16 behind 16000, two groups, 131.6 -> 125.2; looked up and fetched one to five tiles further ahead, the former took 90 to
-// 104).  Tokens that many groups read are in L2 mostly (fetched ahead, 64 nodes over 131072 took 1.60 ms for 1.51).
+// Tokens that few groups read come from memory for many of them, and K has one stage: where a request has up to four groups'
+// rows on average, the next tile's rows are brought to L2 once this tile's copies are under way.  Without / with, in us, 32
+// requests behind 8000 tokens, pages of 64: 128 heads, one group each 86 / 78, two 133 / 128, four 228 / 230, five 273 / 276; 16
+// heads 87 / 83, 134 / 128, four 228 / 220, five 274 / 273, six 322 / 330.  (16 trees of 12 to 48 groups have it off, as
+// has one tree of 64: fetched ahead, that took 1.60 ms for 1.51.  Rows looked up and fetched one to five tiles further ahead took
+// 90 to 104 us for 81, one group.)
 constexpr float kLazy = 8.f;
 constexpr int kMinUnits = 2;             // least units per cluster (1, 3 and 4: slower small calls)
 constexpr uint32_t kIdescS = idesc_bf16_f32(kM, kTok);
@@ -643,7 +645,7 @@ extern "C" int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int 
     plan.clusters = cluster2_count(tree_kernel, kThreads, kSmem, kMaxClusters, cached);
     if (plan.clusters < 1) return ECHO_ECUDA;
     plan.least = kMinUnits;
-    plan.ahead = cap <= 5 * B;  // four groups a request
+    plan.ahead = n_rows <= 4ll * rows_per_group(heads, false) * B;
     plan.small = false;
     // The plan is scheduled beside the kernel before it (the masks' lets it be) and waits for that to end.  One warp plans
     // a call of at most 32 requests and groups: one tree of eight nodes, 128 heads, 20.7 us against 22.0 with a block of 1024.
