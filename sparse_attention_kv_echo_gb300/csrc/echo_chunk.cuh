@@ -304,8 +304,8 @@ __device__ __forceinline__ Cut cut_of(const Walk<kTok>& walk, const PlanHead& he
 
 // One token of every tile of a piece, looked up ahead of its copy: the list entry
 // (selections) of two tiles ahead and the table entry of the next tile are in flight
-// while this tile's rows are copied.  kStep: tokens of a tile, kTok or a part of it.
-template <int kStep>
+// while this tile's rows are copied.
+template <int kTok>
 struct Gather {
     const int32_t* sel;  // the row's list, null: causal or window
     PageView pv;
@@ -329,18 +329,18 @@ struct Gather {
         }
         if (t >= 0) entry = pv.tab[page_of(a, pv, static_cast<uint32_t>(t), &at)];
     }
-    // r: token within the tile; ahead: tiles to start past the piece's first; scale: kTok / kStep.
-    __device__ __forceinline__ void start(const ChunkArgs& a, const Piece& p, int r, int ahead = 0, int scale = 1) {
+    // r: token within the tile; ahead: tiles to start past the piece's first.
+    __device__ __forceinline__ void start(const ChunkArgs& a, const Piece& p, int r, int ahead = 0) {
         sel = a.sel ? a.sel + static_cast<int64_t>(p.g.row0) * a.k : nullptr;
         pv = page_view(a, p.g.req, p.g.off);
         lo_tok = p.g.pos0 + p.g.rows + p.g.kept - p.g.nv;
         bad = false;
         at = 0;
-        const int64_t first = static_cast<int64_t>(p.lo * scale + ahead) * kStep + r, end = static_cast<int64_t>(p.hi) * scale * kStep;
+        const int64_t first = static_cast<int64_t>(p.lo + ahead) * kTok + r, end = static_cast<int64_t>(p.hi) * kTok;
         last = static_cast<int>(end);
         v = static_cast<int>(min(first, end));  // at the end: nothing to look up any more
         const int t0 = v < end ? token(p, v) : -1;
-        tok = v < end - kStep ? token(p, v + kStep) : -1;
+        tok = v < end - kTok ? token(p, v + kTok) : -1;
         look(a, p, t0);
     }
     // The cache row of the current tile's token, -1 when it has none.
@@ -352,8 +352,8 @@ struct Gather {
     }
     __device__ __forceinline__ void next(const ChunkArgs& a, const Piece& p) {
         const int t = tok;
-        v = min(v + kStep, last);
-        tok = v < last - kStep ? token(p, v + kStep) : -1;
+        v = min(v + kTok, last);
+        tok = v < last - kTok ? token(p, v + kTok) : -1;
         look(a, p, t);
     }
 };
