@@ -249,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < w; ++j) mx[j] = fmaxf(mx[j], mx[j + w]);
                 ctl->mx[st][half][row] = mx[0];
-                ok = !softmax_sync_or(!ok);
+                ok = !softmax_or<kSoftmax>(!ok);
                 over = !ok;
                 if (over) break;  // all four warps together
                 const float tmx = fmaxf(mx[0], ctl->mx[st][half ^ 1][row]) * scale_log2;
@@ -305,7 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ctl->mx[t & 1u][half][row] = l;
                 if (pieces >= 1) ok = ok && mbar_wait(smem_addr(&ctl->fin_free), (pieces - 1) & 1u, abort);
                 ++pieces;
-                ok = !softmax_sync_or(!ok);
+                ok = !softmax_or<kSoftmax>(!ok);
                 if (!ok) break;
                 L = l + ctl->mx[t & 1u][half ^ 1][row];
             }
@@ -334,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (p.hi > p.lo) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ctl->fin_ready));
-                (void)softmax_sync_or(false);  // mx is read before the next tile's maxima
+                (void)softmax_or<kSoftmax>(false);  // mx is read before the next tile's maxima
             }
         }
         if (!ok) give_up(watch);

@@ -439,16 +439,17 @@ __device__ __forceinline__ void store_o(uint32_t taddr, const float (&f)[4], con
         }
 }
 
-// Barrier over the softmax warps; true when any thread votes so.
-__device__ __forceinline__ bool softmax_sync_or(bool v) {
+// Barrier over the softmax warps, kThreads threads; true when any of them votes so.
+template <int kThreads>
+__device__ __forceinline__ bool softmax_or(bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(v))
+        : "r"(static_cast<uint32_t>(v)), "n"(kThreads)
         : "memory");
     return r != 0;
 }

@@ -143,20 +143,6 @@ struct Tokens {
     }
 };
 
-// Barrier over the softmax warps; true when any thread votes so.
-__device__ __forceinline__ bool softmax_or(bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(v)), "n"(kSoftmax)
-        : "memory");
-    return r != 0;
-}
-
 // The MMAs of a third of K (constants all: a descriptor computed at run time costs four times what the MMA does).
 template <int G>
 __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t sQ, uint32_t sK) {
@@ -297,7 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < w; ++j) mx[j] = fmaxf(mx[j], mx[j + w]);
                 ctl->mx[st][2 * half + set][row] = mx[0];
-                ok = !softmax_or(!ok);
+                ok = !softmax_or<kSoftmax>(!ok);
                 over = !ok;
                 if (over) break;  // all eight warps together
                 const float(&all)[4][64] = ctl->mx[st];
@@ -356,7 +342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (p.hi > p.lo) {
                 float(&sums)[4][64] = ctl->mx[t & 1u];
                 sums[2 * half + set][row] = l;
-                ok = !softmax_or(!ok);
+                ok = !softmax_or<kSoftmax>(!ok);
                 if (!ok) break;
                 L = (sums[0][row] + sums[1][row]) + (sums[2][row] + sums[3][row]);
             }
@@ -396,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i >> 4) * (kLatDv * 2))[16 * set + (i & 15)] = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            (void)softmax_or(false);  // the factors are there, the sums read before the next tile's maxima
+            (void)softmax_or<kSoftmax>(false);  // the factors are there, the sums read before the next tile's maxima
             ok = mbar_wait(smem_addr(&ctl->pv_done[1]), (t - 1) & 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
