@@ -669,8 +669,8 @@ int echo_tree_masks(int B, const int64_t* row_off, int64_t n_rows, const int32_t
  * mask [n_rows,words] u32, device.  The rows of a request with more than 32 * words see
  * nothing and set ECHO_ST_BADDATA.  Every cache row of a request's context must be finite,
  * those of nodes that no row sees too: they are read, with weights of zero.  The other
- * arguments, the workspace (echo_mla_chunk_workspace_size) and the errors as
- * echo_mla_chunk; words < 1 or no mask: ECHO_EINVAL, words > ECHO_TREE_MAX_WORDS:
+ * arguments, the workspace (echo_mla_chunk_workspace_size), the roundings (weights of bf16, sums of
+ * fp32) and the errors as echo_mla_chunk; words < 1 or no mask: ECHO_EINVAL, words > ECHO_TREE_MAX_WORDS:
  * ECHO_EUNSUPPORTED.
  */
 int echo_mla_tree(int B, const int64_t* row_off, int64_t n_rows, int heads, const uint16_t* q, const uint32_t* mask,

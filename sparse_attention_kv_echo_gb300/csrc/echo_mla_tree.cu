@@ -16,8 +16,11 @@
 //
 // What bounds it: the MMAs of a tile are 2176 cycles, a tile takes some 2740: copies into shared memory and the operands
 // read from it share its ports.  Tensor pipe 79% active on 16 trees of 12 to 48 nodes over 2048 to 32768 tokens, 128 heads
-// (1.12 ms a launch by itself, 1.60 PFLOP/s; 1.25 among others, under the power cap).  Tiles of 64 tokens took 1.31 ms, 58%.
-// 64 nodes over 131072 tokens: 1.32 ms by itself, 1.52 among others (tiles of 64: 1.82).
+// (1.10 ms a launch by itself, 1.62 PFLOP/s; 1.27 among others, under the power cap).  Tiles of 64 tokens took 1.31 ms, 58%.
+// 64 nodes over 131072 tokens: 1.29 ms by itself, 1.53 among others (tiles of 64: 1.82).
+//
+// The weights enter P V as bf16, as an MMA of bf16 rows takes both its operands: the result, of bf16 too, is 2.0e-3 from 64 bits
+// where weights of fp32 give 1.7e-3.  Scores, the sums of the unrounded weights and O are fp32, O in legs of kLeg tiles.
 #include "echo_chunk.cuh"
 
 namespace echo {

@@ -24,8 +24,8 @@
 // any number of CTAs.  What bounds the call: a few chains or trees, the latency of its steps (one chain of five
 // over 32000 tokens, 8.7 us in a graph: 1.9 to read the tree, 0.5 a walk, 2 a sum with its barrier, 2 the draw); many, the
 // instructions of the sums, some 10 a token and pair of values, and the chain of rejections of the longest walk.  64 chains of
-// six over 131072 tokens in fp32 19 us (60 MB, a third of the memory's rate), 32 trees of 32 to 48 nodes in bf16 30 us, 16
-// greedy trees of 8 to 24 over 50001 tokens 14 us (each in a graph).
+// six over 131072 tokens in fp32 19 us (60 MB, 3.1 TB/s), 32 trees of 32 to 48 nodes in bf16 30 us, 16 greedy trees of 8 to 24
+// over 50001 tokens 14 us (each in a graph on one input).
 #include <cuda_bf16.h>
 
 #include "echo_common.cuh"
